@@ -18,7 +18,13 @@
  *   pkv_copy_blocks    copy-on-write of shared cache blocks;
  *   *_fp8              the store, the decode and the decode step over an fp8
  *                      E4M3 cache;
- *   pkv_mixed_step     a batch of decode requests and prefill chunks.
+ *   pkv_mixed_step     a batch of decode requests and prefill chunks;
+ *   pkv_qk_norm_rope   head norm and position rotation of q and k, with or
+ *                      without the store (pkv_qk_norm_rope_store);
+ *   pkv_plan_slots     block tables, slot map, positions and prefix sums of a
+ *                      round from its request lengths;
+ *   pkv_tree_decode    attention of drafted token trees over the cache
+ *                      (pkv_tree_masks: their masks and positions).
  *
  * Cache layout. One layer's K cache and V cache are two separate arrays of
  * shape [num_blocks, block_size, num_kv_heads, head_dim], row-major, bf16.
@@ -84,6 +90,8 @@ typedef enum { PKV_BF16 = 0 } pkv_dtype;
 #define PKV_DEVERR_BLOCK_ID 0x2u    /* block_tables entry outside [0, num_blocks) */
 #define PKV_DEVERR_LENGTH 0x4u      /* a length beyond its table row or max_* bound, or negative */
 #define PKV_DEVERR_TIMEOUT 0x8u     /* an on-chip wait hit its iteration limit */
+#define PKV_DEVERR_NO_BLOCKS 0x10u  /* the free list ran out, or its cursor lies outside it */
+#define PKV_DEVERR_TREE 0x20u       /* a parent link that is neither -1 nor an earlier node */
 
 /* ----------------------------------------------------------------- store --
  * For t < num_tokens: slot = slot_mapping[t]; slot < 0 marks a padded token
@@ -397,6 +405,159 @@ pkv_status pkv_paged_prefill(void *out, const void *q,
                              int32_t block_size, int32_t num_blocks, float scale,
                              int32_t causal, void *workspace, size_t workspace_bytes,
                              pkv_dtype dtype, void *stream);
+
+/* ------------------------------------------------- head norm and rotation --
+ * pkv_qk_norm_rope: for every token t and every query head row x of q[t] (with
+ * q_weight) and key head row x of k[t] (with k_weight), head_dim values each:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight      (y = x where the weight is NULL)
+ *   pairs (a, b) of y turn by the token's angle row, i < rotary_dim / 2:
+ *     a' = a cos_i - b sin_i,   b' = b cos_i + a sin_i
+ *   pair i is (i, i + rotary_dim / 2), or (2i, 2i + 1) with interleaved != 0;
+ *   values from rotary_dim on are y unchanged.
+ * in fp32, rounded once to bf16.
+ *   q, k              token t's rows start at q + t * q_token_stride (elements),
+ *                     num_q_heads (num_kv_heads) * head_dim contiguous values,
+ *                     so they may be views into a fused QKV tensor.
+ *   q_out, k_out      the results, with token strides of their own. An output
+ *                     may be its own input (same address and stride); any other
+ *                     overlap of inputs and outputs is not allowed.
+ *   q_weight, k_weight [head_dim] bf16 or NULL, each by itself.
+ *   positions         [num_tokens] int32 in [0, max_position).
+ *   cos_sin           [max_position, rotary_dim] float: cos_0 .. cos_{r/2-1},
+ *                     sin_0 .. sin_{r/2-1} of each position.
+ * A token whose position is out of range is skipped and sets
+ * PKV_DEVERR_LENGTH. head_dim 64, 128 or 256; rotary_dim a multiple of 16 in
+ * [16, head_dim]; other shapes return PKV_ERR_SHAPE. Every pointer but
+ * positions is 16-byte aligned, strides are multiples of 8 elements. eps >= 0.
+ * num_tokens == 0 is a no-op.
+ *
+ * pkv_qk_norm_rope_store: the same, but key row t goes to cache slot
+ * slot_mapping[t] and value row t (v, bit for bit) beside it, as
+ * pkv_store_kvcache would write them: a negative slot writes neither (q_out is
+ * written all the same), a slot beyond the cache sets PKV_DEVERR_SLOT. Slots
+ * must be distinct.
+ */
+pkv_status pkv_qk_norm_rope(void *q_out, int64_t q_out_token_stride,
+                            void *k_out, int64_t k_out_token_stride,
+                            const void *q, const void *k,
+                            int64_t q_token_stride, int64_t k_token_stride,
+                            const void *q_weight, const void *k_weight, float eps,
+                            const int32_t *positions, const float *cos_sin,
+                            int32_t max_position, int32_t rotary_dim, int32_t interleaved,
+                            int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                            int32_t head_dim, pkv_dtype dtype, void *stream);
+
+pkv_status pkv_qk_norm_rope_store(void *q_out, int64_t q_out_token_stride,
+                                  const void *q, const void *k, const void *v,
+                                  int64_t q_token_stride, int64_t k_token_stride,
+                                  int64_t v_token_stride,
+                                  const void *q_weight, const void *k_weight, float eps,
+                                  const int32_t *positions, const float *cos_sin,
+                                  int32_t max_position, int32_t rotary_dim, int32_t interleaved,
+                                  void *k_cache, void *v_cache, const int32_t *slot_mapping,
+                                  int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                  pkv_dtype dtype, void *stream);
+
+/* ----------------------------------------------------------- slot planning --
+ * pkv_plan_slots: the index arrays of a round from its request lengths, with no
+ * trip to the host. Request i has context_lens[i] tokens in the cache, whose
+ * ceil(context_lens[i] / block_size) blocks are the first entries of row i of
+ * block_tables, and gets new_lens[i] more. The blocks it lacks are taken from
+ * free_blocks, first to last from entry *free_cursor on and in request order
+ * (the first-in-first-out free list of LLM Infra 101 v0.5), and written behind
+ * the row's entries. Then, with total = sum of new_lens:
+ *   cu_seqlens_q      [num_seqs + 1] prefix sums of new_lens
+ *   cu_seqlens_k      [num_seqs + 1] prefix sums of context_lens + new_lens
+ *   context_lens_out  [num_seqs] context_lens + new_lens
+ *   positions         [max_tokens] row cu_seqlens_q[i] + j: context_lens[i] + j;
+ *                     0 from row total on
+ *   slot_mapping      [max_tokens] the slot of that position; -1 from row total
+ *                     on (a padded token to the store calls)
+ *   free_cursor_out   [1] *free_cursor + blocks taken
+ * These are what pkv_store_kvcache, pkv_paged_decode, pkv_paged_prefill and
+ * pkv_mixed_step take. free_cursor_out must not be free_cursor, nor
+ * context_lens_out one of the two inputs of lengths (PKV_ERR_ARG).
+ * What does not fit is cut and reported: lengths outside [0,
+ * max_blocks_per_seq * block_size] and rows beyond max_tokens shorten new_lens
+ * (PKV_DEVERR_LENGTH); when the free list ends at num_free, table entries and
+ * slots of the missing blocks are -1 (PKV_DEVERR_NO_BLOCKS); an id outside
+ * [0, num_blocks) in the table or the list gives slots of -1
+ * (PKV_DEVERR_BLOCK_ID). num_blocks * block_size and max_blocks_per_seq *
+ * block_size must be below 2^31.
+ */
+pkv_status pkv_plan_slots(const int32_t *context_lens, const int32_t *new_lens, int32_t num_seqs,
+                          int32_t *block_tables, int32_t max_blocks_per_seq,
+                          const int32_t *free_blocks, int32_t num_free,
+                          const int32_t *free_cursor, int32_t *free_cursor_out,
+                          int32_t *slot_mapping, int32_t *positions, int32_t max_tokens,
+                          int32_t *cu_seqlens_q, int32_t *cu_seqlens_k, int32_t *context_lens_out,
+                          int32_t block_size, int32_t num_blocks, void *stream);
+
+/* ----------------------------------------------------------- drafted trees --
+ * A drafted tree of sequence i is rows cu_seqlens_q[i] .. cu_seqlens_q[i+1]-1:
+ * tokens proposed behind its context_lens[i] cached ones, several per position.
+ * Their K and V stay outside the cache until they are accepted; the accepted
+ * rows are then written with pkv_store_kvcache at slots that pkv_plan_slots
+ * gives for the accepted counts, so rejected drafts need neither blocks nor
+ * clean-up.
+ *
+ * pkv_tree_masks: from parents [total_q] (index of the parent in its own tree,
+ * smaller than the node's own; -1: the last cached token)
+ *   tree_mask   [total_q, mask_words] bit u % 32 of word u / 32 of node t's row
+ *               is set when u is t or one of its ancestors; mask_words >=
+ *               ceil(max_seqlen_q / 32), all words of a row are written
+ *   positions   [total_q] context_lens[i] + number of ancestors
+ * A link that is neither -1 nor an earlier node counts as -1 and sets
+ * PKV_DEVERR_TREE; a tree that is longer than max_seqlen_q or ends beyond
+ * total_q is skipped and sets PKV_DEVERR_LENGTH. Rows behind the last tree are
+ * left as they are. max_seqlen_q <= 65535 * 128.
+ *
+ * pkv_tree_decode: for every drafted row t of sequence i and query head g, with
+ * G = num_q_heads / num_kv_heads and h = g / G,
+ *   out[t, g, :] = softmax(scale * q[t, g, :] . K_x[h]) V_x[h]  over
+ *     x = every cached position p < context_lens[i] (through block_tables), and
+ *     x = every drafted row u of the same sequence whose bit is set in row t of
+ *         tree_mask (its K and V are key[u], value[u]).
+ * Any bit pattern is allowed: it need not be a tree, and a row that sees
+ * nothing (no bit set, no cached token) is zero. What a row does not see has no
+ * part in its result, whatever bits it holds.
+ *   out, q          [total_q, num_q_heads, 128] bf16, contiguous; rows behind
+ *                   cu_seqlens_q[num_seqs] are left as they are.
+ *   key, value      the drafted rows, num_kv_heads * 128 contiguous values at
+ *                   token strides of their own (multiples of 8 elements).
+ *   cu_seqlens_q    [num_seqs + 1] int32, non-decreasing from 0; at most
+ *                   max_seqlen_q rows a sequence.
+ *   context_lens    [num_seqs] int32 in [0, max_context_len]; max_context_len
+ *                   <= max_blocks_per_seq * block_size.
+ *   tree_mask       [total_q, mask_words] int32, mask_words >=
+ *                   ceil(max_seqlen_q / 32).
+ *   workspace       pkv_tree_decode_workspace_size(...) bytes, 256-byte aligned;
+ *                   needs no initialisation; two calls in flight at once need
+ *                   two workspaces.
+ * A sequence whose lengths are out of range is skipped and sets
+ * PKV_DEVERR_LENGTH. head_dim 128, up to 16 query heads a KV head, any
+ * block_size >= 1; other shapes return PKV_ERR_SHAPE.
+ */
+pkv_status pkv_tree_masks(const int32_t *parents, const int32_t *cu_seqlens_q,
+                          const int32_t *context_lens, int32_t num_seqs, int32_t total_q,
+                          int32_t max_seqlen_q, int32_t *tree_mask, int32_t mask_words,
+                          int32_t *positions, void *stream);
+
+size_t pkv_tree_decode_workspace_size(int32_t max_seqlen_q, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim);
+
+pkv_status pkv_tree_decode(void *out, const void *q, const void *key, const void *value,
+                           int64_t key_token_stride, int64_t value_token_stride,
+                           const void *k_cache, const void *v_cache,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *context_lens, const int32_t *cu_seqlens_q,
+                           const int32_t *tree_mask, int32_t mask_words,
+                           int32_t num_seqs, int32_t total_q, int32_t max_seqlen_q,
+                           int32_t max_context_len, int32_t num_q_heads, int32_t num_kv_heads,
+                           int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+                           void *workspace, size_t workspace_bytes,
+                           pkv_dtype dtype, void *stream);
 
 /* ------------------------------------------------------------- utilities --
  * pkv_get_device_errors: waits for `stream`, then returns (in *bits) and

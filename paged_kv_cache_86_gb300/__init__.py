@@ -6,14 +6,18 @@ binding plus the seeded synthetic workload generator used by tests and the
 bench. Importing the package does not load the library; the first call does,
 and fails loudly if it has not been built.
 """
-from ._lib import (PkvError, copy_blocks, decode_step, decode_step_fp8, decode_workspace_size,
-                   get_device_errors,
+from ._lib import (PkvError, SlotPlan, copy_blocks, decode_step, decode_step_fp8,
+                   decode_workspace_size, get_device_errors,
                    load, mixed_step, mixed_workspace_size, paged_decode, paged_decode_fp8,
-                   paged_prefill, prefill_workspace_size, selftest_bounded_wait, store_kvcache,
-                   store_kvcache_fp8, version)
+                   paged_prefill, plan_slots, prefill_workspace_size, qk_norm_rope,
+                   qk_norm_rope_store, selftest_bounded_wait, store_kvcache,
+                   store_kvcache_fp8, tree_decode, tree_decode_workspace_size, tree_masks,
+                   version)
 
-__all__ = ["PkvError", "copy_blocks", "decode_step", "decode_step_fp8", "decode_workspace_size",
-           "get_device_errors",
+__all__ = ["PkvError", "SlotPlan", "copy_blocks", "decode_step", "decode_step_fp8",
+           "decode_workspace_size", "get_device_errors",
            "load", "mixed_step", "mixed_workspace_size", "paged_decode", "paged_decode_fp8",
-           "paged_prefill", "prefill_workspace_size", "selftest_bounded_wait", "store_kvcache",
-           "store_kvcache_fp8", "version"]
+           "paged_prefill", "plan_slots", "prefill_workspace_size", "qk_norm_rope",
+           "qk_norm_rope_store", "selftest_bounded_wait", "store_kvcache",
+           "store_kvcache_fp8", "tree_decode", "tree_decode_workspace_size", "tree_masks",
+           "version"]

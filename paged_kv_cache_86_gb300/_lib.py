@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -23,10 +24,13 @@ STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported shape", -3: "unsuppo
           -4: "workspace missing, misaligned or too small", -5: "CUDA runtime error",
           -6: "device-side range check fired"}
 DEVERR_SLOT, DEVERR_BLOCK_ID, DEVERR_LENGTH, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DEVERR_NO_BLOCKS, DEVERR_TREE = 0x10, 0x20
 
 EXPORTED = ("pkv_store_kvcache", "pkv_decode_workspace_size", "pkv_paged_decode",
             "pkv_prefill_workspace_size", "pkv_paged_prefill", "pkv_get_device_errors",
-            "pkv_status_string", "pkv_version")
+            "pkv_status_string", "pkv_version", "pkv_qk_norm_rope", "pkv_qk_norm_rope_store",
+            "pkv_plan_slots", "pkv_tree_masks", "pkv_tree_decode_workspace_size",
+            "pkv_tree_decode")
 
 
 class PkvError(RuntimeError):
@@ -77,6 +81,19 @@ def load(path: str = LIB_PATH):
         lib.pkv_paged_prefill.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, vp, i32, i32, i32,
                                           i32, i32, i32, i32, i32, f32, i32, vp, sz, ctypes.c_int,
                                           vp]
+        lib.pkv_qk_norm_rope.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, vp, vp, f32, vp, vp,
+                                         i32, i32, i32, i32, i32, i32, i32, ctypes.c_int, vp]
+        lib.pkv_qk_norm_rope_store.argtypes = [vp, i64, vp, vp, vp, i64, i64, i64, vp, vp, f32, vp,
+                                               vp, i32, i32, i32, vp, vp, vp, i32, i32, i32, i32,
+                                               i32, i32, ctypes.c_int, vp]
+        lib.pkv_plan_slots.argtypes = [vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp, i32, vp, vp,
+                                       vp, i32, i32, vp]
+        lib.pkv_tree_masks.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, vp, vp]
+        lib.pkv_tree_decode_workspace_size.argtypes = [i32, i32, i32, i32]
+        lib.pkv_tree_decode_workspace_size.restype = sz
+        lib.pkv_tree_decode.argtypes = [vp, vp, vp, vp, i64, i64, vp, vp, vp, i32, vp, vp, vp, i32,
+                                        i32, i32, i32, i32, i32, i32, i32, i32, i32, f32, vp, sz,
+                                        ctypes.c_int, vp]
         lib.pkv_get_device_errors.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
         lib.pkv_selftest_bounded_wait.argtypes = [i32, vp, vp]
         lib.pkv_status_string.argtypes = [ctypes.c_int]
@@ -85,7 +102,8 @@ def load(path: str = LIB_PATH):
         for name in ("pkv_store_kvcache", "pkv_paged_decode", "pkv_decode_step",
                      "pkv_paged_prefill", "pkv_copy_blocks", "pkv_store_kvcache_fp8",
                      "pkv_paged_decode_fp8", "pkv_decode_step_fp8", "pkv_mixed_step",
-                     "pkv_get_device_errors",
+                     "pkv_get_device_errors", "pkv_qk_norm_rope", "pkv_qk_norm_rope_store",
+                     "pkv_plan_slots", "pkv_tree_masks", "pkv_tree_decode",
                      "pkv_selftest_bounded_wait"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
@@ -477,6 +495,298 @@ def paged_prefill(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_tables,
                                  total_q, hq, hkv, d, bs, nb, float(scale), 1 if causal else 0,
                                  ws_ptr, ws_bytes, PKV_BF16, _stream(q, stream)),
            "pkv_paged_prefill")
+    return out
+
+
+# ------------------------------------------------ drafted rounds on the cache
+
+def _dense(dtype, ndim, **tensors):
+    """dtype, rank and dense row-major layout of each named tensor (see _need)."""
+    for name, t in tensors.items():
+        if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != ndim
+                or not t.is_contiguous()):
+            _need(t, name, dtype, ndim, contiguous=True, on_gpu=False)
+
+
+def _rows(**tensors):
+    """bf16 [T, H, D] tensors whose token rows are dense [H, D] blocks at any token stride."""
+    for name, t in tensors.items():
+        _need(t, name, torch.bfloat16, 3, on_gpu=False)
+        _, h, d = t.shape
+        if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+            raise ValueError(f"{name} rows must be contiguous [H, D] blocks")
+
+
+def _token_stride(t: torch.Tensor) -> int:
+    # the stride of a single row is arbitrary and never used
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _one_device(**tensors) -> torch.device:
+    """Every tensor on the GPU, and on the same one; that device."""
+    dev = None
+    for name, t in tensors.items():
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    return dev
+
+
+class _On:
+    """Makes `device` current and, when a stream is named, that stream too, so that the
+    launch and every buffer allocated inside belong to it. Costs nothing to speak of
+    when both already are."""
+
+    def __init__(self, device: torch.device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        self._ctx = None
+        if stream is not None:
+            self._ctx = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self._ctx = torch.cuda.device(device)
+        self._device, self._stream = device, stream
+
+    def __enter__(self) -> int:
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        s = self._stream if self._stream is not None else torch.cuda.current_stream(self._device)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _norm_rope_args(q, k, positions, cos_sin, q_weight, k_weight):
+    """Checks what both head-norm-and-rotation calls share; the tensors for the device check."""
+    _rows(q=q, k=k)
+    _dense(torch.int32, 1, positions=positions)
+    _dense(torch.float32, 2, cos_sin=cos_sin)
+    named = {"q": q, "k": k, "positions": positions, "cos_sin": cos_sin}
+    t, _, d = q.shape
+    if k.shape[0] != t or k.shape[2] != d or positions.shape[0] != t:
+        raise ValueError("shape mismatch between q/k/positions")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _dense(torch.bfloat16, 1, **{name: w})
+            if w.shape[0] != d:
+                raise ValueError(f"{name} must have head_dim entries")
+            named[name] = w
+    return named
+
+
+def _rows_out(out, like, name: str):
+    """The caller's output rows (checked), or None for a new tensor."""
+    if out is not None:
+        _rows(**{name: out})
+        if out.shape != like.shape or out.device != like.device:
+            raise ValueError(f"{name} must be shaped like its input, on the same device")
+    return out
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q [T, Hq, D] and k [T, Hkv, D] (bf16, token rows may be
+    strided; no norm where the weight [D] is None), then the position rotation by
+    cos_sin[positions] (float32 [max_position, rotary_dim]: cosines, then sines).
+    Returns (q_out, k_out); either may be given, and may be its own input."""
+    named = _norm_rope_args(q, k, positions, cos_sin, q_weight, k_weight)
+    _rows_out(q_out, q, "q_out")
+    _rows_out(k_out, k, "k_out")
+    dev = _one_device(**named)
+    lib = load()
+    t, hq, d = q.shape
+    hkv = k.shape[1]
+    with _On(dev, stream) as st:
+        if q_out is None:
+            q_out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=dev)
+        if k_out is None:
+            k_out = torch.empty((t, hkv, d), dtype=torch.bfloat16, device=dev)
+        _check(lib.pkv_qk_norm_rope(
+            q_out.data_ptr(), _token_stride(q_out), k_out.data_ptr(), _token_stride(k_out),
+            q.data_ptr(), k.data_ptr(), _token_stride(q), _token_stride(k), _opt(q_weight),
+            _opt(k_weight), eps, positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0],
+            cos_sin.shape[1], 1 if interleaved else 0, t, hq, hkv, d, PKV_BF16, st),
+            "pkv_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_store(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight=None,
+                       k_weight=None, eps: float = 1e-6, interleaved: bool = False, q_out=None,
+                       stream=None) -> torch.Tensor:
+    """qk_norm_rope whose key rows go, with the value rows v [T, Hkv, D], into the caches
+    [NB, bs, Hkv, D] at slot_mapping [T] (int32; negative = skip). Returns q_out."""
+    named = _norm_rope_args(q, k, positions, cos_sin, q_weight, k_weight)
+    _rows(v=v)
+    _dense(torch.bfloat16, 4, k_cache=k_cache, v_cache=v_cache)
+    _dense(torch.int32, 1, slot_mapping=slot_mapping)
+    t, hq, d = q.shape
+    nb, bs, hkv, dc = k_cache.shape
+    if (v.shape != k.shape or v_cache.shape != k_cache.shape or (hkv, dc) != k.shape[1:]
+            or slot_mapping.shape[0] != t):
+        raise ValueError("shape mismatch between k/v/caches/slot_mapping")
+    _rows_out(q_out, q, "q_out")
+    dev = _one_device(v=v, k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping, **named)
+    lib = load()
+    with _On(dev, stream) as st:
+        if q_out is None:
+            q_out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=dev)
+        _check(lib.pkv_qk_norm_rope_store(
+            q_out.data_ptr(), _token_stride(q_out), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            _token_stride(q), _token_stride(k), _token_stride(v), _opt(q_weight), _opt(k_weight),
+            eps, positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+            1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(),
+            slot_mapping.data_ptr(), t, hq, hkv, d, bs, nb, PKV_BF16, st),
+            "pkv_qk_norm_rope_store")
+    return q_out
+
+
+class SlotPlan(NamedTuple):
+    """What plan_slots computes, all int32 on the GPU."""
+    slot_mapping: torch.Tensor   # [max_tokens]
+    positions: torch.Tensor      # [max_tokens]
+    cu_seqlens_q: torch.Tensor   # [S + 1]
+    cu_seqlens_k: torch.Tensor   # [S + 1]
+    context_lens: torch.Tensor   # [S], the new tokens included
+    free_cursor: torch.Tensor    # [1], behind the blocks taken
+
+
+def plan_slots(context_lens, new_lens, block_tables, free_blocks, free_cursor, block_size: int,
+               num_blocks: int, max_tokens: int, out: SlotPlan | None = None,
+               stream=None) -> SlotPlan:
+    """Slots, positions and prefix sums of a round in which request i adds new_lens[i] tokens
+    to its context_lens[i] cached ones; blocks it lacks are taken from free_blocks [F] at
+    free_cursor [1] and entered in its row of block_tables [S, MB] (updated in place).
+    Rows behind the last new token, up to max_tokens, get slot -1 and position 0.
+    ``out`` may hold the buffers of an earlier plan of the same sizes."""
+    _dense(torch.int32, 1, context_lens=context_lens, new_lens=new_lens, free_blocks=free_blocks,
+           free_cursor=free_cursor)
+    _dense(torch.int32, 2, block_tables=block_tables)
+    s, mb = block_tables.shape
+    if context_lens.shape[0] != s or new_lens.shape[0] != s or free_cursor.shape[0] != 1:
+        raise ValueError("one length and one block table row per request, and one cursor")
+    if max_tokens < 0:
+        raise ValueError("max_tokens must not be negative")
+    named = dict(context_lens=context_lens, new_lens=new_lens, block_tables=block_tables,
+                 free_blocks=free_blocks, free_cursor=free_cursor)
+    sizes = (max_tokens, max_tokens, s + 1, s + 1, s, 1)
+    if out is not None:
+        for name, t, n in zip(SlotPlan._fields, out, sizes):
+            _dense(torch.int32, 1, **{f"out.{name}": t})
+            if t.shape[0] != n:
+                raise ValueError(f"out.{name} must have {n} entries")
+            named[f"out.{name}"] = t
+    dev = _one_device(**named)
+    lib = load()
+    with _On(dev, stream) as st:
+        if out is None:
+            # one buffer, each part on a 16-byte boundary of its own
+            at = [0]
+            for n in sizes:
+                at.append(at[-1] + (n + 3) // 4 * 4)
+            buf = torch.empty(at[-1], dtype=torch.int32, device=dev)
+            out = SlotPlan(*(buf[a:a + n] for a, n in zip(at, sizes)))
+        slots, pos, cu_q, cu_k, lens, cursor = out
+        _check(lib.pkv_plan_slots(
+            context_lens.data_ptr(), new_lens.data_ptr(), s, block_tables.data_ptr(), mb,
+            free_blocks.data_ptr(), free_blocks.shape[0], free_cursor.data_ptr(),
+            cursor.data_ptr(), slots.data_ptr(), pos.data_ptr(), max_tokens, cu_q.data_ptr(),
+            cu_k.data_ptr(), lens.data_ptr(), block_size, num_blocks, st), "pkv_plan_slots")
+    return out
+
+
+def tree_masks(parents, cu_seqlens_q, context_lens, max_seqlen_q: int, tree_mask=None,
+               positions=None, stream=None):
+    """Ancestor masks and positions of drafted trees: parents [total_q] holds each node's
+    parent in its own tree (an earlier node, or -1). Returns (tree_mask [total_q, W] int32
+    with W = ceil(max_seqlen_q / 32) or the given tensor's width, positions [total_q])."""
+    _dense(torch.int32, 1, parents=parents, cu_seqlens_q=cu_seqlens_q, context_lens=context_lens)
+    total, s = parents.shape[0], context_lens.shape[0]
+    if cu_seqlens_q.shape[0] != s + 1:
+        raise ValueError("cu_seqlens_q must have one entry more than context_lens")
+    named = dict(parents=parents, cu_seqlens_q=cu_seqlens_q, context_lens=context_lens)
+    if tree_mask is not None:
+        _dense(torch.int32, 2, tree_mask=tree_mask)
+        if tree_mask.shape[0] != total:
+            raise ValueError("tree_mask must have one row per node")
+        named["tree_mask"] = tree_mask
+    if positions is not None:
+        _dense(torch.int32, 1, positions=positions)
+        if positions.shape[0] != total:
+            raise ValueError("positions must have one entry per node")
+        named["positions"] = positions
+    dev = _one_device(**named)
+    lib = load()
+    with _On(dev, stream) as st:
+        if tree_mask is None:
+            words = max(0, int(max_seqlen_q) + 31) // 32
+            tree_mask = torch.empty((total, words), dtype=torch.int32, device=dev)
+        if positions is None:
+            positions = torch.empty(total, dtype=torch.int32, device=dev)
+        _check(lib.pkv_tree_masks(
+            parents.data_ptr(), cu_seqlens_q.data_ptr(), context_lens.data_ptr(), s, total,
+            int(max_seqlen_q), tree_mask.data_ptr(), tree_mask.shape[1], positions.data_ptr(),
+            st), "pkv_tree_masks")
+    return tree_mask, positions
+
+
+def tree_decode_workspace_size(max_seqlen_q: int, num_q_heads: int, num_kv_heads: int,
+                               head_dim: int = 128) -> int:
+    return int(load().pkv_tree_decode_workspace_size(max_seqlen_q, num_q_heads, num_kv_heads,
+                                                     head_dim))
+
+
+def tree_decode(q, key, value, k_cache, v_cache, block_tables, context_lens, cu_seqlens_q,
+                tree_mask, scale: float, max_seqlen_q: int, max_context_len: int | None = None,
+                out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Attention of drafted rows q [total_q, Hq, 128] over their sequence's context_lens[i]
+    cached tokens and the drafted rows key / value [total_q, Hkv, 128] (token rows may be
+    strided; not written to the cache) whose bit is set in tree_mask [total_q, W].
+    Returns out [total_q, Hq, 128] bf16; rows behind cu_seqlens_q[-1] are not written."""
+    _dense(torch.bfloat16, 3, q=q)
+    _rows(key=key, value=value)
+    _dense(torch.bfloat16, 4, k_cache=k_cache, v_cache=v_cache)
+    _dense(torch.int32, 2, block_tables=block_tables, tree_mask=tree_mask)
+    _dense(torch.int32, 1, context_lens=context_lens, cu_seqlens_q=cu_seqlens_q)
+    total, hq, d = q.shape
+    nb, bs, hkv, dc = k_cache.shape
+    s = context_lens.shape[0]
+    if dc != d or v_cache.shape != k_cache.shape:
+        raise ValueError("q / cache head_dim mismatch")
+    if key.shape != (total, hkv, d) or value.shape != (total, hkv, d):
+        raise ValueError("key / value must be [total_q, Hkv, D]")
+    if (block_tables.shape[0] != s or cu_seqlens_q.shape[0] != s + 1
+            or tree_mask.shape[0] != total):
+        raise ValueError("metadata shape mismatch")
+    dev = _one_device(q=q, key=key, value=value, k_cache=k_cache, v_cache=v_cache,
+                      block_tables=block_tables, context_lens=context_lens,
+                      cu_seqlens_q=cu_seqlens_q, tree_mask=tree_mask)
+    mb = block_tables.shape[1]
+    if max_context_len is None:
+        max_context_len = mb * bs
+    lib = load()
+    with _On(dev, stream) as st:
+        out = _out_like(out, q)
+        if workspace is None:
+            need = lib.pkv_tree_decode_workspace_size(max_seqlen_q, hq, hkv, d)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on q's device")
+        _check(lib.pkv_tree_decode(
+            out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(), _token_stride(key),
+            _token_stride(value), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            mb, context_lens.data_ptr(), cu_seqlens_q.data_ptr(), tree_mask.data_ptr(),
+            tree_mask.shape[1], s, total, int(max_seqlen_q), int(max_context_len), hq, hkv, d, bs,
+            nb, scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            PKV_BF16, st), "pkv_tree_decode")
     return out
 
 

@@ -567,6 +567,274 @@ pkv_status pkv_paged_prefill(void *out, const void *q, const void *k_cache, cons
   return from_cuda(pkv::launch_paged_prefill(a, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+// Checks shared by the two head-norm-and-rotation entries; fills the arguments
+// that both have. The caller adds the key / value destination.
+pkv_status qk_rope_args(pkv::QkRopeArgs *a, void *q_out, int64_t q_out_stride, const void *q,
+                        const void *k, int64_t q_stride, int64_t k_stride, const void *q_weight,
+                        const void *k_weight, float eps, const int32_t *positions,
+                        const float *cos_sin, int32_t max_position, int32_t rotary_dim,
+                        int32_t interleaved, int32_t num_tokens, int32_t num_q_heads,
+                        int32_t num_kv_heads, int32_t head_dim) {
+  const int64_t q_row = int64_t(num_q_heads) * head_dim, k_row = int64_t(num_kv_heads) * head_dim;
+  if (!q_out || !q || !k || !positions || !cos_sin) return PKV_ERR_ARG;
+  if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(cos_sin) ||
+      (q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)))
+    return PKV_ERR_ARG;
+  if (q_stride < q_row || q_out_stride < q_row || k_stride < k_row || q_stride % 8 != 0 ||
+      q_out_stride % 8 != 0 || k_stride % 8 != 0)
+    return PKV_ERR_ARG;
+  if (q_out == q && q_out_stride != q_stride) return PKV_ERR_ARG;  // rows would overlap other rows
+  cudaError_t e;
+  a->err = pkv::device_error_word(&e);
+  if (!a->err) return PKV_ERR_CUDA;
+  a->q_out = static_cast<__nv_bfloat16 *>(q_out);
+  a->q = static_cast<const __nv_bfloat16 *>(q);
+  a->k = static_cast<const __nv_bfloat16 *>(k);
+  a->v = nullptr;
+  a->v_out = nullptr;
+  a->v_stride = 0;
+  a->q_stride = q_stride;
+  a->k_stride = k_stride;
+  a->q_out_stride = q_out_stride;
+  a->q_weight = static_cast<const __nv_bfloat16 *>(q_weight);
+  a->k_weight = static_cast<const __nv_bfloat16 *>(k_weight);
+  a->eps = eps;
+  a->positions = positions;
+  a->cos_sin = cos_sin;
+  a->max_position = max_position;
+  a->rotary_dim = rotary_dim;
+  a->interleaved = interleaved != 0;
+  a->slot_mapping = nullptr;
+  a->num_slots = 0;
+  a->num_tokens = num_tokens;
+  a->num_q_heads = num_q_heads;
+  a->num_kv_heads = num_kv_heads;
+  a->parts = 1;
+  return PKV_OK;
+}
+
+// The part of the same checks that needs no pointer.
+pkv_status qk_rope_shape(float eps, int32_t max_position, int32_t rotary_dim, int32_t num_tokens,
+                         int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                         pkv_dtype dtype) {
+  if (dtype != PKV_BF16) return PKV_ERR_DTYPE;
+  if (num_tokens < 0 || num_q_heads < 1 || num_kv_heads < 1 || max_position < 1 ||
+      !std::isfinite(eps) || eps < 0.f)
+    return PKV_ERR_ARG;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return PKV_ERR_SHAPE;
+  if (rotary_dim < 16 || rotary_dim > head_dim || rotary_dim % 16 != 0) return PKV_ERR_SHAPE;
+  return PKV_OK;
+}
+}  // namespace
+
+pkv_status pkv_qk_norm_rope(void *q_out, int64_t q_out_token_stride, void *k_out,
+                            int64_t k_out_token_stride, const void *q, const void *k,
+                            int64_t q_token_stride, int64_t k_token_stride, const void *q_weight,
+                            const void *k_weight, float eps, const int32_t *positions,
+                            const float *cos_sin, int32_t max_position, int32_t rotary_dim,
+                            int32_t interleaved, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, pkv_dtype dtype,
+                            void *stream) {
+  pkv_status st = qk_rope_shape(eps, max_position, rotary_dim, num_tokens, num_q_heads,
+                                num_kv_heads, head_dim, dtype);
+  if (st != PKV_OK || num_tokens == 0) return st;
+  if (!k_out || !aligned16(k_out) || k_out_token_stride < int64_t(num_kv_heads) * head_dim ||
+      k_out_token_stride % 8 != 0 || (k_out == k && k_out_token_stride != k_token_stride))
+    return PKV_ERR_ARG;
+  pkv::QkRopeArgs a;
+  st = qk_rope_args(&a, q_out, q_out_token_stride, q, k, q_token_stride, k_token_stride, q_weight,
+                    k_weight, eps, positions, cos_sin, max_position, rotary_dim, interleaved,
+                    num_tokens, num_q_heads, num_kv_heads, head_dim);
+  if (st != PKV_OK) return st;
+  a.k_out = static_cast<__nv_bfloat16 *>(k_out);
+  a.k_out_stride = k_out_token_stride;
+  return from_cuda(pkv::launch_qk_rope(a, head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_qk_norm_rope_store(void *q_out, int64_t q_out_token_stride, const void *q,
+                                  const void *k, const void *v, int64_t q_token_stride,
+                                  int64_t k_token_stride, int64_t v_token_stride,
+                                  const void *q_weight, const void *k_weight, float eps,
+                                  const int32_t *positions, const float *cos_sin,
+                                  int32_t max_position, int32_t rotary_dim, int32_t interleaved,
+                                  void *k_cache, void *v_cache, const int32_t *slot_mapping,
+                                  int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                  pkv_dtype dtype, void *stream) {
+  pkv_status st = qk_rope_shape(eps, max_position, rotary_dim, num_tokens, num_q_heads,
+                                num_kv_heads, head_dim, dtype);
+  if (st != PKV_OK) return st;
+  if (block_size < 1 || num_blocks < 1) return PKV_ERR_ARG;
+  if (num_tokens == 0) return PKV_OK;
+  const int64_t row = int64_t(num_kv_heads) * head_dim;
+  if (!v || !k_cache || !v_cache || !slot_mapping || !aligned16(v) || !aligned16(k_cache) ||
+      !aligned16(v_cache) || v_token_stride < row || v_token_stride % 8 != 0)
+    return PKV_ERR_ARG;
+  pkv::QkRopeArgs a;
+  st = qk_rope_args(&a, q_out, q_out_token_stride, q, k, q_token_stride, k_token_stride, q_weight,
+                    k_weight, eps, positions, cos_sin, max_position, rotary_dim, interleaved,
+                    num_tokens, num_q_heads, num_kv_heads, head_dim);
+  if (st != PKV_OK) return st;
+  a.v = static_cast<const __nv_bfloat16 *>(v);
+  a.v_stride = v_token_stride;
+  a.k_out = static_cast<__nv_bfloat16 *>(k_cache);
+  a.v_out = static_cast<__nv_bfloat16 *>(v_cache);
+  a.k_out_stride = row;
+  a.slot_mapping = slot_mapping;
+  a.num_slots = int64_t(num_blocks) * block_size;
+  return from_cuda(pkv::launch_qk_rope(a, head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_plan_slots(const int32_t *context_lens, const int32_t *new_lens, int32_t num_seqs,
+                          int32_t *block_tables, int32_t max_blocks_per_seq,
+                          const int32_t *free_blocks, int32_t num_free,
+                          const int32_t *free_cursor, int32_t *free_cursor_out,
+                          int32_t *slot_mapping, int32_t *positions, int32_t max_tokens,
+                          int32_t *cu_seqlens_q, int32_t *cu_seqlens_k, int32_t *context_lens_out,
+                          int32_t block_size, int32_t num_blocks, void *stream) {
+  if (num_seqs < 0 || max_blocks_per_seq < 0 || num_free < 0 || max_tokens < 0 || block_size < 1 ||
+      num_blocks < 1)
+    return PKV_ERR_ARG;
+  if (int64_t(num_blocks) * block_size > 0x7fffffffll ||           // slots are int32
+      int64_t(max_blocks_per_seq) * block_size > 0x7fffffffll)     // and so are positions
+    return PKV_ERR_ARG;
+  if (!free_cursor || !free_cursor_out || !cu_seqlens_q || !cu_seqlens_k) return PKV_ERR_ARG;
+  if (num_seqs > 0 && (!context_lens || !new_lens || !context_lens_out ||
+                       (!block_tables && max_blocks_per_seq > 0)))
+    return PKV_ERR_ARG;
+  if (max_tokens > 0 && (!slot_mapping || !positions)) return PKV_ERR_ARG;
+  if (num_free > 0 && !free_blocks) return PKV_ERR_ARG;
+  // every CTA reads these inputs while one of them writes the outputs
+  if (free_cursor == free_cursor_out ||
+      (num_seqs > 0 && (context_lens_out == context_lens || context_lens_out == new_lens)))
+    return PKV_ERR_ARG;
+  cudaError_t e;
+  uint32_t *err = pkv::device_error_word(&e);
+  if (!err) return PKV_ERR_CUDA;
+  pkv::PlanSlotsArgs a;
+  a.context_lens = context_lens;
+  a.new_lens = new_lens;
+  a.num_seqs = num_seqs;
+  a.block_tables = block_tables;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.free_blocks = free_blocks;
+  a.num_free = num_free;
+  a.free_cursor = free_cursor;
+  a.cursor_out = free_cursor_out;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.max_tokens = max_tokens;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.cu_seqlens_k = cu_seqlens_k;
+  a.context_out = context_lens_out;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.err = err;
+  return from_cuda(pkv::launch_plan_slots(a, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_tree_masks(const int32_t *parents, const int32_t *cu_seqlens_q,
+                          const int32_t *context_lens, int32_t num_seqs, int32_t total_q,
+                          int32_t max_seqlen_q, int32_t *tree_mask, int32_t mask_words,
+                          int32_t *positions, void *stream) {
+  if (num_seqs < 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_q > 65535 * 128)
+    return PKV_ERR_ARG;
+  if (mask_words < (int64_t(max_seqlen_q) + 31) / 32) return PKV_ERR_ARG;
+  if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
+  if (!parents || !cu_seqlens_q || !context_lens || !tree_mask || !positions) return PKV_ERR_ARG;
+  cudaError_t e;
+  uint32_t *err = pkv::device_error_word(&e);
+  if (!err) return PKV_ERR_CUDA;
+  pkv::TreeMasksArgs a;
+  a.parents = parents;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.context_lens = context_lens;
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  a.max_seqlen_q = max_seqlen_q;
+  a.tree_mask = tree_mask;
+  a.mask_words = mask_words;
+  a.positions = positions;
+  a.err = err;
+  return from_cuda(pkv::launch_tree_masks(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pkv_tree_decode_workspace_size(int32_t max_seqlen_q, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim) {
+  if (max_seqlen_q < 0 || num_q_heads < 1 || num_kv_heads < 1 || head_dim != 128 ||
+      !pkv::tree_decode_supported(num_q_heads, num_kv_heads))
+    return 0;
+  return pkv::tree_decode_workspace_bytes(max_seqlen_q, num_q_heads, num_kv_heads);
+}
+
+pkv_status pkv_tree_decode(void *out, const void *q, const void *key, const void *value,
+                           int64_t key_token_stride, int64_t value_token_stride,
+                           const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                           int32_t max_blocks_per_seq, const int32_t *context_lens,
+                           const int32_t *cu_seqlens_q, const int32_t *tree_mask,
+                           int32_t mask_words, int32_t num_seqs, int32_t total_q,
+                           int32_t max_seqlen_q, int32_t max_context_len, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                           int32_t num_blocks, float scale, void *workspace,
+                           size_t workspace_bytes, pkv_dtype dtype, void *stream) {
+  if (dtype != PKV_BF16) return PKV_ERR_DTYPE;
+  if (num_seqs < 0 || total_q < 0 || max_seqlen_q < 0 || max_context_len < 0 || num_q_heads < 1 ||
+      num_kv_heads < 1 || block_size < 1 || num_blocks < 1 || max_blocks_per_seq < 0 ||
+      !std::isfinite(scale * 1.4426950408889634f))
+    return PKV_ERR_ARG;
+  if (head_dim != 128 || !pkv::tree_decode_supported(num_q_heads, num_kv_heads))
+    return PKV_ERR_SHAPE;
+  if (int64_t(max_context_len) > int64_t(max_blocks_per_seq) * block_size ||
+      int64_t(num_blocks) * block_size > 0x7fffffffll - 128 ||   // cache rows are numbered in int32
+      mask_words < (int64_t(max_seqlen_q) + 31) / 32)
+    return PKV_ERR_ARG;
+  if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
+  if (!out || !q || !key || !value || !k_cache || !v_cache || !context_lens || !cu_seqlens_q ||
+      !tree_mask || (!block_tables && max_blocks_per_seq > 0))
+    return PKV_ERR_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(key) || !aligned16(value) ||
+      !aligned16(k_cache) || !aligned16(v_cache))
+    return PKV_ERR_ARG;
+  const int64_t row = int64_t(num_kv_heads) * head_dim;
+  if (key_token_stride < row || value_token_stride < row || key_token_stride % 8 != 0 ||
+      value_token_stride % 8 != 0)
+    return PKV_ERR_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < pkv::tree_decode_workspace_bytes(max_seqlen_q, num_q_heads, num_kv_heads))
+    return PKV_ERR_WORKSPACE;
+  cudaError_t e;
+  uint32_t *err = pkv::device_error_word(&e);
+  if (!err) return PKV_ERR_CUDA;
+  pkv::TreeDecodeArgs a;
+  a.out = out;
+  a.q = q;
+  a.key = key;
+  a.value = value;
+  a.key_stride = key_token_stride;
+  a.value_stride = value_token_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.context_lens = context_lens;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.tree_mask = tree_mask;
+  a.mask_words = mask_words;
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  a.max_seqlen_q = max_seqlen_q;
+  a.max_context_len = max_context_len;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.scale = scale;
+  a.workspace = workspace;
+  a.err = err;
+  return from_cuda(pkv::launch_tree_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
 pkv_status pkv_get_device_errors(void *stream, uint32_t *bits) {
   cudaError_t e;
   uint32_t *err = pkv::device_error_word(&e);

@@ -2,6 +2,7 @@
 // translation units. Host-side only; argument checking happens in api.cu.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstddef>
 #include <cstdint>
@@ -170,5 +171,104 @@ cudaError_t launch_paged_prefill(const PrefillArgs &a, cudaStream_t stream);
 // two query heads per CTA in ping-pong (prefill_pp.cu): even GQA groups
 bool prefill_pp_supported(int num_q_heads, int num_kv_heads, int block_size);
 cudaError_t launch_prefill_pp(const PrefillArgs &a, cudaStream_t stream);
+
+// ---- head norm and position rotation of q and k (qk_rope.cu)
+// Strides in elements. slot_mapping == nullptr: key rows go to row t of k_out;
+// otherwise to row slot_mapping[t] of k_out / v_out (the caches).
+struct QkRopeArgs {
+  __nv_bfloat16 *q_out;
+  __nv_bfloat16 *k_out;
+  __nv_bfloat16 *v_out;                // nullptr without a value side
+  const __nv_bfloat16 *q;
+  const __nv_bfloat16 *k;
+  const __nv_bfloat16 *v;              // nullptr without a value side
+  int64_t q_stride, k_stride, v_stride;
+  int64_t q_out_stride, k_out_stride;  // v_out rows have k_out's stride
+  const __nv_bfloat16 *q_weight;       // [head_dim], nullptr: no norm
+  const __nv_bfloat16 *k_weight;
+  float eps;
+  const int32_t *positions;
+  const float *cos_sin;                // [max_position, rotary_dim]
+  int32_t max_position;
+  int32_t rotary_dim;
+  bool interleaved;
+  const int32_t *slot_mapping;
+  int64_t num_slots;
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  uint32_t *err;
+  int parts;                           // warps a token's rows are spread over (set by the launcher)
+};
+cudaError_t launch_qk_rope(QkRopeArgs a, int head_dim, cudaStream_t stream);
+
+// ---- slot planning and tree masks (slots.cu)
+struct PlanSlotsArgs {
+  const int32_t *context_lens;
+  const int32_t *new_lens;
+  int32_t num_seqs;
+  int32_t *block_tables;
+  int32_t max_blocks_per_seq;
+  const int32_t *free_blocks;
+  int32_t num_free;
+  const int32_t *free_cursor;
+  int32_t *cursor_out;
+  int32_t *slot_mapping;
+  int32_t *positions;
+  int32_t max_tokens;
+  int32_t *cu_seqlens_q;
+  int32_t *cu_seqlens_k;
+  int32_t *context_out;
+  int32_t block_size;
+  int32_t num_blocks;
+  uint32_t *err;
+};
+cudaError_t launch_plan_slots(const PlanSlotsArgs &a, cudaStream_t stream);
+
+struct TreeMasksArgs {
+  const int32_t *parents;
+  const int32_t *cu_seqlens_q;
+  const int32_t *context_lens;
+  int32_t num_seqs;
+  int32_t total_q;
+  int32_t max_seqlen_q;
+  int32_t *tree_mask;
+  int32_t mask_words;
+  int32_t *positions;
+  uint32_t *err;
+};
+cudaError_t launch_tree_masks(const TreeMasksArgs &a, cudaStream_t stream);
+
+// ---- tree attention over the cache (tree_decode.cu)
+struct TreeDecodeArgs {
+  void *out;
+  const void *q;
+  const void *key;                     // drafted tokens' K and V rows, strides in elements
+  const void *value;
+  int64_t key_stride;
+  int64_t value_stride;
+  const void *k_cache;
+  const void *v_cache;
+  const int32_t *block_tables;
+  int32_t max_blocks_per_seq;
+  const int32_t *context_lens;
+  const int32_t *cu_seqlens_q;
+  const int32_t *tree_mask;
+  int32_t mask_words;
+  int32_t num_seqs;
+  int32_t total_q;
+  int32_t max_seqlen_q;
+  int32_t max_context_len;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t block_size;
+  int32_t num_blocks;
+  float scale;
+  void *workspace;
+  uint32_t *err;
+};
+bool tree_decode_supported(int num_q_heads, int num_kv_heads);
+size_t tree_decode_workspace_bytes(int max_seqlen_q, int num_q_heads, int num_kv_heads);
+cudaError_t launch_tree_decode(const TreeDecodeArgs &a, cudaStream_t stream);
 
 }  // namespace pkv

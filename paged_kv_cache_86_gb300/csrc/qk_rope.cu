@@ -1,0 +1,184 @@
+// qk_rope.cu -- head norm and position rotation of a step's queries and keys,
+// in the pass that also writes the keys and values to their cache slots.
+//
+// For every token t and head row x of D values (query heads with q_weight, key
+// heads with k_weight):
+//   y  = x * rsqrt(mean(x^2) + eps) * w            (skipped when the weight is absent)
+//   y' = y with each pair (a, b) turned by the token's angle row:
+//        a' = a cos_i - b sin_i,  b' = b cos_i + a sin_i,  i < rotary_dim / 2
+// where pair i is (i, i + rotary_dim/2) or, interleaved, (2i, 2i + 1), and dims
+// from rotary_dim on pass through. All of it is fp32 with one rounding to bf16
+// at the end; the value rows of the storing variant move bit for bit.
+//
+// Bound by HBM: each row is read once and written once (the angle row, 4 *
+// rotary_dim bytes a token, is shared by all its heads). A row belongs to D/16
+// neighbouring lanes and each lane holds the two 8-value chunks whose dims turn
+// into one another (chunk l and chunk l + rotary_dim/16), so the turn needs no
+// exchange between lanes, the sum of squares log2(D/16) shuffles, and every
+// access is 16 bytes. A warp stays with one token, so the angles are loaded
+// once and serve all the rows it handles.
+#include <cuda_runtime.h>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kWarps = 4;
+
+struct Chunk {
+  float v[8];
+};
+
+__device__ __forceinline__ Chunk unpack(uint4 r) {
+  Chunk c;
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = bf16x2_to_float2(w[i]);
+    c.v[2 * i] = f.x;
+    c.v[2 * i + 1] = f.y;
+  }
+  return c;
+}
+
+__device__ __forceinline__ uint4 pack(const Chunk &c) {
+  return make_uint4(float2_to_bf16x2(c.v[0], c.v[1]), float2_to_bf16x2(c.v[2], c.v[3]),
+                    float2_to_bf16x2(c.v[4], c.v[5]), float2_to_bf16x2(c.v[6], c.v[7]));
+}
+
+// kD: head_dim. kInter: interleaved pairs.
+template <int kD, bool kInter>
+__global__ void __launch_bounds__(kWarps * 32) qk_rope_kernel(const QkRopeArgs a) {
+  constexpr int kLanes = kD / 16;          // lanes of a row
+  constexpr int kRows = 32 / kLanes;       // rows a warp handles at once
+  const int lane = threadIdx.x & 31;
+  const int64_t gw = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t t = gw / a.parts;          // token
+  const int part = static_cast<int>(gw - t * a.parts);
+  if (t >= a.num_tokens) return;
+  const int pos = __ldg(a.positions + t);
+  if (pos < 0 || pos >= a.max_position) {
+    if (lane == 0) raise_error(a.err, PKV_DEVERR_LENGTH);
+    return;
+  }
+  int64_t slot = t;                        // row of the key (and value) output
+  if (a.slot_mapping != nullptr) {
+    slot = __ldg(a.slot_mapping + t);
+    if (slot >= a.num_slots) {
+      if (lane == 0) raise_error(a.err, PKV_DEVERR_SLOT);
+      slot = -1;
+    }
+  }
+  const int l = lane % kLanes, sub = lane / kLanes;
+  const int turn = a.rotary_dim / 16;      // lanes whose two chunks turn
+  // the lane's two chunks of 8 values, in elements of the row
+  const int c0 = (l < turn ? l : 2 * l) * 8;
+  const int c1 = l < turn ? c0 + turn * 8 : c0 + 8;
+  float cs[8], sn[8];
+  if (l < turn) {
+    const float *row = a.cos_sin + static_cast<int64_t>(pos) * a.rotary_dim;
+    const int half = a.rotary_dim / 2;
+    // neox: pair i is (c0 + i, c1 + i); interleaved: pairs c0/2 + 0..3 and c1/2 + 0..3
+    const int p0 = kInter ? c0 / 2 : c0, p1 = kInter ? c1 / 2 : c0 + 4;
+    *reinterpret_cast<float4 *>(cs) = __ldg(reinterpret_cast<const float4 *>(row + p0));
+    *reinterpret_cast<float4 *>(cs + 4) = __ldg(reinterpret_cast<const float4 *>(row + p1));
+    *reinterpret_cast<float4 *>(sn) = __ldg(reinterpret_cast<const float4 *>(row + half + p0));
+    *reinterpret_cast<float4 *>(sn + 4) = __ldg(reinterpret_cast<const float4 *>(row + half + p1));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cs[i] = 1.f;
+      sn[i] = 0.f;
+    }
+  }
+  const int heads = a.num_q_heads + a.num_kv_heads;
+  const int rows = heads + (a.v != nullptr ? a.num_kv_heads : 0);
+  for (int r0 = part * kRows; r0 < rows; r0 += a.parts * kRows) {
+    const int r = r0 + sub;
+    const __nv_bfloat16 *src = nullptr, *w = nullptr;
+    __nv_bfloat16 *dst = nullptr;
+    if (r < a.num_q_heads) {
+      src = a.q + t * a.q_stride + r * kD;
+      dst = a.q_out + t * a.q_out_stride + r * kD;
+      w = a.q_weight;
+    } else if (r < heads) {
+      const int h = r - a.num_q_heads;
+      src = a.k + t * a.k_stride + h * kD;
+      if (slot >= 0) dst = a.k_out + slot * a.k_out_stride + h * kD;
+      w = a.k_weight;
+    } else if (r < rows) {
+      const int h = r - heads;
+      src = a.v + t * a.v_stride + h * kD;
+      if (slot >= 0) dst = a.v_out + slot * a.k_out_stride + h * kD;
+    }
+    uint4 x0 = make_uint4(0u, 0u, 0u, 0u), x1 = x0;
+    if (dst != nullptr) {
+      x0 = *reinterpret_cast<const uint4 *>(src + c0);
+      x1 = *reinterpret_cast<const uint4 *>(src + c1);
+    }
+    Chunk u = unpack(x0), z = unpack(x1);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += u.v[i] * u.v[i] + z.v[i] * z.v[i];
+#pragma unroll
+    for (int off = kLanes / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    if (dst == nullptr) continue;
+    if (w != nullptr) {
+      const float inv = rsqrtf(ss * (1.f / kD) + a.eps);
+      const Chunk w0 = unpack(__ldg(reinterpret_cast<const uint4 *>(w + c0)));
+      const Chunk w1 = unpack(__ldg(reinterpret_cast<const uint4 *>(w + c1)));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        u.v[i] *= inv * w0.v[i];
+        z.v[i] *= inv * w1.v[i];
+      }
+    }
+    if (r < heads && l < turn) {
+      if constexpr (kInter) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a0 = u.v[2 * i], b0 = u.v[2 * i + 1], a1 = z.v[2 * i], b1 = z.v[2 * i + 1];
+          u.v[2 * i] = a0 * cs[i] - b0 * sn[i];
+          u.v[2 * i + 1] = b0 * cs[i] + a0 * sn[i];
+          z.v[2 * i] = a1 * cs[4 + i] - b1 * sn[4 + i];
+          z.v[2 * i + 1] = b1 * cs[4 + i] + a1 * sn[4 + i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p = u.v[i], s = z.v[i];
+          u.v[i] = p * cs[i] - s * sn[i];
+          z.v[i] = s * cs[i] + p * sn[i];
+        }
+      }
+    }
+    const bool as_is = r >= heads || (w == nullptr && l >= turn);
+    *reinterpret_cast<uint4 *>(dst + c0) = as_is ? x0 : pack(u);
+    *reinterpret_cast<uint4 *>(dst + c1) = as_is ? x1 : pack(z);
+  }
+}
+
+template <int kD>
+void launch(const QkRopeArgs &a, unsigned grid, cudaStream_t stream) {
+  if (a.interleaved)
+    qk_rope_kernel<kD, true><<<grid, kWarps * 32, 0, stream>>>(a);
+  else
+    qk_rope_kernel<kD, false><<<grid, kWarps * 32, 0, stream>>>(a);
+}
+
+}  // namespace
+
+cudaError_t launch_qk_rope(QkRopeArgs a, int head_dim, cudaStream_t stream) {
+  if (a.num_tokens == 0) return cudaSuccess;
+  a.parts = 1;
+  const int64_t warps = static_cast<int64_t>(a.num_tokens) * a.parts;
+  const unsigned grid = static_cast<unsigned>((warps + kWarps - 1) / kWarps);
+  if (head_dim == 64) launch<64>(a, grid, stream);
+  else if (head_dim == 128) launch<128>(a, grid, stream);
+  else launch<256>(a, grid, stream);
+  return cudaGetLastError();
+}
+
+}  // namespace pkv
