@@ -537,7 +537,13 @@ pkv_status pkv_plan_slots(const int32_t *context_lens, const int32_t *new_lens, 
  *                   two workspaces.
  * A sequence whose lengths are out of range is skipped and sets
  * PKV_DEVERR_LENGTH. head_dim 128, up to 16 query heads a KV head, any
- * block_size >= 1; other shapes return PKV_ERR_SHAPE.
+ * block_size >= 1; other shapes return PKV_ERR_SHAPE. num_seqs * num_kv_heads *
+ * (max_context_len / 128 + max_seqlen_q / 128 + 2) * (row groups of a tree: 256
+ * rows of max_seqlen_q * G) must stay below 2^30, and the cache below 2^31 rows
+ * (PKV_ERR_ARG).
+ * Work is split into equal ranges of 128-key tiles over the GPU's SMs; a
+ * sequence that spans several ranges is finished by a log-sum-exp combine pass
+ * (a second launch). Results do not depend on the workspace's contents.
  */
 pkv_status pkv_tree_masks(const int32_t *parents, const int32_t *cu_seqlens_q,
                           const int32_t *context_lens, int32_t num_seqs, int32_t total_q,

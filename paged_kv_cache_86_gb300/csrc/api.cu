@@ -787,7 +787,8 @@ pkv_status pkv_tree_decode(void *out, const void *q, const void *key, const void
     return PKV_ERR_SHAPE;
   if (int64_t(max_context_len) > int64_t(max_blocks_per_seq) * block_size ||
       int64_t(num_blocks) * block_size > 0x7fffffffll - 128 ||   // cache rows are numbered in int32
-      mask_words < (int64_t(max_seqlen_q) + 31) / 32)
+      mask_words < (int64_t(max_seqlen_q) + 31) / 32 ||
+      !pkv::tree_decode_fits(num_seqs, max_seqlen_q, max_context_len, num_q_heads, num_kv_heads))
     return PKV_ERR_ARG;
   if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
   if (!out || !q || !key || !value || !k_cache || !v_cache || !context_lens || !cu_seqlens_q ||
@@ -800,9 +801,11 @@ pkv_status pkv_tree_decode(void *out, const void *q, const void *key, const void
   if (key_token_stride < row || value_token_stride < row || key_token_stride % 8 != 0 ||
       value_token_stride % 8 != 0)
     return PKV_ERR_ARG;
+  const size_t need = pkv::tree_decode_workspace_bytes(max_seqlen_q, num_q_heads, num_kv_heads);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      workspace_bytes < pkv::tree_decode_workspace_bytes(max_seqlen_q, num_q_heads, num_kv_heads))
+      workspace_bytes < need || workspace_bytes < 256)
     return PKV_ERR_WORKSPACE;
+  if (need == 0) return PKV_ERR_CUDA;
   cudaError_t e;
   uint32_t *err = pkv::device_error_word(&e);
   if (!err) return PKV_ERR_CUDA;

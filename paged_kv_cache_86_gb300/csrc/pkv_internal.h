@@ -268,6 +268,10 @@ struct TreeDecodeArgs {
   uint32_t *err;
 };
 bool tree_decode_supported(int num_q_heads, int num_kv_heads);
+// The key tiles of a call are numbered in 32 bits: whether the bounds allow it.
+bool tree_decode_fits(int num_seqs, int max_seqlen_q, int max_context_len, int num_q_heads,
+                      int num_kv_heads);
+// 0 without a device.
 size_t tree_decode_workspace_bytes(int max_seqlen_q, int num_q_heads, int num_kv_heads);
 cudaError_t launch_tree_decode(const TreeDecodeArgs &a, cudaStream_t stream);
 
