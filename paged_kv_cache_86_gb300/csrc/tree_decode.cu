@@ -23,21 +23,21 @@
 // cuts leaves partial records (O, m, l) that tree_combine_kernel merges by the
 // log-sum-exp rule.
 //
-// A CTA runs its tiles through two softmax warpgroups, x = 0 and 1, that
-// alternate: an "op" is one key tile met by one MMA row tile, op g belongs to
-// x = g & 1, and the tensor core issues PV(g - 2), S(g) for g = 0, 1, 2, ...
-// across streams, so while one warpgroup computes its softmax the tensor core
-// and the other one work.
+// Two softmax warpgroups x = 0, 1, each with a score region (TMEM columns 128 x
+// ..), an output accumulator O_x (256 + 128 x ..), a maximum and a sum a row. A
+// step g is one 128-row MMA tile meeting one key tile; it belongs to x = g & 1,
+// and the tensor core gets PV(g - 2), S(g) for g = 0, 1, 2, ... across streams:
+// while one warpgroup computes its softmax the tensor core and the other work.
 //   * streams of one row tile (T_i * G <= 128): consecutive key tiles alternate
-//     between the warpgroups, each with its own O, maximum and sum; at the end
-//     the one with the last tile merges both, reading the other's O from TMEM.
-//   * streams of two row tiles: every key tile is met by both; K and V are
-//     loaded once.
-// Accumulators S_0, S_1, O_0, O_1 fill the 512 TMEM columns; P is written as
-// bf16 over S and is the A operand of the PV MMA from there. P is exp2 of fp32
-// scores and enters the fp32 row sum before it is rounded; the one rounding of
-// the weights to bf16 (2^-8 of each at most) is what the tensor core's operand
-// type asks for. O is rescaled only when a row's maximum grows by over 2^8.
+//     between the warpgroups; at the end the one with the last tile merges both,
+//     reading the other's O from TMEM.
+//   * streams of two row tiles: x takes row tile x, and each key tile makes two
+//     steps; K and V are loaded once.
+// P is written as bf16 over S and is the A operand of the PV MMA from there. P is
+// exp2 of fp32 scores and enters the fp32 row sum before it is rounded; the one
+// rounding of the weights to bf16 (2^-8 of each at most) is what the tensor
+// core's operand type asks for. O is rescaled only when a row's maximum grows by
+// over 2^8.
 //
 // Loads (warps 8 and 10): whole tiles of blocks that are a multiple of 8 rows
 // by TMA boxes; partial tiles, other block sizes and the drafts by TMA row
@@ -65,32 +65,29 @@ constexpr int kTile = 128;
 constexpr int kHD = 128;
 constexpr int kRegion = 16384;       // 128 rows x 64 dims, 128-byte swizzle
 constexpr int kTileBytes = 2 * kRegion;
-constexpr int kKStages = 3;
-constexpr int kVStages = 2;
+// a V tile waits for its weights, a K tile for nothing
+constexpr int kKStages = 2;
+constexpr int kVStages = 3;
 constexpr int kThreads = 384;        // softmax 0 (warps 0-3), softmax 1 (4-7), loaders + MMA (8-11)
 constexpr int kWarpK = 8, kWarpMma = 9, kWarpV = 10;
-// Registers: launched at 168 a thread; warpgroup 2 drops to 104 and the softmax
-// warpgroups rise to 200, which adds up to the launch total again.
-constexpr int kRegsLaunch = 168, kRegsLow = 104, kRegsHigh = 200;
-static_assert(2 * 128 * kRegsHigh + 128 * kRegsLow == kThreads * kRegsLaunch,
-              "setmaxnreg split must add up to the launch allocation");
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.f;
 constexpr int kSegRing = 4;
 constexpr int kSegReaders = 1 + 1 + 8;   // V loader, MMA issuer, softmax warps
 
-constexpr int kOffQ = 0;                                // two Q tiles
-constexpr int kOffK = kOffQ + 2 * kTileBytes;
-constexpr int kOffV = kOffK + kKStages * kTileBytes;
-constexpr int kOffMl = kOffV + kVStages * kTileBytes;   // float2[128]
+constexpr int kOffMl = 0;                               // float2[128]
 constexpr int kOffSeg = kOffMl + kTile * 8;
 constexpr int kSegBytes = 64;
 constexpr int kOffBar = kOffSeg + kSegRing * kSegBytes;
-// q full/empty x2, k and v full/empty, s/p/pv/o_free x2, ml full/free, seg full/empty
-constexpr int kNumBars = 4 + 2 * kKStages + 2 * kVStages + 8 + 2 + 2 * kSegRing;
+// q full/empty x2, k and v full/empty, s_full, p_full, o_free, pv_done, wg_end x2, ml
+// full/free, drained, seg full/empty
+constexpr int kNumBars = 4 + 2 * kKStages + 2 * kVStages + 10 + 3 + 2 * kSegRing;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;        // TMEM address, abort flag, start
-constexpr int kSmemBytes = kOffMisc + 32 + 1024;        // the base is rounded up to 1024 bytes
+constexpr int kOffQ = (kOffMisc + 32 + 1023) / 1024 * 1024;   // two Q tiles
+constexpr int kOffK = kOffQ + 2 * kTileBytes;
+constexpr int kOffV = kOffK + kKStages * kTileBytes;
+constexpr int kSmemBytes = kOffV + kVStages * kTileBytes;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 // One CTA's part of one stream, handed from the K loader to the other roles.
@@ -104,7 +101,7 @@ struct Seg {
   int ntok;     // its tokens
   int t0, t1;   // tiles of the stream
   int slot;     // partial record, -1: the whole stream is here
-  int op0;      // first op
+  int step0;    // its first step
   int qtile;    // running number of its first Q tile
   int bad;      // set when a drafted V value was not finite
 };
@@ -217,18 +214,45 @@ __device__ __forceinline__ void umma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tme
       :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32_u(uint32_t taddr, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_st16_u(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
       :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
          "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
-         "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
-         "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+         "r"(v[14]), "r"(v[15])
       : "memory");
 }
+
+// Maximum of 32 values, four chains of three-operand maxima (NaN is ignored).
+__device__ __forceinline__ float max32(const float (&v)[32]) {
+  float a[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = fmaxf(v[i], v[i + 4]);
+#pragma unroll
+  for (int e = 8; e < 32; e += 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = fmax3(a[i], v[e + i], v[e + 4 + i]);
+  }
+  return fmaxf(fmax3(a[0], a[1], a[2]), a[3]);
+}
+
+// One lane of a converged warp. Operands of TMA copies and MMAs live in uniform
+// registers: inside `if (elect_one())`, in warp-uniform control flow, the compiler
+// keeps them there, and an MMA costs 4 instructions; under `lane == 0` it costs 10
+// and a copy with operands that differ by lane a loop over the lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// A value all lanes hold, uniform to the compiler.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Four rows r of a [rows, row_elems] array, 64 elements from column x on, to
 // 4 x 128 bytes of shared memory (rows outside the array read as zero).
@@ -242,8 +266,34 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
+// Wait for the phase with the given parity: suspended in hardware for up to
+// kSuspendNs at a time (it measured up to 4 us), because a dozen warps that poll
+// take shared-memory cycles from the MMAs' operands. Gives up when *abort becomes non-zero or after
+// kMaxPolls polls.
+constexpr uint32_t kSuspendNs = 1000000u;
+constexpr uint32_t kMaxPolls = 1u << 19;
+
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, const volatile int *abort) {
+#pragma unroll 1
+  for (uint32_t n = 0; n < kMaxPolls; ++n) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity), "r"(kSuspendNs) : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+  }
+  return false;
+}
+
+__device__ __forceinline__ void mbar_arrive_count(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(n) : "memory");
+}
+
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int *abort) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+  return __all_sync(0xffffffffu, poll(bar, parity, abort));
 }
 
 // Lengths of sequence i, checked: drafts == 0 when there is nothing to do.
@@ -267,9 +317,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                    const __grid_constant__ CUtensorMap tm_vg, const __grid_constant__ CUtensorMap tm_kd,
                    const __grid_constant__ CUtensorMap tm_vd, const TreeParams p) {
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_addr = smem_addr(smem_raw);
-  const uint32_t base = (raw_addr + 1023u) & ~1023u;
-  uint8_t *smem = smem_raw + (base - raw_addr);
+  uint8_t *smem = smem_raw;
+  const uint32_t base = smem_addr(smem_raw);
+  if ((base & 1023u) != 0) {   // the swizzled tiles need it, and nothing is left to round up
+    if (threadIdx.x == 0) p.bounds[blockIdx.x].row0 = -1;
+    raise_error(p.err, PKV_DEVERR_TIMEOUT);
+    return;
+  }
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   // let the combine be scheduled early (it waits for this grid's end)
@@ -286,15 +340,18 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   constexpr int kBx = kBv + 2 * kVStages;
   auto s_full = [&](int x) { return bar0 + 8u * (kBx + x); };
   auto p_full = [&](int x) { return bar0 + 8u * (kBx + 2 + x); };
-  auto pv_done = [&](int x) { return bar0 + 8u * (kBx + 4 + x); };
-  auto o_free = [&](int x) { return bar0 + 8u * (kBx + 6 + x); };
-  const uint32_t ml_full = bar0 + 8u * (kBx + 8), ml_free = bar0 + 8u * (kBx + 9);
-  auto seg_full = [&](int i) { return bar0 + 8u * (kBx + 10 + i); };
-  auto seg_empty = [&](int i) { return bar0 + 8u * (kBx + 10 + kSegRing + i); };
+  auto o_free = [&](int x) { return bar0 + 8u * (kBx + 4 + x); };
+  auto pv_done = [&](int x) { return bar0 + 8u * (kBx + 6 + x); };
+  auto wg_end = [&](int x) { return bar0 + 8u * (kBx + 8 + x); };
+  const uint32_t ml_full = bar0 + 8u * (kBx + 10), ml_free = bar0 + 8u * (kBx + 11);
+  const uint32_t drained = bar0 + 8u * (kBx + 12);
+  auto seg_full = [&](int i) { return bar0 + 8u * (kBx + 13 + i); };
+  auto seg_empty = [&](int i) { return bar0 + 8u * (kBx + 13 + kSegRing + i); };
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
-  volatile int *start = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);  // seq, tile, range, total
-  float2 *ml_x = reinterpret_cast<float2 *>(smem + kOffMl);
+  volatile int *start = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);  // first sequence, tile
+  const volatile int *never = reinterpret_cast<volatile int *>(smem + kOffMisc + 16);  // stays 0
+  float2 *ml = reinterpret_cast<float2 *>(smem + kOffMl);
   auto seg_at = [&](int i) {
     return reinterpret_cast<volatile Seg *>(smem + kOffSeg + (i % kSegRing) * kSegBytes);
   };
@@ -305,8 +362,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       mbar_init(q_empty(s), 1);
       mbar_init(s_full(s), 1);
       mbar_init(p_full(s), 4);
-      mbar_init(pv_done(s), 1);
       mbar_init(o_free(s), 4);
+      mbar_init(pv_done(s), 1);
+      mbar_init(wg_end(s), 4);
     }
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(k_full(s), 1);
@@ -318,11 +376,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
     mbar_init(ml_full, 4);
     mbar_init(ml_free, 4);
+    mbar_init(drained, 1);
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(seg_full(i), 1);
       mbar_init(seg_empty(i), kSegReaders);
     }
     *abort_flag = 0;
+    *reinterpret_cast<volatile int *>(smem + kOffMisc + 16) = 0;
     fence_barrier_init();
   }
   if (warp == kWarpMma) {
@@ -360,11 +420,19 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (w < warp) before += v;
     total += v;
   }
+  // range b is [floor(b * units / ctas), floor((b + 1) * units / ctas)), so that
+  // with num_kv_heads | ctas every head is cut at the same tiles; no range is empty
   const int units = total * p.num_kv_heads;
-  const int range = max(1, (units + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
-  const long long lo64 = static_cast<long long>(blockIdx.x) * range;
-  const int lo = lo64 < units ? static_cast<int>(lo64) : units;
-  const int hi = static_cast<int>(min(lo64 + range, static_cast<long long>(units)));
+  const int ctas = min(static_cast<int>(gridDim.x), max(units, 1));
+  const int bid = static_cast<int>(blockIdx.x);
+  auto range_lo = [&](int b) {
+    return static_cast<int>(static_cast<long long>(min(b, ctas)) * units / ctas);
+  };
+  // the range that tile f lies in
+  auto range_of = [&](int f) {
+    return static_cast<int>(((static_cast<long long>(f) + 1) * ctas - 1) / units);
+  };
+  const int lo = range_lo(bid), hi = range_lo(bid + 1);
   const int off0 = lo < hi ? lo % total : -1;   // the range starts at this tile of its head
   {
     int at = before + inc - mine;               // this thread's first tile
@@ -381,44 +449,43 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
-  auto tmem_s = [&](int x) { return tmem + x * kTile; };           // P over columns 0..63
+  auto tmem_s = [&](int x) { return tmem + x * kTile; };
   auto tmem_o = [&](int x) { return tmem + (2 + x) * kTile; };
   const uint32_t sQ = base + kOffQ;
   auto sK = [&](int s) { return base + kOffK + s * kTileBytes; };
   auto sV = [&](int s) { return base + kOffV + s * kTileBytes; };
-  auto fail = [&]() {
-    *abort_flag = 1;
-    raise_error(p.err, PKV_DEVERR_TIMEOUT);
+  auto fail = [&]() {   // a whole warp
+    if (lane == 0) {
+      *abort_flag = 1;
+      raise_error(p.err, PKV_DEVERR_TIMEOUT);
+    }
+    __syncwarp();
   };
-  // Segment n for a reader: copied out of the ring; false on a timeout. The ring
-  // entry is given back by seg_done().
-  auto read_seg = [&](int n, Seg &s, bool whole_warp) -> bool {
-    const uint32_t par = (n / kSegRing) & 1;
-    const bool got = whole_warp ? warp_wait(seg_full(n % kSegRing), par, abort_flag)
-                                : mbar_wait(seg_full(n % kSegRing), par, abort_flag);
-    if (!got) return false;
+  // Segment n for a reader (a whole warp): copied out of the ring; false on a
+  // timeout. seg_done() gives the ring entry back.
+  auto read_seg = [&](int n, Seg &s) -> bool {
+    if (!warp_wait(seg_full(n % kSegRing), (n / kSegRing) & 1, abort_flag)) return false;
     const volatile Seg *v = seg_at(n);
-    s.head = v->head;
-    s.ctx = v->ctx;
-    s.drafts = v->drafts;
-    s.q0 = v->q0;
-    s.seq = v->seq;
-    s.tok0 = v->tok0;
-    s.ntok = v->ntok;
-    s.t0 = v->t0;
-    s.t1 = v->t1;
-    s.slot = v->slot;
-    s.op0 = v->op0;
-    s.qtile = v->qtile;
+    s.head = uniform(v->head);
+    s.ctx = uniform(v->ctx);
+    s.drafts = uniform(v->drafts);
+    s.q0 = uniform(v->q0);
+    s.seq = uniform(v->seq);
+    s.tok0 = uniform(v->tok0);
+    s.ntok = uniform(v->ntok);
+    s.t0 = uniform(v->t0);
+    s.t1 = uniform(v->t1);
+    s.slot = uniform(v->slot);
+    s.step0 = uniform(v->step0);
+    s.qtile = uniform(v->qtile);
     return true;
   };
-  auto seg_done = [&](int n, bool whole_warp) {
-    if (whole_warp) __syncwarp();
-    if (!whole_warp || lane == 0) mbar_arrive(seg_empty(n % kSegRing));
+  auto seg_done = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(seg_empty(n % kSegRing));
   };
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsLow));
     if (warp == kWarpK || warp == kWarpV) {
       // ------------------------------------------------------------- loaders
       const bool is_k = warp == kWarpK;
@@ -445,52 +512,60 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           if (is_k) raise_error(p.err, PKV_DEVERR_BLOCK_ID);
           return oob_row;
         };
-        const bool boxes = p.box_rows > 0 && tk.cached == kTile;
-        const int pieces = boxes ? kTile / p.box_rows : tk.rows / 4;
-        int4 r = make_int4(oob_row, oob_row, oob_row, oob_row);
-        bool draft = false;
-        if (lane < pieces) {
-          if (boxes) {
-            r.x = cache_row(j * kTile + lane * p.box_rows);
-          } else {
-            const int k0 = 4 * lane;
-            draft = tk.drafts > 0 && k0 >= tk.at;
-            if (draft) {
-              const int u = k0 - tk.at, first = sg.q0 + tk.u0;
-              r.x = u < tk.drafts ? first + u : p.total_q;
-              r.y = u + 1 < tk.drafts ? first + u + 1 : p.total_q;
-              r.z = u + 2 < tk.drafts ? first + u + 2 : p.total_q;
-              r.w = u + 3 < tk.drafts ? first + u + 3 : p.total_q;
-            } else {
-              const int key = j * kTile + k0;
-              if (k0 < tk.cached) r.x = cache_row(key);
-              if (k0 + 1 < tk.cached) r.y = cache_row(key + 1);
-              if (k0 + 2 < tk.cached) r.z = cache_row(key + 2);
-              if (k0 + 3 < tk.cached) r.w = cache_row(key + 3);
-            }
-          }
-        }
         const int s = issued % stages, round = issued / stages;
         const uint32_t full = is_k ? k_full(s) : v_full(s);
-        int good = 1;
-        if (lane == 0) {
-          if (round > 0 && !mbar_wait(is_k ? k_empty(s) : v_empty(s), (round - 1) & 1, abort_flag)) {
-            good = 0;
-            fail();
+        uint32_t dst = is_k ? sK(s) : sV(s);
+        int4 r = make_int4(oob_row, oob_row, oob_row, oob_row);
+        const bool boxes = p.box_rows > 0 && tk.cached == kTile;
+        if (boxes) {
+          // lane l holds the row of piece l
+          if (lane < kTile / p.box_rows) r.x = cache_row(j * kTile + lane * p.box_rows);
+        } else {
+          // lane l holds the four rows from row 4 l of the tile on
+          const int k0 = 4 * lane;
+          if (tk.drafts > 0 && k0 >= tk.at) {
+            const int u = k0 - tk.at, first = sg.q0 + tk.u0;
+            r.x = u < tk.drafts ? first + u : p.total_q;
+            r.y = u + 1 < tk.drafts ? first + u + 1 : p.total_q;
+            r.z = u + 2 < tk.drafts ? first + u + 2 : p.total_q;
+            r.w = u + 3 < tk.drafts ? first + u + 3 : p.total_q;
           } else {
-            mbar_arrive_expect_tx(full, tk.rows * kHD * 2);
+            const int key = j * kTile + k0;
+            if (k0 < tk.cached) r.x = cache_row(key);
+            if (k0 + 1 < tk.cached) r.y = cache_row(key + 1);
+            if (k0 + 2 < tk.cached) r.z = cache_row(key + 2);
+            if (k0 + 3 < tk.cached) r.w = cache_row(key + 3);
           }
         }
-        if (!__shfl_sync(0xffffffffu, good, 0)) return false;
-        const uint32_t dst = is_k ? sK(s) : sV(s);
-        if (lane < pieces) {
-          if (boxes) {
-            tma_load_3d(dst + lane * p.box_rows * 128, map_box, 0, sg.head, r.x, full);
-            tma_load_3d(dst + kRegion + lane * p.box_rows * 128, map_box, 64, sg.head, r.x, full);
-          } else {
-            const CUtensorMap *map = draft ? map_draft : map_rows;
-            tma_gather4(dst + lane * 512, map, sg.head * kHD, r, full);
-            tma_gather4(dst + kRegion + lane * 512, map, sg.head * kHD + 64, r, full);
+        if (round > 0 && !warp_wait(is_k ? k_empty(s) : v_empty(s), (round - 1) & 1, abort_flag)) {
+          fail();
+          return false;
+        }
+        if (elect_one()) mbar_arrive_expect_tx(full, tk.rows * kHD * 2);
+        if (boxes) {
+#pragma unroll 1
+          for (int b = 0; b < kTile / p.box_rows; ++b) {
+            const int row = __shfl_sync(0xffffffffu, r.x, b);
+            if (elect_one()) {
+              tma_load_3d(dst, map_box, 0, sg.head, row, full);
+              tma_load_3d(dst + kRegion, map_box, 64, sg.head, row, full);
+            }
+            dst += p.box_rows * 128;
+          }
+        } else {
+#pragma unroll 1
+          for (int b = 0; b < tk.rows / 4; ++b) {
+            int4 q;
+            q.x = __shfl_sync(0xffffffffu, r.x, b);
+            q.y = __shfl_sync(0xffffffffu, r.y, b);
+            q.z = __shfl_sync(0xffffffffu, r.z, b);
+            q.w = __shfl_sync(0xffffffffu, r.w, b);
+            const CUtensorMap *map = tk.drafts > 0 && 4 * b >= tk.at ? map_draft : map_rows;
+            if (elect_one()) {
+              tma_gather4(dst, map, sg.head * kHD, q, full);
+              tma_gather4(dst + kRegion, map, sg.head * kHD + 64, q, full);
+            }
+            dst += 512;
           }
         }
         ++issued;
@@ -498,7 +573,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       };
       if (is_k) {
         // walk the range: streams of (head, sequence, row group)
-        int qtiles = 0, q_issued = 0, op = 0, n = 0;
+        int qtiles = 0, q_issued = 0, step = 0, n = 0;
         int left = hi - lo;
         int head = left > 0 ? lo / total : 0, seq = left > 0 ? start[0] : 0;
         int off = left > 0 ? start[1] : 0;       // tile inside the sequence's row groups
@@ -538,210 +613,253 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             sg.ntok = min(pair_tokens, sg.drafts - sg.tok0);
             const bool two = sg.ntok > p.tile_tokens;
             sg.slot = (sg.t0 == 0 && sg.t1 == nt) ? -1
-                      : 2 * static_cast<int>(blockIdx.x) + (sg.t0 == 0 ? 1 : 0);
-            if (two) op = (op + 1) & ~1;         // both row tiles of a key tile in one op pair
-            sg.op0 = op;
+                      : 2 * bid + (sg.t0 == 0 ? 1 : 0);
+            if (two) step = (step + 1) & ~1;     // row tile x in region x
+            sg.step0 = step;
             sg.qtile = qtiles;
-            const int steps = sg.t1 - sg.t0;
-            op += two ? 2 * steps : steps;
+            const int tiles = sg.t1 - sg.t0;
+            step += two ? 2 * tiles : tiles;
             // the stream that the range start cuts is merged at its first cut
-            if (first_seg && sg.t0 > 0 && sg.t0 <= range) {
+            if (first_seg && sg.t0 > 0 && range_of(lo - sg.t0) == bid - 1) {
               bd.row0 = sg.q0 + sg.tok0;
               bd.ntok = sg.ntok;
               bd.head = head;
-              bd.first = static_cast<int>(blockIdx.x) - 1;
-              bd.last = (lo - sg.t0 + nt - 1) / range;
+              bd.first = bid - 1;
+              bd.last = range_of(lo - sg.t0 + nt - 1);
             }
             first_seg = false;
-            int good = 1;
-            if (lane == 0) {
-              if (n >= kSegRing &&
-                  !mbar_wait(seg_empty(n % kSegRing), ((n / kSegRing) - 1) & 1, abort_flag)) {
-                good = 0;
-                fail();
-              } else {
-                volatile Seg *v = seg_at(n);
-                v->head = sg.head;
-                v->ctx = sg.ctx;
-                v->drafts = sg.drafts;
-                v->q0 = sg.q0;
-                v->seq = sg.seq;
-                v->tok0 = sg.tok0;
-                v->ntok = sg.ntok;
-                v->t0 = sg.t0;
-                v->t1 = sg.t1;
-                v->slot = sg.slot;
-                v->op0 = sg.op0;
-                v->qtile = sg.qtile;
-                v->bad = 0;
-                mbar_arrive(seg_full(n % kSegRing));
-              }
-              // Q tiles: box_tokens * group rows a box
-              for (int x = 0; good && x < (two ? 2 : 1); ++x) {
-                const int s = (qtiles + x) & 1, round = (qtiles + x) >> 1;
-                if (round > 0 && !mbar_wait(q_empty(s), (round - 1) & 1, abort_flag)) {
-                  good = 0;
-                  fail();
-                  break;
-                }
-                const int tok = min(p.tile_tokens, sg.ntok - x * p.tile_tokens);
-                const int boxes = (tok + p.box_tokens - 1) / p.box_tokens;
-                const int box_rows = p.box_tokens * p.group;
-                mbar_arrive_expect_tx(q_full(s), boxes * box_rows * kHD * 2);
-                for (int b = 0; b < boxes; ++b) {
-                  const int row = sg.q0 + sg.tok0 + x * p.tile_tokens + b * p.box_tokens;
-                  const uint32_t dst = sQ + s * kTileBytes + b * box_rows * 128;
-                  tma_load_3d(dst, &tm_q, 0, head * p.group, row, q_full(s));
-                  tma_load_3d(dst + kRegion, &tm_q, 64, head * p.group, row, q_full(s));
-                }
-                ++q_issued;
-              }
-            }
-            if (!__shfl_sync(0xffffffffu, good, 0)) {
+            if (n >= kSegRing &&
+                !warp_wait(seg_empty(n % kSegRing), ((n / kSegRing) - 1) & 1, abort_flag)) {
+              fail();
               ok = false;
               break;
             }
+            if (lane == 0) {
+              volatile Seg *v = seg_at(n);
+              v->head = sg.head;
+              v->ctx = sg.ctx;
+              v->drafts = sg.drafts;
+              v->q0 = sg.q0;
+              v->seq = sg.seq;
+              v->tok0 = sg.tok0;
+              v->ntok = sg.ntok;
+              v->t0 = sg.t0;
+              v->t1 = sg.t1;
+              v->slot = sg.slot;
+              v->step0 = sg.step0;
+              v->qtile = sg.qtile;
+              v->bad = 0;
+              mbar_arrive(seg_full(n % kSegRing));
+            }
+            __syncwarp();
+            // Q tiles: box_tokens * group rows a box
+            for (int x = 0; x < (two ? 2 : 1); ++x) {
+              const int s = (qtiles + x) & 1, round = (qtiles + x) >> 1;
+              if (round > 0 && !warp_wait(q_empty(s), (round - 1) & 1, abort_flag)) {
+                fail();
+                ok = false;
+                break;
+              }
+              const int tok = min(p.tile_tokens, sg.ntok - x * p.tile_tokens);
+              const int boxes = (tok + p.box_tokens - 1) / p.box_tokens;
+              const int box_rows = p.box_tokens * p.group;
+              if (elect_one()) mbar_arrive_expect_tx(q_full(s), boxes * box_rows * kHD * 2);
+#pragma unroll 1
+              for (int b = 0; b < boxes; ++b) {
+                const int row = sg.q0 + sg.tok0 + x * p.tile_tokens + b * p.box_tokens;
+                const uint32_t dst = sQ + s * kTileBytes + b * box_rows * 128;
+                if (elect_one()) {
+                  tma_load_3d(dst, &tm_q, 0, head * p.group, row, q_full(s));
+                  tma_load_3d(dst + kRegion, &tm_q, 64, head * p.group, row, q_full(s));
+                }
+              }
+              ++q_issued;
+            }
+            if (!ok) break;
             ++n;
             qtiles += two ? 2 : 1;
             for (int j = sg.t0; ok && j < sg.t1; ++j) ok = load_tile(sg, j);
-            left -= steps;
+            left -= tiles;
             sg.t0 = 0;
           }
           ++seq;
           off = 0;
         }
-        if (lane == 0) {
-          p.bounds[blockIdx.x] = bd;
-          if (ok) {                              // the walk's end
-            if (n >= kSegRing &&
-                !mbar_wait(seg_empty(n % kSegRing), ((n / kSegRing) - 1) & 1, abort_flag)) {
-              fail();
-            } else {
-              seg_at(n)->head = -1;
-              mbar_arrive(seg_full(n % kSegRing));
-            }
+        if (lane == 0) p.bounds[bid] = bd;
+        if (ok) {                                // the walk's end
+          if (n >= kSegRing &&
+              !warp_wait(seg_empty(n % kSegRing), ((n / kSegRing) - 1) & 1, abort_flag)) {
+            fail();
+          } else if (lane == 0) {
+            seg_at(n)->head = -1;
+            mbar_arrive(seg_full(n % kSegRing));
           }
-          for (int s = max(0, q_issued - 2); s < q_issued; ++s)   // drain
-            mbar_wait(q_full(s & 1), (s >> 1) & 1, nullptr);
+          __syncwarp();
         }
+        for (int s = max(0, q_issued - 2); s < q_issued; ++s)   // drain
+          warp_wait(q_full(s & 1), (s >> 1) & 1, never);
       } else {
         Seg sg;
         for (int n = 0; ok; ++n) {
-          if (!read_seg(n, sg, true)) {
+          if (!read_seg(n, sg)) {
             fail();
             break;
           }
-          seg_done(n, true);
+          seg_done(n);
           if (sg.head < 0) break;
           for (int j = sg.t0; ok && j < sg.t1; ++j) ok = load_tile(sg, j);
         }
       }
-      if (lane == 0)   // the last copies must land before the CTA exits
-        for (int j = max(0, issued - stages); j < issued; ++j)
-          mbar_wait(is_k ? k_full(j % stages) : v_full(j % stages), (j / stages) & 1, nullptr);
+      for (int j = max(0, issued - stages); j < issued; ++j)   // the last copies must land
+        warp_wait(is_k ? k_full(j % stages) : v_full(j % stages), (j / stages) & 1, never);
     } else if (warp == kWarpMma) {
       // ---------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = umma_idesc_bf16(kTile, kTile, false);
-        constexpr uint32_t idesc_pv = umma_idesc_bf16(kTile, kHD, true);  // B (V) MN-major
-        bool ok = true;
-        int s_count[2] = {0, 0}, pv_count[2] = {0, 0}, o_used[2] = {0, 0};
-        // the PV that each x owes: MMA steps (0: none), first of its segment,
-        // V tile, last user of it
-        int steps[2] = {0, 0}, first[2] = {0, 0}, vtile[2] = {0, 0}, frees[2] = {0, 0};
-        auto issue_pv = [&](int x) -> bool {
-          if (steps[x] == 0) return true;
-          const int s = vtile[x] % kVStages;
-          if (!mbar_wait(v_full(s), (vtile[x] / kVStages) & 1, abort_flag) ||
-              !mbar_wait(p_full(x), pv_count[x] & 1, abort_flag))
-            return false;
-          // the first PV of a segment overwrites O_x: the last one must be read out
-          if (first[x]) {
-            if (o_used[x] > 0 && !mbar_wait(o_free(x), (o_used[x] - 1) & 1, abort_flag)) return false;
-            ++o_used[x];
+      // The warp's own instructions are on the path of every tile: one copy of the
+      // code for both x, ring positions counted up, descriptors that differ by adds.
+      constexpr uint32_t idesc_s = umma_idesc_bf16(kTile, 0, false);            // N is added
+      constexpr uint32_t idesc_pv = umma_idesc_bf16(kTile, kHD, true);          // B (V) MN-major
+      constexpr uint32_t kTileStep = kTileBytes >> 4;
+      const uint32_t tm = uniform(static_cast<int>(tmem));
+      const uint64_t dq0 = desc_kmajor(sQ, 0), dk0 = desc_kmajor(sK(0), 0), dv0 = desc_v_mnmajor(sV(0));
+      struct Owed {        // the PV of an x's last step
+        int steps = 0;     // its MMAs (16 keys each); 0: none
+        int stage = 0, parity = 0;       // of the V tile
+        int segs = 0;                    // segments that have begun to overwrite O_x
+        bool fresh = false;              // the x's first PV of the segment overwrites O_x
+        bool frees = false;              // last user of the V tile
+        bool ends = false;               // the x's last PV of the segment
+        int p_parity = 0;                // of p_full(x)
+      };
+      Owed mine, other;                  // of this step's x and of the other one
+      bool ok = true;
+      int x = 0, step = 0;
+      int ks = 0, kp = 0, vs = 0, vp = 0;   // stage and parity of the next K and V tile
+      auto issue_pv = [&]() -> bool {
+        if (mine.steps == 0) return true;
+        if (!warp_wait(v_full(mine.stage), mine.parity, abort_flag) ||
+            !warp_wait(p_full(x), mine.p_parity, abort_flag))
+          return false;
+        mine.p_parity ^= 1;
+        // what the last segment left in O_x must have been read out
+        if (mine.fresh) {
+          if (mine.segs > 0 && !warp_wait(o_free(x), (mine.segs - 1) & 1, abort_flag)) return false;
+          ++mine.segs;
+        }
+        tc_fence_after();
+        const int stage = uniform(mine.stage), n_mma = uniform(mine.steps);
+        const uint64_t dv = desc_at(dv0, stage * kTileStep);
+        const uint32_t to = tm + (2 + x) * kTile, ts = tm + x * kTile;
+        const uint32_t acc = uniform(mine.fresh ? 0 : 1);
+        if (elect_one()) {
+          if (n_mma == kTile / 16) {
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              umma_bf16_tmem_a(to, ts + kk * 8, desc_at(dv, kk * (2048 >> 4)), idesc_pv,
+                               kk > 0 ? 1u : acc);
+          } else {
+#pragma unroll 1
+            for (int kk = 0; kk < n_mma; ++kk)
+              umma_bf16_tmem_a(to, ts + kk * 8, desc_at(dv, kk * (2048 >> 4)), idesc_pv,
+                               kk > 0 ? 1u : acc);
           }
-          tc_fence_after();
-          const uint64_t dv = desc_v_mnmajor(sV(s));
-          for (int kk = 0; kk < steps[x]; ++kk)
-            umma_bf16_tmem_a(tmem_o(x), tmem_s(x) + kk * 8, desc_at(dv, kk * (2048 >> 4)), idesc_pv,
-                             (first[x] && kk == 0) ? 0u : 1u);
-          umma_commit(pv_done(x));
-          ++pv_count[x];
-          if (frees[x]) umma_commit(v_empty(s));
-          steps[x] = 0;
-          return true;
-        };
-        int op = 0, ktile = 0, vbase = 0;
-        Seg sg;
-        for (int n = 0; ok; ++n) {
-          if (!read_seg(n, sg, false)) {
+          if (mine.frees) umma_commit(v_empty(stage));
+          if (mine.ends) umma_commit(pv_done(x));
+        }
+        mine.steps = 0;
+        return true;
+      };
+      auto next_step = [&]() {
+        const Owed t = mine;
+        mine = other;
+        other = t;
+        x ^= 1;
+        ++step;
+      };
+      Seg sg = {};
+      for (int n = 0; ok; ++n) {
+        if (!read_seg(n, sg)) {
+          ok = false;
+          break;
+        }
+        seg_done(n);
+        if (sg.head < 0) break;
+        if (step < sg.step0) {       // a step left out
+          ok = issue_pv();
+          next_step();
+        }
+        const bool two = sg.ntok > p.tile_tokens;
+        const int steps = (two ? 2 : 1) * (sg.t1 - sg.t0), whole = sg.ctx / kTile;
+#pragma unroll 1
+        for (int i = 0; ok && i < steps; ++i) {
+          if (!issue_pv()) {
             ok = false;
             break;
           }
-          seg_done(n, false);
-          if (sg.head < 0) break;
-          for (; ok && op < sg.op0; ++op) ok = issue_pv(op & 1);  // an op left out
-          const bool two = sg.ntok > p.tile_tokens;
-          const int tiles = sg.t1 - sg.t0, ops = two ? 2 * tiles : tiles;
-          for (int i = 0; ok && i < ops; ++i, ++op) {
-            const int x = op & 1;
-            if (!issue_pv(x)) {
-              ok = false;
-              break;
-            }
-            const int tile = two ? i >> 1 : i;
-            const int qt = sg.qtile + (two ? x : 0);
-            const int s = ktile % kKStages;
-            if ((i < (two ? 2 : 1) && !mbar_wait(q_full(qt & 1), (qt >> 1) & 1, abort_flag)) ||
-                !mbar_wait(k_full(s), (ktile / kKStages) & 1, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t dq = desc_kmajor(sQ + (qt & 1) * kTileBytes, 0), dk = desc_kmajor(sK(s), 0);
+          const int qt = sg.qtile + (two ? x : 0);
+          if ((i < (two ? 2 : 1) && !warp_wait(q_full(qt & 1), (qt >> 1) & 1, abort_flag)) ||
+              !warp_wait(k_full(ks), kp, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int tile = sg.t0 + (two ? i >> 1 : i);
+          const int rows = tile < whole ? kTile : tile_keys(sg.ctx, sg.drafts, tile).rows;
+          const uint32_t idesc = idesc_s | (static_cast<uint32_t>(rows >> 3) << 17);
+          const uint64_t dq = desc_at(dq0, (qt & 1) * kTileStep), dk = desc_at(dk0, ks * kTileStep);
+          const uint32_t ts = tm + x * kTile;
+          const bool frees = !two || x == 1;
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kHD / 16; ++kk)
-              umma_bf16(tmem_s(x), desc_at(dq, kmajor_step(kk)), desc_at(dk, kmajor_step(kk)), idesc_s,
+              umma_bf16(ts, desc_at(dq, kmajor_step(kk)), desc_at(dk, kmajor_step(kk)), idesc,
                         kk > 0 ? 1u : 0u);
             umma_commit(s_full(x));
-            ++s_count[x];
-            const bool frees_kv = !two || x == 1;
-            if (frees_kv) {
-              umma_commit(k_empty(s));
-              ++ktile;
-            }
-            if (i >= ops - (two ? 2 : 1)) umma_commit(q_empty(qt & 1));
-            steps[x] = tile_keys(sg.ctx, sg.drafts, sg.t0 + tile).rows / 16;
-            first[x] = i < 2;
-            vtile[x] = vbase + tile;
-            frees[x] = frees_kv;
+            if (frees) umma_commit(k_empty(ks));
+            if (i >= steps - (two ? 2 : 1)) umma_commit(q_empty(qt & 1));
           }
-          vbase += tiles;
-        }
-        if (ok) ok = issue_pv(op & 1) && issue_pv((op + 1) & 1);
-        if (!ok) fail();
-        for (int x = 0; x < 2; ++x) {  // every issued MMA completes before TMEM is freed
-          if (s_count[x] > 0) mbar_wait(s_full(x), (s_count[x] - 1) & 1, nullptr);
-          if (pv_count[x] > 0) mbar_wait(pv_done(x), (pv_count[x] - 1) & 1, nullptr);
+          mine.steps = rows / 16;
+          mine.fresh = i < 2;
+          mine.ends = i >= steps - 2;
+          mine.frees = frees;
+          mine.stage = vs;
+          mine.parity = vp;
+          if (frees) {
+            if (++ks == kKStages) {
+              ks = 0;
+              kp ^= 1;
+            }
+            if (++vs == kVStages) {
+              vs = 0;
+              vp ^= 1;
+            }
+          }
+          next_step();
         }
       }
-      __syncwarp();
+      if (ok) {
+        ok = issue_pv();
+        next_step();
+        ok = ok && issue_pv();
+      }
+      if (!ok) fail();
+      // every issued MMA completes before TMEM is freed
+      if (elect_one()) umma_commit(drained);
+      warp_wait(drained, 0, never);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kRegsHigh));
     // ------------------------------------------------------ softmax 0 / 1
     const int x = warp >> 2;
     const int quad = warp & 3;                       // TMEM lanes 32 * quad ..
-    const int r = quad * 32 + lane;                  // row of the MMA tile
+    const int row = quad * 32 + lane;                // row of the MMA tile
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const int r_tok = r / p.group, r_head = r - r_tok * p.group;
+    const int r_tok = row / p.group, r_head = row - r_tok * p.group;
     const float c = p.scale_log2;
     bool ok = true;
-    int s_count = 0, vbase = 0, merges = 0;
-    int pv_count[2] = {0, 0};
+    int steps_seen = 0, tbase = 0, merges = 0;
+    int segs[2] = {0, 0};                            // segments each warpgroup has had steps in
     Seg sg;
     for (int n = 0; ok; ++n) {
-      if (!read_seg(n, sg, true)) {
+      if (!read_seg(n, sg)) {
         ok = false;
         break;
       }
@@ -753,67 +871,44 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       const bool live = r_tok < ntok_x;                          // this row exists
       const bool warp_live = quad * 32 < ntok_x * p.group;       // some row of the warp does
       const int64_t q_row = static_cast<int64_t>(sg.q0) + sg.tok0 + tok_x + r_tok;
-      const int step = two ? 1 : 2;
-      const int i0 = two ? 0 : ((x - sg.op0) & 1);
+      const int whole_tiles = sg.ctx / kTile;
+      const int i0 = two ? 0 : (x - sg.step0) & 1;   // this warpgroup's first tile
       float m_used = -INFINITY, l_sum = 0.f;         // running maximum of the scores, row sum
 
-      for (int i = i0; ok && i < tiles; i += step) {
-        const TileKeys tk = tile_keys(sg.ctx, sg.drafts, sg.t0 + i);
-        const bool whole = tk.cached == kTile;
-        // the row's visible columns of a tile that is not all cached keys
-        uint32_t vis[4] = {0u, 0u, 0u, 0u};
-        if (!whole && warp_live) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int left = tk.drafts - 32 * w;
-            if (live && left > 0) {
-              vis[w] = static_cast<uint32_t>(
-                  __ldg(p.tree_mask + q_row * p.mask_words + (tk.u0 >> 5) + w));
-              if (left < 32) vis[w] &= (1u << left) - 1u;
-            }
-          }
-          // move the drafts' bits up to their columns and add the cached ones
-          if (tk.at & 64) {
-            vis[3] = vis[1];
-            vis[2] = vis[0];
-            vis[1] = vis[0] = 0u;
-          }
-          if (tk.at & 32) {
-            vis[3] = vis[2];
-            vis[2] = vis[1];
-            vis[1] = vis[0];
-            vis[0] = 0u;
-          }
-          const int sh = tk.at & 31;
-          vis[3] = __funnelshift_l(vis[2], vis[3], sh);
-          vis[2] = __funnelshift_l(vis[1], vis[2], sh);
-          vis[1] = __funnelshift_l(vis[0], vis[1], sh);
-          vis[0] <<= sh;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int left = tk.cached - 32 * w;
-            vis[w] |= left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
-          }
+      // warps without a row take no part: the first warp arrives for them too
+      const int live_warps = min(4, (ntok_x * p.group + 31) / 32);
+      const uint32_t arrivals = quad == 0 ? 5 - live_warps : 1;
+      const int my_steps = two ? tiles : (tiles - i0 + 1) / 2;
+      if (!warp_live) steps_seen += my_steps;
+      for (int i = i0; ok && warp_live && i < tiles; i += two ? 1 : 2) {
+        const bool whole = sg.t0 + i < whole_tiles;
+        TileKeys tk;
+        tk.drafts = 0;
+        const int32_t *mask_row = p.tree_mask + q_row * p.mask_words;
+        if (!whole) {
+          tk = tile_keys(sg.ctx, sg.drafts, sg.t0 + i);
+          if (live && tk.drafts > 0)
+            asm volatile("prefetch.global.L1 [%0];" :: "l"(mask_row + (tk.u0 >> 5)));
         }
-        if (!warp_wait(s_full(x), s_count & 1, abort_flag)) {
+        if (!warp_wait(s_full(x), steps_seen & 1, abort_flag)) {
           ok = false;
           break;
         }
-        ++s_count;
+        ++steps_seen;
         if (tk.drafts > 0) {
           // drafted V values that are not finite must not meet the weights of
-          // rows that do not see them (0 * NaN); thread r takes V row r
-          const int vt = vbase + i;
+          // rows that do not see them (0 * NaN); the live threads share the V rows
+          const int vt = tbase + i;
           if (!warp_wait(v_full(vt % kVStages), (vt / kVStages) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          if (r >= tk.at && r < tk.at + tk.drafts) {
-            const uint32_t row = sV(vt % kVStages) + r * 128;
+          for (int u = row; u < tk.drafts; u += 32 * live_warps) {
+            const uint32_t v_row = sV(vt % kVStages) + (tk.at + u) * 128;
             uint32_t inf = 0u;
-#pragma unroll 4
+#pragma unroll 1
             for (int e = 0; e < 16; ++e) {
-              const uint4 v = lds128(row + (e >> 3) * kRegion + (e & 7) * 16);
+              const uint4 v = lds128(v_row + (e >> 3) * kRegion + (e & 7) * 16);
               // an all-ones exponent carries into the sign bit
               inf |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
                      ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
@@ -822,8 +917,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
               // the flag first: a warpgroup that already finds zeros here sees it too
               seg_at(n)->bad = 1;
               __threadfence_block();
+#pragma unroll 1
               for (int e = 0; e < 64; ++e) {
-                const uint32_t a = row + (e >> 5) * kRegion + (e & 31) * 4;
+                const uint32_t a = v_row + (e >> 5) * kRegion + (e & 31) * 4;
                 uint32_t v;
                 asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
                 if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
@@ -835,22 +931,53 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           }
           __syncwarp();
         }
-        if (warp_live) {
+        {
           tc_fence_after();
-          float s[kTile];
+          const uint32_t ts = tmem_s(x) + lane_off;
+          if (!whole || p.flip != 1.f) {
+            // a negative or zero scale and the columns the row does not see, back
+            // into TMEM, so that what follows is the same code for every tile
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) {
+              uint32_t word = 0xffffffffu;             // the row's visible columns of the 32
+              if (!whole) {
+                const int left = tk.cached - 32 * cc;
+                word = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
+                const int u = 32 * cc - tk.at;         // draft of the first column
+                if (live && u > -32 && u < tk.drafts) {
+                  const int32_t *m = mask_row + (tk.u0 >> 5) + (u >> 5);
+                  const uint32_t lo = u >= 0 ? static_cast<uint32_t>(__ldg(m)) : 0u;
+                  const uint32_t hi =
+                      (u & ~31) + 32 < tk.drafts ? static_cast<uint32_t>(__ldg(m + 1)) : 0u;
+                  uint32_t bits = __funnelshift_r(lo, hi, u & 31);
+                  if (tk.drafts - u < 32) bits &= (1u << (tk.drafts - u)) - 1u;
+                  word |= bits;
+                }
+              }
+              float s[32];
+              tmem_ld32(ts + cc * 32, s);
+              tmem_wait_ld();
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc)
-            tmem_ld32(tmem_s(x) + lane_off + cc * 32, *reinterpret_cast<float(*)[32]>(s + cc * 32));
-          tmem_wait_ld();
-          if (p.flip != 1.f) {
-#pragma unroll
-            for (int e = 0; e < kTile; ++e) s[e] *= p.flip;
+              for (int e = 0; e < 32; ++e) s[e] = ((word >> e) & 1u) ? s[e] * p.flip : -INFINITY;
+              tmem_st32(ts + cc * 32, s);
+            }
+            tmem_wait_st();
           }
-          if (!whole) {
-#pragma unroll
-            for (int e = 0; e < kTile; ++e) s[e] = ((vis[e >> 5] >> (e & 31)) & 1u) ? s[e] : -INFINITY;
+          // The scores are read twice, 32 columns at a time in short loops: code that
+          // holds the whole row in registers is four times as long and its
+          // instruction fetches cost more than the second read.
+          float s0[32], s1[32];
+          float mt = -INFINITY;
+          tmem_ld32(ts, s0);
+#pragma unroll 1
+          for (int cc = 0; cc < 4; cc += 2) {
+            tmem_wait_ld();
+            tmem_ld32(ts + cc * 32 + 32, s1);
+            mt = fmaxf(mt, max32(s0));
+            tmem_wait_ld();
+            tmem_ld32(ts + ((cc * 32 + 64) & 127), s0);   // the last one starts the second read
+            mt = fmaxf(mt, max32(s1));
           }
-          const float mt = max128(s);
           const bool grow =
               mt != -INFINITY && (m_used == -INFINITY || (mt - m_used) * c > kRescaleThreshold);
           float alpha = 1.f;
@@ -861,8 +988,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             m_used = mt;
           }
-          // O_x holds this x's earlier PVs of the segment, complete because S
-          // completed after them
+          // O_x holds this x's earlier PVs of the segment, complete because this S
+          // was issued behind them
           if (i > i0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
             for (int cc = 0; cc < 4; ++cc) {
@@ -877,66 +1004,68 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           }
           // a row that has seen nothing yet keeps weights of 0: exp2(-inf - 0)
           const float mc = m_used == -INFINITY ? 0.f : m_used * c;
-          float2 rs2[4];
+          float2 rs2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          auto weigh = [&](const float (&s)[32], int cc) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) rs2[e] = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float2 xx = ffma2(make_float2(s[half * 64 + 2 * e], s[half * 64 + 2 * e + 1]),
-                                      make_float2(c, c), make_float2(-mc, -mc));
+            for (int e = 0; e < 16; ++e) {
+              const float2 xx =
+                  ffma2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(c, c), make_float2(-mc, -mc));
               const float2 pp = make_float2(ex2(xx.x), ex2(xx.y));
-              rs2[e & 3] = fadd2(rs2[e & 3], pp);
+              rs2[e & 1] = fadd2(rs2[e & 1], pp);
               pk[e] = float2_to_bf16x2(pp.x, pp.y);
             }
-            tmem_st32_u(tmem_s(x) + lane_off + half * 32, pk);
+            tmem_st16_u(ts + cc * 16, pk);   // over scores that have been read
+          };
+#pragma unroll 1
+          for (int cc = 0; cc < 4; cc += 2) {
+            tmem_wait_ld();
+            tmem_ld32(ts + cc * 32 + 32, s1);
+            weigh(s0, cc);
+            tmem_wait_ld();
+            if (cc == 0) tmem_ld32(ts + 64, s0);
+            weigh(s1, cc + 1);
           }
-          const float2 rs01 = fadd2(rs2[0], rs2[1]), rs23 = fadd2(rs2[2], rs2[3]);
-          l_sum += (rs01.x + rs01.y) + (rs23.x + rs23.y);
+          l_sum += (rs2[0].x + rs2[0].y) + (rs2[1].x + rs2[1].y);
           tmem_wait_st();
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(x));
+        if (lane == 0) mbar_arrive_count(p_full(x), arrivals);
       }
       if (!ok) break;
 
       // ---- the segment's end
-      int ops_x[2];                                  // ops of each warpgroup in the segment
+      tbase += tiles;
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int y0 = (y - sg.op0) & 1;
-        ops_x[y] = two ? tiles : tiles > y0 ? (tiles - y0 + 1) / 2 : 0;
-        pv_count[y] += ops_x[y];
-      }
-      vbase += tiles;
+      for (int y = 0; y < 2; ++y)
+        if (two || tiles > ((y - sg.step0) & 1)) ++segs[y];
+      const int owner = two ? x : (sg.step0 + tiles - 1) & 1;
       const bool merge = !two && tiles > 1;          // both warpgroups hold a part of the rows
-      const int owner = two ? x : (sg.op0 + tiles - 1) & 1;
-      if (merge && owner != x) {
-        // hand the row's maximum and sum to the other warpgroup
-        if (merges > 0) ok = warp_wait(ml_free, (merges - 1) & 1, abort_flag);
-        if (ok) {
-          ml_x[r] = make_float2(m_used, l_sum);
+      if (!warp_live) {
+      } else if (owner != x) {
+        if (merge) {
+          // hand the rows' maxima and sums to the other warpgroup
+          if (merges > 0) ok = warp_wait(ml_free, (merges - 1) & 1, abort_flag);
+          ml[row] = make_float2(m_used, l_sum);
           __syncwarp();
-          if (lane == 0) mbar_arrive(ml_full);
+          if (lane == 0) mbar_arrive_count(ml_full, arrivals);
         }
-      } else if (owner == x) {
-        ok = warp_wait(pv_done(x), (pv_count[x] - 1) & 1, abort_flag);
+      } else {
         float own = 1.f, oth = 0.f;                  // factors of O_x and the other's O
         float m_all = m_used;
-        if (ok && merge) {
-          ok = warp_wait(ml_full, merges & 1, abort_flag) &&
-               warp_wait(pv_done(1 - x), (pv_count[1 - x] - 1) & 1, abort_flag);
-          const float2 o = ml_x[r];
+        if (merge) {
+          ok = warp_wait(ml_full, merges & 1, abort_flag);
+          const float2 o = ml[row];
+          __syncwarp();
+          if (lane == 0) mbar_arrive_count(ml_free, arrivals);
           m_all = fmaxf(m_used, o.x);
           own = m_used == -INFINITY ? 0.f : ex2((m_used - m_all) * c);
           oth = o.x == -INFINITY ? 0.f : ex2((o.x - m_all) * c);
-          l_sum = l_sum * own + o.y * oth;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(ml_free);
+          l_sum = (m_used == -INFINITY ? 0.f : l_sum * own) + (o.x == -INFINITY ? 0.f : o.y * oth);
         }
+        ok = ok && warp_wait(pv_done(x), (segs[x] - 1) & 1, abort_flag) &&
+             (!merge || warp_wait(pv_done(1 - x), (segs[1 - x] - 1) & 1, abort_flag));
         tc_fence_after();
         const bool bad = seg_at(n)->bad != 0;
         if (ok && warp_live) {
@@ -945,22 +1074,23 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           oth *= inv;
           __nv_bfloat16 *orow = p.out + (q_row * p.num_q_heads + sg.head * p.group + r_head) * kHD;
           const int64_t rec = static_cast<int64_t>(sg.slot) * p.rows_cap +
-                              tok_x * p.group + r;   // partial record's row
-          if (sg.slot >= 0 && live)
+                              tok_x * p.group + row;   // partial record's row
+          if (sg.slot >= 0 && live) 
             p.ml[rec] = make_float2(m_all == -INFINITY ? -INFINITY : m_all * c, l_sum);
 #pragma unroll 1
           for (int cc = 0; cc < 4; ++cc) {
             float o[32];
             tmem_ld32(tmem_o(x) + lane_off + cc * 32, o);
             tmem_wait_ld();
+            // an accumulator the row has no part in may not have been written
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= own;
+            for (int e = 0; e < 32; ++e) o[e] = own == 0.f ? 0.f : o[e] * own;
             if (merge) {
               float o2[32];
               tmem_ld32(tmem_o(1 - x) + lane_off + cc * 32, o2);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = fmaf(o2[e], oth, o[e]);
+              for (int e = 0; e < 32; ++e) o[e] = oth == 0.f ? o[e] : fmaf(o2[e], oth, o[e]);
             }
             if (bad && live) {
               // give back what was taken out of V for the drafts this row sees
@@ -1005,12 +1135,16 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(o_free(x));
-          if (merge) mbar_arrive(o_free(1 - x));
+          mbar_arrive_count(o_free(x), arrivals);
+          if (merge) mbar_arrive_count(o_free(1 - x), arrivals);
         }
       }
       if (merge) ++merges;
-      seg_done(n, true);
+      seg_done(n);
+      // the warpgroup stays together by segments, so that a warp without a row never
+      // misses a phase of the other barriers
+      if (lane == 0) mbar_arrive(wg_end(x));
+      ok = ok && warp_wait(wg_end(x), n & 1, abort_flag);
     }
     if (!ok) fail();
   }
@@ -1023,42 +1157,86 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   }
 }
 
-// Merge the pieces of the streams that range boundaries cut: one warp a row,
-// each lane four dims. A stream's pieces lie in CTAs first .. last, in record
-// 2c + 1 of the first (it starts there) and 2c of the others.
+// Merge the pieces of the streams that range boundaries cut, each lane four dims
+// of a row. A stream's pieces lie in CTAs first .. last, in record 2c + 1 of the
+// first (it starts there) and 2c of the others. A warp merges a row of up to
+// eight pieces; with more, the CTA's eight warps share the row's pieces, so that
+// no warp waits for more than a few loads in turn.
 constexpr int kCombineWarps = 8;
 
-__global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kCombineWarps * 32, 2) tree_combine_kernel(const TreeParams p) {
+  __shared__ float2 s_ml[kCombineWarps];
+  __shared__ float4 s_o[kCombineWarps][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Boundary b = p.bounds[blockIdx.x];
   if (b.row0 < 0) return;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = b.ntok * p.group;
-  for (int row = blockIdx.y * kCombineWarps + (threadIdx.x >> 5); row < rows;
-       row += gridDim.y * kCombineWarps) {
-    // records hold two row tiles of tile_tokens * group rows back to back
-    auto rec = [&](int piece) {
-      return static_cast<int64_t>(2 * piece + (piece == b.first ? 1 : 0)) * p.rows_cap + row;
-    };
-    float m = -INFINITY;
-    for (int c = b.first + lane; c <= b.last; c += 32) m = fmaxf(m, p.ml[rec(c)].x);
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    float l = 0.f;
+  const bool shared_row = b.last - b.first >= kCombineWarps;
+  const int share = shared_row ? kCombineWarps : 1;   // warps on a row
+  const int part = shared_row ? warp : 0;
+  const int row0 = shared_row ? blockIdx.y : blockIdx.y * kCombineWarps + warp;
+  const int row_step = gridDim.y * (shared_row ? 1 : kCombineWarps);
+  for (int row = row0; row < rows; row += row_step) {
+    float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m != -INFINITY) {
-#pragma unroll 4
-      for (int c = b.first; c <= b.last; ++c) {
-        const float2 ml = p.ml[rec(c)];
-        const float4 v = reinterpret_cast<const float4 *>(p.po + rec(c) * kHD)[lane];
-        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-        if (ml.x == -INFINITY) continue;   // a piece the row sees nothing of
-        l += w * ml.y;
-        o.x += w * v.x;
-        o.y += w * v.y;
-        o.z += w * v.z;
-        o.w += w * v.w;
+    // eight pieces' loads in flight at a time
+    for (int c0 = b.first + part; c0 <= b.last; c0 += 8 * share) {
+      float2 ml[8];
+      float4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = min(c0 + j * share, b.last);
+        const int64_t rec = static_cast<int64_t>(2 * c + (c == b.first ? 1 : 0)) * p.rows_cap + row;
+        ml[j] = p.ml[rec];
+        v[j] = reinterpret_cast<const float4 *>(p.po + rec * kHD)[lane];
       }
+      float mt = m;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c0 + j * share <= b.last) mt = fmaxf(mt, ml[j].x);
+      if (mt == -INFINITY) continue;
+      const float a = m == -INFINITY ? 0.f : ex2(m - mt);
+      l *= a;
+      o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+      m = mt;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // nothing of a piece of which the row sees nothing
+        if (c0 + j * share > b.last || ml[j].x == -INFINITY) continue;
+        const float w = ex2(ml[j].x - m);
+        l += w * ml[j].y;
+        o.x += w * v[j].x;
+        o.y += w * v[j].y;
+        o.z += w * v[j].z;
+        o.w += w * v[j].w;
+      }
+    }
+    if (shared_row) {
+      s_o[warp][lane] = o;
+      if (lane == 0) s_ml[warp] = make_float2(m, l);
+      __syncthreads();
+      if (warp == 0) {
+        float mt = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kCombineWarps; ++w) mt = fmaxf(mt, s_ml[w].x);
+        l = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kCombineWarps; ++w) {
+          const float2 ml = s_ml[w];
+          if (ml.x == -INFINITY) continue;
+          const float f = ex2(ml.x - mt);
+          const float4 v = s_o[w][lane];
+          l += f * ml.y;
+          o.x += f * v.x;
+          o.y += f * v.y;
+          o.z += f * v.z;
+          o.w += f * v.w;
+        }
+      }
+      __syncthreads();
+      if (warp != 0) continue;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int tok = row / p.group, g = row - tok * p.group;
@@ -1170,11 +1348,6 @@ cudaError_t launch_tree_decode(const TreeDecodeArgs &a, cudaStream_t stream) {
   std::call_once(attr_once, [] {
     attr_err = cudaFuncSetAttribute(tree_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     kSmemBytes);
-    // setmaxnreg.inc waits until the registers it asks for are free: refuse a
-    // build whose launch allocation is not the one the split adds up to
-    cudaFuncAttributes fa;
-    if (attr_err == cudaSuccess) attr_err = cudaFuncGetAttributes(&fa, tree_decode_kernel);
-    if (attr_err == cudaSuccess && fa.numRegs != kRegsLaunch) attr_err = cudaErrorInvalidConfiguration;
   });
   if (attr_err != cudaSuccess) return attr_err;
   const int grid = decode_tc_grid();
@@ -1230,7 +1403,7 @@ cudaError_t launch_tree_decode(const TreeDecodeArgs &a, cudaStream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (p.rows_cap + kCombineWarps - 1) / kCombineWarps);
+  cfg.gridDim = dim3(grid, p.rows_cap < 32 ? p.rows_cap : 32);
   cfg.blockDim = dim3(kCombineWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
