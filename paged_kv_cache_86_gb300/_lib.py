@@ -499,31 +499,48 @@ def paged_prefill(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_tables,
 
 
 # ------------------------------------------------ drafted rounds on the cache
+#
+# The smallest of these calls take a few microseconds on the GPU, so each one
+# tests its arguments in one expression of plain attribute reads; only when that
+# fails does it look for the tensor at fault and name it.
+
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+# the current stream's handle without building a Stream object (2 us of a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def _dense(dtype, ndim, **tensors):
     """dtype, rank and dense row-major layout of each named tensor (see _need)."""
     for name, t in tensors.items():
-        if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != ndim
-                or not t.is_contiguous()):
-            _need(t, name, dtype, ndim, contiguous=True, on_gpu=False)
+        _need(t, name, dtype, ndim, contiguous=True, on_gpu=False)
 
 
 def _rows(**tensors):
     """bf16 [T, H, D] tensors whose token rows are dense [H, D] blocks at any token stride."""
     for name, t in tensors.items():
-        _need(t, name, torch.bfloat16, 3, on_gpu=False)
+        _need(t, name, _BF16, 3, on_gpu=False)
         _, h, d = t.shape
         if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
             raise ValueError(f"{name} rows must be contiguous [H, D] blocks")
 
 
-def _token_stride(t: torch.Tensor) -> int:
-    # the stride of a single row is arbitrary and never used
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _row_stride(t) -> int:
+    """Token stride of bf16 [T, H, D] rows, or -1 where _rows tells what is wrong."""
+    if t.dtype is not _BF16:
+        return -1
+    try:
+        n, h, d = t.shape
+    except ValueError:
+        return -1
+    st, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
+        return -1
+    return st if n > 1 else h * d   # the stride of a single row is arbitrary and never used
 
 
-def _one_device(**tensors) -> torch.device:
-    """Every tensor on the GPU, and on the same one; that device."""
+def _refuse_device(**tensors):
+    """Raise for the first tensor that is not on the GPU of the ones before it."""
     dev = None
     for name, t in tensors.items():
         if not t.is_cuda:
@@ -532,64 +549,82 @@ def _one_device(**tensors) -> torch.device:
             dev = t.device
         elif t.device != dev:
             raise ValueError(f"{name} is on {t.device}, not on {dev}")
-    return dev
+    raise AssertionError("the tensors share a device")
 
 
-class _On:
-    """Makes `device` current and, when a stream is named, that stream too, so that the
-    launch and every buffer allocated inside belong to it. Costs nothing to speak of
-    when both already are."""
-
-    def __init__(self, device: torch.device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        self._ctx = None
-        if stream is not None:
-            self._ctx = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self._ctx = torch.cuda.device(device)
-        self._device, self._stream = device, stream
-
-    def __enter__(self) -> int:
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        s = self._stream if self._stream is not None else torch.cuda.current_stream(self._device)
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+def _enter(index: int, stream):
+    """(context to leave, stream handle): makes GPU `index` current and, when a stream is
+    named, that stream too, so that the launch and every buffer allocated until the
+    context is left belong to it. None where both are current already."""
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return None, _raw_stream(index)
+        ctx = torch.cuda.device(index)
+        ctx.__enter__()
+        return ctx, _raw_stream(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    ctx = torch.cuda.stream(stream)
+    ctx.__enter__()
+    return ctx, stream.cuda_stream
 
 
-def _norm_rope_args(q, k, positions, cos_sin, q_weight, k_weight):
-    """Checks what both head-norm-and-rotation calls share; the tensors for the device check."""
-    _rows(q=q, k=k)
-    _dense(torch.int32, 1, positions=positions)
-    _dense(torch.float32, 2, cos_sin=cos_sin)
-    named = {"q": q, "k": k, "positions": positions, "cos_sin": cos_sin}
+def _leave(ctx):
+    if ctx is not None:
+        ctx.__exit__(None, None, None)
+
+
+def _check_norm_rope(q, k, positions, cos_sin, q_weight, k_weight):
+    """Checks the types, layouts and sizes that both head-norm-and-rotation calls share;
+    the token strides of q and k."""
+    try:
+        qs, ks = _row_stride(q), _row_stride(k)
+        fine = (qs >= 0 and ks >= 0 and positions.dtype is _I32 and positions.dim() == 1
+                and positions.is_contiguous() and cos_sin.dtype is _F32 and cos_sin.dim() == 2
+                and cos_sin.is_contiguous()
+                and (q_weight is None or (q_weight.dtype is _BF16 and q_weight.dim() == 1
+                                          and q_weight.is_contiguous()))
+                and (k_weight is None or (k_weight.dtype is _BF16 and k_weight.dim() == 1
+                                          and k_weight.is_contiguous())))
+    except AttributeError:
+        fine = False
+    if not fine:
+        _rows(q=q, k=k)
+        _dense(_I32, 1, positions=positions)
+        _dense(_F32, 2, cos_sin=cos_sin)
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                _dense(_BF16, 1, **{name: w})
     t, _, d = q.shape
-    if k.shape[0] != t or k.shape[2] != d or positions.shape[0] != t:
+    tk, _, dk = k.shape
+    if tk != t or dk != d or positions.numel() != t:
         raise ValueError("shape mismatch between q/k/positions")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _dense(torch.bfloat16, 1, **{name: w})
-            if w.shape[0] != d:
-                raise ValueError(f"{name} must have head_dim entries")
-            named[name] = w
-    return named
+    if q_weight is not None and q_weight.numel() != d:
+        raise ValueError("q_weight must have head_dim entries")
+    if k_weight is not None and k_weight.numel() != d:
+        raise ValueError("k_weight must have head_dim entries")
+    return qs, ks
 
 
-def _rows_out(out, like, name: str):
-    """The caller's output rows (checked), or None for a new tensor."""
-    if out is not None:
-        _rows(**{name: out})
-        if out.shape != like.shape or out.device != like.device:
-            raise ValueError(f"{name} must be shaped like its input, on the same device")
-    return out
+def _norm_rope_device(q, k, positions, cos_sin, q_weight, k_weight) -> int:
+    """The GPU that all the tensors are on."""
+    index = q.get_device()
+    if not (index >= 0 and k.get_device() == index and positions.get_device() == index
+            and cos_sin.get_device() == index
+            and (q_weight is None or q_weight.get_device() == index)
+            and (k_weight is None or k_weight.get_device() == index)):
+        named = {"q": q, "k": k, "positions": positions, "cos_sin": cos_sin,
+                 "q_weight": q_weight, "k_weight": k_weight}
+        _refuse_device(**{n: t for n, t in named.items() if t is not None})
+    return index
 
 
-def _opt(t):
-    return None if t is None else t.data_ptr()
+def _check_rows_out(out, like, name: str) -> int:
+    """The caller's output rows; their token stride."""
+    _rows(**{name: out})
+    if out.shape != like.shape or out.device != like.device:
+        raise ValueError(f"{name} must be shaped like its input, on the same device")
+    return _row_stride(out)
 
 
 def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -598,24 +633,32 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps: fl
     strided; no norm where the weight [D] is None), then the position rotation by
     cos_sin[positions] (float32 [max_position, rotary_dim]: cosines, then sines).
     Returns (q_out, k_out); either may be given, and may be its own input."""
-    named = _norm_rope_args(q, k, positions, cos_sin, q_weight, k_weight)
-    _rows_out(q_out, q, "q_out")
-    _rows_out(k_out, k, "k_out")
-    dev = _one_device(**named)
-    lib = load()
+    if q_out is not None:
+        qos = _check_rows_out(q_out, q, "q_out")
+    if k_out is not None:
+        kos = _check_rows_out(k_out, k, "k_out")
+    qs, ks = _check_norm_rope(q, k, positions, cos_sin, q_weight, k_weight)
+    index = _norm_rope_device(q, k, positions, cos_sin, q_weight, k_weight)
+    lib = _lib or load()
     t, hq, d = q.shape
     hkv = k.shape[1]
-    with _On(dev, stream) as st:
+    max_position, rotary_dim = cos_sin.shape
+    ctx, st = _enter(index, stream)
+    try:
         if q_out is None:
-            q_out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=dev)
+            q_out, qos = torch.empty((t, hq, d), dtype=_BF16, device=q.device), hq * d
         if k_out is None:
-            k_out = torch.empty((t, hkv, d), dtype=torch.bfloat16, device=dev)
-        _check(lib.pkv_qk_norm_rope(
-            q_out.data_ptr(), _token_stride(q_out), k_out.data_ptr(), _token_stride(k_out),
-            q.data_ptr(), k.data_ptr(), _token_stride(q), _token_stride(k), _opt(q_weight),
-            _opt(k_weight), eps, positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0],
-            cos_sin.shape[1], 1 if interleaved else 0, t, hq, hkv, d, PKV_BF16, st),
-            "pkv_qk_norm_rope")
+            k_out, kos = torch.empty((t, hkv, d), dtype=_BF16, device=q.device), hkv * d
+        status = lib.pkv_qk_norm_rope(
+            q_out.data_ptr(), qos, k_out.data_ptr(), kos, q.data_ptr(), k.data_ptr(), qs, ks,
+            None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), eps, positions.data_ptr(),
+            cos_sin.data_ptr(), max_position, rotary_dim, 1 if interleaved else 0, t, hq, hkv, d,
+            PKV_BF16, st)
+        if status != 0:
+            raise PkvError(status, "pkv_qk_norm_rope")
+    finally:
+        _leave(ctx)
     return q_out, k_out
 
 
@@ -624,28 +667,47 @@ def qk_norm_rope_store(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_s
                        stream=None) -> torch.Tensor:
     """qk_norm_rope whose key rows go, with the value rows v [T, Hkv, D], into the caches
     [NB, bs, Hkv, D] at slot_mapping [T] (int32; negative = skip). Returns q_out."""
-    named = _norm_rope_args(q, k, positions, cos_sin, q_weight, k_weight)
-    _rows(v=v)
-    _dense(torch.bfloat16, 4, k_cache=k_cache, v_cache=v_cache)
-    _dense(torch.int32, 1, slot_mapping=slot_mapping)
+    if q_out is not None:
+        qos = _check_rows_out(q_out, q, "q_out")
+    qs, ks = _check_norm_rope(q, k, positions, cos_sin, q_weight, k_weight)
+    try:
+        vs = _row_stride(v)
+        fine = (vs >= 0 and k_cache.dtype is _BF16 and k_cache.dim() == 4
+                and k_cache.is_contiguous() and v_cache.dtype is _BF16 and v_cache.dim() == 4
+                and v_cache.is_contiguous() and slot_mapping.dtype is _I32
+                and slot_mapping.dim() == 1 and slot_mapping.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        _rows(v=v)
+        _dense(_BF16, 4, k_cache=k_cache, v_cache=v_cache)
+        _dense(_I32, 1, slot_mapping=slot_mapping)
     t, hq, d = q.shape
     nb, bs, hkv, dc = k_cache.shape
     if (v.shape != k.shape or v_cache.shape != k_cache.shape or (hkv, dc) != k.shape[1:]
             or slot_mapping.shape[0] != t):
         raise ValueError("shape mismatch between k/v/caches/slot_mapping")
-    _rows_out(q_out, q, "q_out")
-    dev = _one_device(v=v, k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping, **named)
-    lib = load()
-    with _On(dev, stream) as st:
+    index = _norm_rope_device(q, k, positions, cos_sin, q_weight, k_weight)
+    if not (v.get_device() == index and k_cache.get_device() == index
+            and v_cache.get_device() == index and slot_mapping.get_device() == index):
+        _refuse_device(q=q, v=v, k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping)
+    lib = _lib or load()
+    ctx, st = _enter(index, stream)
+    try:
         if q_out is None:
-            q_out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=dev)
-        _check(lib.pkv_qk_norm_rope_store(
-            q_out.data_ptr(), _token_stride(q_out), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            _token_stride(q), _token_stride(k), _token_stride(v), _opt(q_weight), _opt(k_weight),
-            eps, positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
-            1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(),
-            slot_mapping.data_ptr(), t, hq, hkv, d, bs, nb, PKV_BF16, st),
-            "pkv_qk_norm_rope_store")
+            q_out, qos = torch.empty((t, hq, d), dtype=_BF16, device=q.device), hq * d
+        max_position, rotary_dim = cos_sin.shape
+        status = lib.pkv_qk_norm_rope_store(
+            q_out.data_ptr(), qos, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+            None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), eps, positions.data_ptr(),
+            cos_sin.data_ptr(), max_position, rotary_dim, 1 if interleaved else 0,
+            k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), t, hq, hkv, d, bs,
+            nb, PKV_BF16, st)
+        if status != 0:
+            raise PkvError(status, "pkv_qk_norm_rope_store")
+    finally:
+        _leave(ctx)
     return q_out
 
 
@@ -666,41 +728,64 @@ def plan_slots(context_lens, new_lens, block_tables, free_blocks, free_cursor, b
     to its context_lens[i] cached ones; blocks it lacks are taken from free_blocks [F] at
     free_cursor [1] and entered in its row of block_tables [S, MB] (updated in place).
     Rows behind the last new token, up to max_tokens, get slot -1 and position 0.
-    ``out`` may hold the buffers of an earlier plan of the same sizes."""
-    _dense(torch.int32, 1, context_lens=context_lens, new_lens=new_lens, free_blocks=free_blocks,
-           free_cursor=free_cursor)
-    _dense(torch.int32, 2, block_tables=block_tables)
+    ``out`` may hold the buffers of an earlier plan of the same sizes. The new tensors
+    are parts of one buffer."""
+    try:
+        fine = (context_lens.dtype is _I32 and context_lens.dim() == 1
+                and context_lens.is_contiguous() and new_lens.dtype is _I32
+                and new_lens.dim() == 1 and new_lens.is_contiguous()
+                and free_blocks.dtype is _I32 and free_blocks.dim() == 1
+                and free_blocks.is_contiguous() and free_cursor.dtype is _I32
+                and free_cursor.dim() == 1 and free_cursor.is_contiguous()
+                and block_tables.dtype is _I32 and block_tables.dim() == 2
+                and block_tables.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        _dense(_I32, 1, context_lens=context_lens, new_lens=new_lens, free_blocks=free_blocks,
+               free_cursor=free_cursor)
+        _dense(_I32, 2, block_tables=block_tables)
     s, mb = block_tables.shape
     if context_lens.shape[0] != s or new_lens.shape[0] != s or free_cursor.shape[0] != 1:
         raise ValueError("one length and one block table row per request, and one cursor")
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    named = dict(context_lens=context_lens, new_lens=new_lens, block_tables=block_tables,
-                 free_blocks=free_blocks, free_cursor=free_cursor)
-    sizes = (max_tokens, max_tokens, s + 1, s + 1, s, 1)
+    index = context_lens.get_device()
+    if not (index >= 0 and new_lens.get_device() == index and block_tables.get_device() == index
+            and free_blocks.get_device() == index and free_cursor.get_device() == index):
+        _dense_out_plan(out, max_tokens, s)
+        _refuse_device(context_lens=context_lens, new_lens=new_lens, block_tables=block_tables,
+                       free_blocks=free_blocks, free_cursor=free_cursor)
     if out is not None:
-        for name, t, n in zip(SlotPlan._fields, out, sizes):
-            _dense(torch.int32, 1, **{f"out.{name}": t})
-            if t.shape[0] != n:
-                raise ValueError(f"out.{name} must have {n} entries")
-            named[f"out.{name}"] = t
-    dev = _one_device(**named)
-    lib = load()
-    with _On(dev, stream) as st:
+        _dense_out_plan(out, max_tokens, s)
+        if any(t.get_device() != index for t in out):
+            _refuse_device(context_lens=context_lens,
+                           **{f"out.{n}": t for n, t in zip(SlotPlan._fields, out)})
+    lib = _lib or load()
+    ctx, st = _enter(index, stream)
+    try:
         if out is None:
-            # one buffer, each part on a 16-byte boundary of its own
-            at = [0]
-            for n in sizes:
-                at.append(at[-1] + (n + 3) // 4 * 4)
-            buf = torch.empty(at[-1], dtype=torch.int32, device=dev)
-            out = SlotPlan(*(buf[a:a + n] for a, n in zip(at, sizes)))
+            buf = torch.empty(2 * max_tokens + 3 * s + 3, dtype=_I32, device=context_lens.device)
+            out = SlotPlan(*buf.split_with_sizes((max_tokens, max_tokens, s + 1, s + 1, s, 1)))
         slots, pos, cu_q, cu_k, lens, cursor = out
         _check(lib.pkv_plan_slots(
             context_lens.data_ptr(), new_lens.data_ptr(), s, block_tables.data_ptr(), mb,
             free_blocks.data_ptr(), free_blocks.shape[0], free_cursor.data_ptr(),
             cursor.data_ptr(), slots.data_ptr(), pos.data_ptr(), max_tokens, cu_q.data_ptr(),
             cu_k.data_ptr(), lens.data_ptr(), block_size, num_blocks, st), "pkv_plan_slots")
+    finally:
+        _leave(ctx)
     return out
+
+
+def _dense_out_plan(out, max_tokens: int, s: int):
+    """The caller's plan buffers."""
+    if out is None:
+        return
+    for name, t, n in zip(SlotPlan._fields, out, (max_tokens, max_tokens, s + 1, s + 1, s, 1)):
+        _need(t, f"out.{name}", _I32, 1, contiguous=True, on_gpu=False)
+        if t.shape[0] != n:
+            raise ValueError(f"out.{name} must have {n} entries")
 
 
 def tree_masks(parents, cu_seqlens_q, context_lens, max_seqlen_q: int, tree_mask=None,
@@ -708,33 +793,46 @@ def tree_masks(parents, cu_seqlens_q, context_lens, max_seqlen_q: int, tree_mask
     """Ancestor masks and positions of drafted trees: parents [total_q] holds each node's
     parent in its own tree (an earlier node, or -1). Returns (tree_mask [total_q, W] int32
     with W = ceil(max_seqlen_q / 32) or the given tensor's width, positions [total_q])."""
-    _dense(torch.int32, 1, parents=parents, cu_seqlens_q=cu_seqlens_q, context_lens=context_lens)
+    try:
+        fine = (parents.dtype is _I32 and parents.dim() == 1 and parents.is_contiguous()
+                and cu_seqlens_q.dtype is _I32 and cu_seqlens_q.dim() == 1
+                and cu_seqlens_q.is_contiguous() and context_lens.dtype is _I32
+                and context_lens.dim() == 1 and context_lens.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        _dense(_I32, 1, parents=parents, cu_seqlens_q=cu_seqlens_q, context_lens=context_lens)
     total, s = parents.shape[0], context_lens.shape[0]
     if cu_seqlens_q.shape[0] != s + 1:
         raise ValueError("cu_seqlens_q must have one entry more than context_lens")
-    named = dict(parents=parents, cu_seqlens_q=cu_seqlens_q, context_lens=context_lens)
+    named = {"parents": parents, "cu_seqlens_q": cu_seqlens_q, "context_lens": context_lens}
     if tree_mask is not None:
-        _dense(torch.int32, 2, tree_mask=tree_mask)
+        _dense(_I32, 2, tree_mask=tree_mask)
         if tree_mask.shape[0] != total:
             raise ValueError("tree_mask must have one row per node")
         named["tree_mask"] = tree_mask
     if positions is not None:
-        _dense(torch.int32, 1, positions=positions)
+        _dense(_I32, 1, positions=positions)
         if positions.shape[0] != total:
             raise ValueError("positions must have one entry per node")
         named["positions"] = positions
-    dev = _one_device(**named)
-    lib = load()
-    with _On(dev, stream) as st:
+    index = parents.get_device()
+    if index < 0 or any(t.get_device() != index for t in named.values()):
+        _refuse_device(**named)
+    lib = _lib or load()
+    ctx, st = _enter(index, stream)
+    try:
         if tree_mask is None:
             words = max(0, int(max_seqlen_q) + 31) // 32
-            tree_mask = torch.empty((total, words), dtype=torch.int32, device=dev)
+            tree_mask = torch.empty((total, words), dtype=_I32, device=parents.device)
         if positions is None:
-            positions = torch.empty(total, dtype=torch.int32, device=dev)
+            positions = torch.empty(total, dtype=_I32, device=parents.device)
         _check(lib.pkv_tree_masks(
             parents.data_ptr(), cu_seqlens_q.data_ptr(), context_lens.data_ptr(), s, total,
             int(max_seqlen_q), tree_mask.data_ptr(), tree_mask.shape[1], positions.data_ptr(),
             st), "pkv_tree_masks")
+    finally:
+        _leave(ctx)
     return tree_mask, positions
 
 
@@ -751,42 +849,67 @@ def tree_decode(q, key, value, k_cache, v_cache, block_tables, context_lens, cu_
     cached tokens and the drafted rows key / value [total_q, Hkv, 128] (token rows may be
     strided; not written to the cache) whose bit is set in tree_mask [total_q, W].
     Returns out [total_q, Hq, 128] bf16; rows behind cu_seqlens_q[-1] are not written."""
-    _dense(torch.bfloat16, 3, q=q)
-    _rows(key=key, value=value)
-    _dense(torch.bfloat16, 4, k_cache=k_cache, v_cache=v_cache)
-    _dense(torch.int32, 2, block_tables=block_tables, tree_mask=tree_mask)
-    _dense(torch.int32, 1, context_lens=context_lens, cu_seqlens_q=cu_seqlens_q)
+    try:
+        ks, vs = _row_stride(key), _row_stride(value)
+        fine = (q.dtype is _BF16 and q.dim() == 3 and q.is_contiguous() and ks >= 0 and vs >= 0
+                and k_cache.dtype is _BF16 and k_cache.dim() == 4
+                and k_cache.is_contiguous() and v_cache.dtype is _BF16 and v_cache.dim() == 4
+                and v_cache.is_contiguous() and block_tables.dtype is _I32
+                and block_tables.dim() == 2 and block_tables.is_contiguous()
+                and tree_mask.dtype is _I32 and tree_mask.dim() == 2
+                and tree_mask.is_contiguous() and context_lens.dtype is _I32
+                and context_lens.dim() == 1 and context_lens.is_contiguous()
+                and cu_seqlens_q.dtype is _I32 and cu_seqlens_q.dim() == 1
+                and cu_seqlens_q.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        _dense(_BF16, 3, q=q)
+        _rows(key=key, value=value)
+        _dense(_BF16, 4, k_cache=k_cache, v_cache=v_cache)
+        _dense(_I32, 2, block_tables=block_tables, tree_mask=tree_mask)
+        _dense(_I32, 1, context_lens=context_lens, cu_seqlens_q=cu_seqlens_q)
     total, hq, d = q.shape
     nb, bs, hkv, dc = k_cache.shape
     s = context_lens.shape[0]
     if dc != d or v_cache.shape != k_cache.shape:
         raise ValueError("q / cache head_dim mismatch")
-    if key.shape != (total, hkv, d) or value.shape != (total, hkv, d):
+    rows = (total, hkv, d)
+    if key.shape != rows or value.shape != rows:
         raise ValueError("key / value must be [total_q, Hkv, D]")
-    if (block_tables.shape[0] != s or cu_seqlens_q.shape[0] != s + 1
-            or tree_mask.shape[0] != total):
+    tables, mb = block_tables.shape
+    masks, words = tree_mask.shape
+    if tables != s or cu_seqlens_q.shape[0] != s + 1 or masks != total:
         raise ValueError("metadata shape mismatch")
-    dev = _one_device(q=q, key=key, value=value, k_cache=k_cache, v_cache=v_cache,
-                      block_tables=block_tables, context_lens=context_lens,
-                      cu_seqlens_q=cu_seqlens_q, tree_mask=tree_mask)
-    mb = block_tables.shape[1]
+    index = q.get_device()
+    if not (index >= 0 and key.get_device() == index and value.get_device() == index
+            and k_cache.get_device() == index and v_cache.get_device() == index
+            and block_tables.get_device() == index and context_lens.get_device() == index
+            and cu_seqlens_q.get_device() == index and tree_mask.get_device() == index):
+        _refuse_device(q=q, key=key, value=value, k_cache=k_cache, v_cache=v_cache,
+                       block_tables=block_tables, context_lens=context_lens,
+                       cu_seqlens_q=cu_seqlens_q, tree_mask=tree_mask)
     if max_context_len is None:
         max_context_len = mb * bs
-    lib = load()
-    with _On(dev, stream) as st:
-        out = _out_like(out, q)
+    lib = _lib or load()
+    ctx, st = _enter(index, stream)
+    try:
+        out = _out_like(out, q) if out is not None else torch.empty(q.shape, dtype=_BF16,
+                                                                    device=q.device)
         if workspace is None:
             need = lib.pkv_tree_decode_workspace_size(max_seqlen_q, hq, hkv, d)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        elif workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous, on q's device")
         _check(lib.pkv_tree_decode(
-            out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(), _token_stride(key),
-            _token_stride(value), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-            mb, context_lens.data_ptr(), cu_seqlens_q.data_ptr(), tree_mask.data_ptr(),
-            tree_mask.shape[1], s, total, int(max_seqlen_q), int(max_context_len), hq, hkv, d, bs,
-            nb, scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            PKV_BF16, st), "pkv_tree_decode")
+            out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(), ks, vs,
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            mb, context_lens.data_ptr(), cu_seqlens_q.data_ptr(), tree_mask.data_ptr(), words, s,
+            total, int(max_seqlen_q), int(max_context_len), hq, hkv, d, bs, nb, scale,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), PKV_BF16, st),
+            "pkv_tree_decode")
+    finally:
+        _leave(ctx)
     return out
 
 

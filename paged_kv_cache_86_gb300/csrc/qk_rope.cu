@@ -26,6 +26,7 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kWarpsPerSm = 32;
 
 struct Chunk {
   float v[8];
@@ -172,9 +173,21 @@ void launch(const QkRopeArgs &a, unsigned grid, cudaStream_t stream) {
 
 cudaError_t launch_qk_rope(QkRopeArgs a, int head_dim, cudaStream_t stream) {
   if (a.num_tokens == 0) return cudaSuccess;
-  a.parts = 1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  // With few tokens a token's rows are spread over up to one warp a pass, until
+  // kWarpsPerSm warps an SM are busy; with many, a warp takes all the rows of its
+  // token and loads its angles once.
+  const int rows = a.num_q_heads + (a.v != nullptr ? 2 : 1) * a.num_kv_heads;
+  const int passes = (rows + 512 / head_dim - 1) / (512 / head_dim);
+  const int64_t want = static_cast<int64_t>(sm_count(dev)) * kWarpsPerSm;
+  int64_t parts = want / a.num_tokens;
+  parts = parts < 1 ? 1 : parts > passes ? passes : parts;
+  a.parts = static_cast<int>(parts);
   const int64_t warps = static_cast<int64_t>(a.num_tokens) * a.parts;
   const unsigned grid = static_cast<unsigned>((warps + kWarps - 1) / kWarps);
+  if (warps > (static_cast<int64_t>(1) << 33)) return cudaErrorInvalidValue;
   if (head_dim == 64) launch<64>(a, grid, stream);
   else if (head_dim == 128) launch<128>(a, grid, stream);
   else launch<256>(a, grid, stream);
