@@ -39,12 +39,13 @@
 // core's operand type asks for. O is rescaled only when a row's maximum grows by
 // over 2^8.
 //
-// Loads (warps 8 and 10): whole tiles of blocks that are a multiple of 8 rows
-// by TMA boxes; partial tiles, other block sizes and the drafts by TMA row
-// gathers (four rows an instruction), which put zeros where a tile has no key,
-// so no stale cache row ever meets an MMA. Drafted V rows a query row must not
-// see may hold anything: their values that are not finite are set to zero in
-// shared memory and added back at the end for the rows that do see them.
+// Loads (warp 8 K, warp 10 V, warp 11 Q and the walk): TMA boxes when the block size is a multiple of 8 (whole
+// tiles in boxes of up to a block, partial tiles and drafts in boxes of 8 rows),
+// else TMA row gathers, four rows an instruction. Rows of a tile that are no key
+// of the sequence may be other rows of a block or other sequences' drafts, and
+// drafts that a row does not see may hold anything: their scores are masked, and
+// V values among them that are not finite are set to zero in shared memory (0 * NaN
+// is not 0), those of drafts to be added back at the end for the rows that see them.
 //
 // Every wait is bounded; on a timeout the CTA records PKV_DEVERR_TIMEOUT,
 // drains its copies and MMAs, frees its TMEM and exits.
@@ -69,12 +70,12 @@ constexpr int kTileBytes = 2 * kRegion;
 constexpr int kKStages = 2;
 constexpr int kVStages = 3;
 constexpr int kThreads = 384;        // softmax 0 (warps 0-3), softmax 1 (4-7), loaders + MMA (8-11)
-constexpr int kWarpK = 8, kWarpMma = 9, kWarpV = 10;
+constexpr int kWarpK = 8, kWarpMma = 9, kWarpV = 10, kWarpWalk = 11;
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.f;
 constexpr int kSegRing = 4;
-constexpr int kSegReaders = 1 + 1 + 8;   // V loader, MMA issuer, softmax warps
+constexpr int kSegReaders = 2 + 1 + 8;   // K and V loaders, MMA issuer, softmax warps
 
 constexpr int kOffMl = 0;                               // float2[128]
 constexpr int kOffSeg = kOffMl + kTile * 8;
@@ -90,7 +91,7 @@ constexpr int kOffV = kOffK + kKStages * kTileBytes;
 constexpr int kSmemBytes = kOffV + kVStages * kTileBytes;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
-// One CTA's part of one stream, handed from the K loader to the other roles.
+// One CTA's part of one stream, handed from the walking warp to the other roles.
 struct Seg {
   int head;     // KV head; -1 ends the walk
   int ctx;      // cached tokens of the sequence
@@ -103,7 +104,7 @@ struct Seg {
   int slot;     // partial record, -1: the whole stream is here
   int step0;    // its first step
   int qtile;    // running number of its first Q tile
-  int bad;      // set when a drafted V value was not finite
+  int bad;      // set when a drafted V value was not finite (seen or not)
 };
 static_assert(sizeof(Seg) <= kSegBytes, "segment ring entry");
 
@@ -154,27 +155,27 @@ __device__ __forceinline__ float ex2(float x) {
 
 // The keys of tile j of a stream: cached rows [128 j, 128 j + cached) in rows
 // 0 .. of the tile, then drafts [u0, u0 + drafts) from row `at` (a multiple of
-// 4) on; rows 0 .. rows - 1 are loaded (a multiple of 16).
+// 8) on; rows 0 .. rows - 1 are loaded (a multiple of 16).
 struct TileKeys {
   int cached, at, u0, drafts, rows;
 };
 
 __device__ __forceinline__ int tree_tiles(int ctx, int drafts) {
   const int full = ctx / kTile, rem = ctx % kTile;
-  if (((rem + 3) & ~3) + drafts <= kTile) return full + 1;
+  if (((rem + 7) & ~7) + drafts <= kTile) return full + 1;
   return full + (rem > 0 ? 1 : 0) + (drafts + kTile - 1) / kTile;
 }
 
 __device__ __forceinline__ TileKeys tile_keys(int ctx, int drafts, int j) {
-  const int full = ctx / kTile, rem = ctx % kTile, rem4 = (rem + 3) & ~3;
+  const int full = ctx / kTile, rem = ctx % kTile, rem8 = (rem + 7) & ~7;
   TileKeys k;
   k.at = k.u0 = k.drafts = 0;
   k.cached = kTile;
   k.rows = kTile;
   if (j < full) return k;
-  if (rem4 + drafts <= kTile) {
+  if (rem8 + drafts <= kTile) {
     k.cached = rem;
-    k.at = rem4;
+    k.at = rem8;
     k.drafts = drafts;
   } else if (rem > 0 && j == full) {
     k.cached = rem;
@@ -313,8 +314,8 @@ __device__ __forceinline__ bool seq_lengths(const TreeParams &p, int i, int *ctx
 
 __global__ void __launch_bounds__(kThreads, 1)
 tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kg,
-                   const __grid_constant__ CUtensorMap tm_vg, const __grid_constant__ CUtensorMap tm_kd,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kp,
+                   const __grid_constant__ CUtensorMap tm_vp, const __grid_constant__ CUtensorMap tm_kd,
                    const __grid_constant__ CUtensorMap tm_vd, const TreeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw;
@@ -413,7 +414,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int before = 0, total = 0;
+  int before = 0, total = 0;   // tiles before this thread's and of all sequences
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     const int v = part[w];
@@ -422,15 +423,22 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   }
   // range b is [floor(b * units / ctas), floor((b + 1) * units / ctas)), so that
   // with num_kv_heads | ctas every head is cut at the same tiles; no range is empty
+  total = uniform(total);
   const int units = total * p.num_kv_heads;
   const int ctas = min(static_cast<int>(gridDim.x), max(units, 1));
   const int bid = static_cast<int>(blockIdx.x);
-  auto range_lo = [&](int b) {
-    return static_cast<int>(static_cast<long long>(min(b, ctas)) * units / ctas);
+  const int per_cta = units / ctas, extra = units - per_cta * ctas;
+  auto range_lo = [&](int b) {   // floor(b * units / ctas)
+    b = min(b, ctas);
+    return b * per_cta + b * extra / ctas;
   };
-  // the range that tile f lies in
-  auto range_of = [&](int f) {
-    return static_cast<int>(((static_cast<long long>(f) + 1) * ctas - 1) / units);
+  auto range_of = [&](int f) {   // the range that tile f lies in
+    int a = 0, b = ctas - 1;
+    while (a < b) {
+      const int m = (a + b + 1) >> 1;
+      if (range_lo(m) <= f) a = m; else b = m - 1;
+    }
+    return a;
   };
   const int lo = range_lo(bid), hi = range_lo(bid + 1);
   const int off0 = lo < hi ? lo % total : -1;   // the range starts at this tile of its head
@@ -487,42 +495,39 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
   if (warp >= 8) {
     if (warp == kWarpK || warp == kWarpV) {
-      // ------------------------------------------------------------- loaders
+      // ---------------------------------------------------- K and V loaders
+      // (one copy of the code for both warps)
       const bool is_k = warp == kWarpK;
       const int stages = is_k ? kKStages : kVStages;
-      const CUtensorMap *map_box = is_k ? &tm_k : &tm_v;
-      const CUtensorMap *map_rows = is_k ? &tm_kg : &tm_vg;
+      const uint32_t full0 = is_k ? k_full(0) : v_full(0), empty0 = is_k ? k_empty(0) : v_empty(0);
+      const uint32_t dst0 = is_k ? sK(0) : sV(0);
+      const CUtensorMap *map_whole = is_k ? &tm_k : &tm_v;
+      const CUtensorMap *map_part = is_k ? &tm_kp : &tm_vp;
       const CUtensorMap *map_draft = is_k ? &tm_kd : &tm_vd;
       const int oob_row = p.num_blocks * p.block_size;
-      int issued = 0;
+      const bool boxes = p.box_rows > 0;
+      int issued = 0, stage = 0, parity = 1;   // the first round finds every stage empty
       bool ok = true;
       if (lane == 0) {
-        tma_prefetch_desc(map_box);
-        tma_prefetch_desc(map_rows);
+        tma_prefetch_desc(map_whole);
+        tma_prefetch_desc(map_part);
         tma_prefetch_desc(map_draft);
-        if (is_k) tma_prefetch_desc(&tm_q);
       }
-      // one key tile of a segment into the next stage
-      auto load_tile = [&](const Seg &sg, int j) -> bool {
-        const TileKeys tk = tile_keys(sg.ctx, sg.drafts, j);
+      Seg sg;
+      for (int n = 0; ok; ++n) {
+        ok = read_seg(n, sg);
+        if (!ok) break;
+        seg_done(n);
+        if (sg.head < 0) break;
         const int32_t *bt = p.block_tables + static_cast<int64_t>(sg.seq) * p.max_blocks_per_seq;
-        auto cache_row = [&](int key) {
-          const int blk = __ldg(bt + key / p.block_size);
-          if (blk >= 0 && blk < p.num_blocks) return blk * p.block_size + key % p.block_size;
-          if (is_k) raise_error(p.err, PKV_DEVERR_BLOCK_ID);
-          return oob_row;
-        };
-        const int s = issued % stages, round = issued / stages;
-        const uint32_t full = is_k ? k_full(s) : v_full(s);
-        uint32_t dst = is_k ? sK(s) : sV(s);
-        int4 r = make_int4(oob_row, oob_row, oob_row, oob_row);
-        const bool boxes = p.box_rows > 0 && tk.cached == kTile;
-        if (boxes) {
-          // lane l holds the row of piece l
-          if (lane < kTile / p.box_rows) r.x = cache_row(j * kTile + lane * p.box_rows);
-        } else {
-          // lane l holds the four rows from row 4 l of the tile on
-          const int k0 = 4 * lane;
+#pragma unroll 1
+        for (int j = sg.t0; j < sg.t1; ++j) {
+          const TileKeys tk = tile_keys(sg.ctx, sg.drafts, j);
+          // lane l holds the first row of the tile's l-th box, or the four rows of its
+          // l-th gather
+          const int step = !boxes ? 4 : tk.cached == kTile ? p.box_rows : 8;   // rows a copy
+          const int k0 = step * lane;
+          int4 r = make_int4(oob_row, oob_row, oob_row, oob_row);
           if (tk.drafts > 0 && k0 >= tk.at) {
             const int u = k0 - tk.at, first = sg.q0 + tk.u0;
             r.x = u < tk.drafts ? first + u : p.total_q;
@@ -530,59 +535,77 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             r.z = u + 2 < tk.drafts ? first + u + 2 : p.total_q;
             r.w = u + 3 < tk.drafts ? first + u + 3 : p.total_q;
           } else {
-            const int key = j * kTile + k0;
-            if (k0 < tk.cached) r.x = cache_row(key);
-            if (k0 + 1 < tk.cached) r.y = cache_row(key + 1);
-            if (k0 + 2 < tk.cached) r.z = cache_row(key + 2);
-            if (k0 + 3 < tk.cached) r.w = cache_row(key + 3);
-          }
-        }
-        if (round > 0 && !warp_wait(is_k ? k_empty(s) : v_empty(s), (round - 1) & 1, abort_flag)) {
-          fail();
-          return false;
-        }
-        if (elect_one()) mbar_arrive_expect_tx(full, tk.rows * kHD * 2);
-        if (boxes) {
 #pragma unroll 1
-          for (int b = 0; b < kTile / p.box_rows; ++b) {
-            const int row = __shfl_sync(0xffffffffu, r.x, b);
-            if (elect_one()) {
-              tma_load_3d(dst, map_box, 0, sg.head, row, full);
-              tma_load_3d(dst + kRegion, map_box, 64, sg.head, row, full);
+            for (int e = (boxes ? 1 : 4) - 1; e >= 0; --e) {   // r.x last
+              r.w = r.z;
+              r.z = r.y;
+              r.y = r.x;
+              r.x = oob_row;
+              const int key = j * kTile + k0 + e;
+              if (k0 + e < tk.cached) {
+                const int blk = __ldg(bt + key / p.block_size);
+                if (blk >= 0 && blk < p.num_blocks)
+                  r.x = blk * p.block_size + key % p.block_size;
+                else if (is_k)
+                  raise_error(p.err, PKV_DEVERR_BLOCK_ID);
+              }
             }
-            dst += p.box_rows * 128;
           }
-        } else {
+          ok = warp_wait(empty0 + 8 * stage, parity, abort_flag);
+          if (!ok) break;
+          const uint32_t full = full0 + 8 * stage;
+          uint32_t dst = dst0 + stage * kTileBytes;
+          if (elect_one()) mbar_arrive_expect_tx(full, tk.rows * kHD * 2);
+          const int first_draft = tk.drafts > 0 ? tk.at : kTile;
 #pragma unroll 1
-          for (int b = 0; b < tk.rows / 4; ++b) {
+          for (int b = 0; b * step < tk.rows; ++b) {
+            const CUtensorMap *map =
+                b * step >= first_draft ? map_draft : tk.cached == kTile ? map_whole : map_part;
             int4 q;
             q.x = __shfl_sync(0xffffffffu, r.x, b);
             q.y = __shfl_sync(0xffffffffu, r.y, b);
             q.z = __shfl_sync(0xffffffffu, r.z, b);
             q.w = __shfl_sync(0xffffffffu, r.w, b);
-            const CUtensorMap *map = tk.drafts > 0 && 4 * b >= tk.at ? map_draft : map_rows;
             if (elect_one()) {
-              tma_gather4(dst, map, sg.head * kHD, q, full);
-              tma_gather4(dst + kRegion, map, sg.head * kHD + 64, q, full);
+              if (boxes) {
+                tma_load_3d(dst, map, 0, sg.head, q.x, full);
+                tma_load_3d(dst + kRegion, map, 64, sg.head, q.x, full);
+              } else {
+                tma_gather4(dst, map, sg.head * kHD, q, full);
+                tma_gather4(dst + kRegion, map, sg.head * kHD + 64, q, full);
+              }
             }
-            dst += 512;
+            dst += step * 128;
+          }
+          ++issued;
+          if (++stage == stages) {
+            stage = 0;
+            parity ^= 1;
           }
         }
-        ++issued;
-        return true;
-      };
-      if (is_k) {
-        // walk the range: streams of (head, sequence, row group)
-        int qtiles = 0, q_issued = 0, step = 0, n = 0;
-        int left = hi - lo;
-        int head = left > 0 ? lo / total : 0, seq = left > 0 ? start[0] : 0;
-        int off = left > 0 ? start[1] : 0;       // tile inside the sequence's row groups
-        int seq_base = -32, c_ctx = 0, c_drafts = 0, c_q0 = 0;  // 32 sequences' lengths, one a lane
-        Boundary bd;
-        bd.row0 = -1;
-        bd.ntok = bd.head = bd.first = bd.last = 0;
-        bool first_seg = true;
-        while (ok && left > 0) {
+      }
+      if (!ok) fail();
+      for (int j = max(0, issued - stages); j < issued; ++j)   // the last copies must land
+        warp_wait(full0 + 8 * (j % stages), (j / stages) & 1, never);
+    } else if (warp == kWarpWalk) {
+      // ---------------------------------------- the walk, and the Q tiles
+      int qtiles = 0, q_issued = 0, step = 0, n = 0;
+      bool ok = true;
+      int left = hi - lo;
+      int head = left > 0 ? lo / total : 0, seq = uniform(left > 0 ? start[0] : 0);
+      int off = uniform(left > 0 ? start[1] : 0);   // tile inside the sequence's row groups
+      int seq_base = -32, c_ctx = 0, c_drafts = 0, c_q0 = 0;  // 32 sequences' lengths, one a lane
+      Boundary bd;
+      bd.row0 = -1;
+      bd.ntok = bd.head = bd.first = bd.last = 0;
+      bool first_seg = true;
+      if (lane == 0) tma_prefetch_desc(&tm_q);
+      // the end of the walk is one more ring entry
+      for (bool more = true; ok && more;) {
+        Seg sg = {};
+        int nt = 0;
+        more = left > 0;
+        if (more) {
           if (seq >= p.num_seqs) {               // on to the next KV head
             seq = 0;
             ++head;
@@ -593,214 +616,163 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (seq_base + lane < p.num_seqs)
               seq_lengths(p, seq_base + lane, &c_ctx, &c_drafts, &c_q0);
           }
-          Seg sg;
           sg.ctx = __shfl_sync(0xffffffffu, c_ctx, seq - seq_base);
           sg.drafts = __shfl_sync(0xffffffffu, c_drafts, seq - seq_base);
           sg.q0 = __shfl_sync(0xffffffffu, c_q0, seq - seq_base);
-          if (sg.drafts == 0) {
+          nt = sg.drafts == 0 ? 0 : tree_tiles(sg.ctx, sg.drafts);
+          const int groups = (sg.drafts + pair_tokens - 1) / pair_tokens;
+          if (off >= nt * groups) {              // the sequence is done (or has no drafts)
             ++seq;
+            off = 0;
             continue;
           }
-          const int nt = tree_tiles(sg.ctx, sg.drafts);
-          const int groups = (sg.drafts + pair_tokens - 1) / pair_tokens;
-          int rg = off / nt;
+        }
+        bool two = false;
+        if (more) {
+          const int rg = off / nt;
           sg.t0 = off - rg * nt;
-          sg.head = head;
-          sg.seq = seq;
-          for (; ok && rg < groups && left > 0; ++rg) {
-            sg.t1 = min(nt, sg.t0 + left);
-            sg.tok0 = rg * pair_tokens;
-            sg.ntok = min(pair_tokens, sg.drafts - sg.tok0);
-            const bool two = sg.ntok > p.tile_tokens;
-            sg.slot = (sg.t0 == 0 && sg.t1 == nt) ? -1
-                      : 2 * bid + (sg.t0 == 0 ? 1 : 0);
-            if (two) step = (step + 1) & ~1;     // row tile x in region x
-            sg.step0 = step;
-            sg.qtile = qtiles;
-            const int tiles = sg.t1 - sg.t0;
-            step += two ? 2 * tiles : tiles;
-            // the stream that the range start cuts is merged at its first cut
-            if (first_seg && sg.t0 > 0 && range_of(lo - sg.t0) == bid - 1) {
-              bd.row0 = sg.q0 + sg.tok0;
-              bd.ntok = sg.ntok;
-              bd.head = head;
-              bd.first = bid - 1;
-              bd.last = range_of(lo - sg.t0 + nt - 1);
-            }
-            first_seg = false;
-            if (n >= kSegRing &&
-                !warp_wait(seg_empty(n % kSegRing), ((n / kSegRing) - 1) & 1, abort_flag)) {
-              fail();
-              ok = false;
-              break;
-            }
-            if (lane == 0) {
-              volatile Seg *v = seg_at(n);
-              v->head = sg.head;
-              v->ctx = sg.ctx;
-              v->drafts = sg.drafts;
-              v->q0 = sg.q0;
-              v->seq = sg.seq;
-              v->tok0 = sg.tok0;
-              v->ntok = sg.ntok;
-              v->t0 = sg.t0;
-              v->t1 = sg.t1;
-              v->slot = sg.slot;
-              v->step0 = sg.step0;
-              v->qtile = sg.qtile;
-              v->bad = 0;
-              mbar_arrive(seg_full(n % kSegRing));
-            }
-            __syncwarp();
-            // Q tiles: box_tokens * group rows a box
-            for (int x = 0; x < (two ? 2 : 1); ++x) {
-              const int s = (qtiles + x) & 1, round = (qtiles + x) >> 1;
-              if (round > 0 && !warp_wait(q_empty(s), (round - 1) & 1, abort_flag)) {
-                fail();
-                ok = false;
-                break;
-              }
-              const int tok = min(p.tile_tokens, sg.ntok - x * p.tile_tokens);
-              const int boxes = (tok + p.box_tokens - 1) / p.box_tokens;
-              const int box_rows = p.box_tokens * p.group;
-              if (elect_one()) mbar_arrive_expect_tx(q_full(s), boxes * box_rows * kHD * 2);
+          sg.t1 = min(nt, sg.t0 + left);
+          sg.tok0 = rg * pair_tokens;
+          sg.ntok = min(pair_tokens, sg.drafts - sg.tok0);
+          two = sg.ntok > p.tile_tokens;
+          sg.slot = (sg.t0 == 0 && sg.t1 == nt) ? -1 : 2 * bid + (sg.t0 == 0 ? 1 : 0);
+          if (two) step = (step + 1) & ~1;       // row tile x in steps g with g & 1 == x
+          sg.step0 = step;
+          const int tiles = sg.t1 - sg.t0;
+          step += two ? 2 * tiles : tiles;
+          off += tiles;
+          left -= tiles;
+          // the stream that the range start cuts is merged at its first cut
+          if (first_seg && sg.t0 > 0 && range_of(lo - sg.t0) == bid - 1) {
+            bd.row0 = sg.q0 + sg.tok0;
+            bd.ntok = sg.ntok;
+            bd.head = head;
+            bd.first = bid - 1;
+            bd.last = range_of(lo - sg.t0 + nt - 1);
+          }
+          first_seg = false;
+        }
+        ok = n < kSegRing || warp_wait(seg_empty(n % kSegRing), ((n / kSegRing) - 1) & 1, abort_flag);
+        if (!ok) break;
+        if (lane == 0) {
+          volatile Seg *v = seg_at(n);
+          v->head = more ? head : -1;
+          v->ctx = sg.ctx;
+          v->drafts = sg.drafts;
+          v->q0 = sg.q0;
+          v->seq = seq;
+          v->tok0 = sg.tok0;
+          v->ntok = sg.ntok;
+          v->t0 = sg.t0;
+          v->t1 = sg.t1;
+          v->slot = sg.slot;
+          v->step0 = sg.step0;
+          v->qtile = qtiles;
+          v->bad = 0;
+          mbar_arrive(seg_full(n % kSegRing));
+        }
+        __syncwarp();
+        ++n;
+        // Q tiles: box_tokens * group rows a box
+        for (int x = 0; more && x < (two ? 2 : 1); ++x) {
+          const int s = qtiles & 1, round = qtiles >> 1;
+          ok = round == 0 || warp_wait(q_empty(s), (round - 1) & 1, abort_flag);
+          if (!ok) break;
+          const int tok = min(p.tile_tokens, sg.ntok - x * p.tile_tokens);
+          const int boxes = (tok + p.box_tokens - 1) / p.box_tokens;
+          const int box_rows = p.box_tokens * p.group;
+          if (elect_one()) mbar_arrive_expect_tx(q_full(s), boxes * box_rows * kHD * 2);
+          uint32_t dst = sQ + s * kTileBytes;
+          int row = sg.q0 + sg.tok0 + x * p.tile_tokens;
 #pragma unroll 1
-              for (int b = 0; b < boxes; ++b) {
-                const int row = sg.q0 + sg.tok0 + x * p.tile_tokens + b * p.box_tokens;
-                const uint32_t dst = sQ + s * kTileBytes + b * box_rows * 128;
-                if (elect_one()) {
-                  tma_load_3d(dst, &tm_q, 0, head * p.group, row, q_full(s));
-                  tma_load_3d(dst + kRegion, &tm_q, 64, head * p.group, row, q_full(s));
-                }
-              }
-              ++q_issued;
+          for (int b = 0; b < boxes; ++b) {
+            if (elect_one()) {
+              tma_load_3d(dst, &tm_q, 0, head * p.group, row, q_full(s));
+              tma_load_3d(dst + kRegion, &tm_q, 64, head * p.group, row, q_full(s));
             }
-            if (!ok) break;
-            ++n;
-            qtiles += two ? 2 : 1;
-            for (int j = sg.t0; ok && j < sg.t1; ++j) ok = load_tile(sg, j);
-            left -= tiles;
-            sg.t0 = 0;
+            dst += box_rows * 128;
+            row += p.box_tokens;
           }
-          ++seq;
-          off = 0;
-        }
-        if (lane == 0) p.bounds[bid] = bd;
-        if (ok) {                                // the walk's end
-          if (n >= kSegRing &&
-              !warp_wait(seg_empty(n % kSegRing), ((n / kSegRing) - 1) & 1, abort_flag)) {
-            fail();
-          } else if (lane == 0) {
-            seg_at(n)->head = -1;
-            mbar_arrive(seg_full(n % kSegRing));
-          }
-          __syncwarp();
-        }
-        for (int s = max(0, q_issued - 2); s < q_issued; ++s)   // drain
-          warp_wait(q_full(s & 1), (s >> 1) & 1, never);
-      } else {
-        Seg sg;
-        for (int n = 0; ok; ++n) {
-          if (!read_seg(n, sg)) {
-            fail();
-            break;
-          }
-          seg_done(n);
-          if (sg.head < 0) break;
-          for (int j = sg.t0; ok && j < sg.t1; ++j) ok = load_tile(sg, j);
+          ++q_issued;
+          ++qtiles;
         }
       }
-      for (int j = max(0, issued - stages); j < issued; ++j)   // the last copies must land
-        warp_wait(is_k ? k_full(j % stages) : v_full(j % stages), (j / stages) & 1, never);
+      if (lane == 0) p.bounds[bid] = bd;
+      if (!ok) fail();
+      for (int s = max(0, q_issued - 2); s < q_issued; ++s)   // drain
+        warp_wait(q_full(s & 1), (s >> 1) & 1, never);
     } else if (warp == kWarpMma) {
       // ---------------------------------------------------------- MMA issuer
-      // The warp's own instructions are on the path of every tile: one copy of the
-      // code for both x, ring positions counted up, descriptors that differ by adds.
+      // The warp's own instructions are on the path of every tile, so there are few:
+      // one copy for both x, ring positions counted up, descriptors that differ by adds.
       constexpr uint32_t idesc_s = umma_idesc_bf16(kTile, 0, false);            // N is added
       constexpr uint32_t idesc_pv = umma_idesc_bf16(kTile, kHD, true);          // B (V) MN-major
       constexpr uint32_t kTileStep = kTileBytes >> 4;
       const uint32_t tm = uniform(static_cast<int>(tmem));
       const uint64_t dq0 = desc_kmajor(sQ, 0), dk0 = desc_kmajor(sK(0), 0), dv0 = desc_v_mnmajor(sV(0));
-      struct Owed {        // the PV of an x's last step
-        int steps = 0;     // its MMAs (16 keys each); 0: none
-        int stage = 0, parity = 0;       // of the V tile
-        int segs = 0;                    // segments that have begun to overwrite O_x
-        bool fresh = false;              // the x's first PV of the segment overwrites O_x
-        bool frees = false;              // last user of the V tile
-        bool ends = false;               // the x's last PV of the segment
-        int p_parity = 0;                // of p_full(x)
-      };
-      Owed mine, other;                  // of this step's x and of the other one
-      bool ok = true;
-      int x = 0, step = 0;
-      int ks = 0, kp = 0, vs = 0, vp = 0;   // stage and parity of the next K and V tile
-      auto issue_pv = [&]() -> bool {
-        if (mine.steps == 0) return true;
-        if (!warp_wait(v_full(mine.stage), mine.parity, abort_flag) ||
-            !warp_wait(p_full(x), mine.p_parity, abort_flag))
-          return false;
-        mine.p_parity ^= 1;
-        // what the last segment left in O_x must have been read out
-        if (mine.fresh) {
-          if (mine.segs > 0 && !warp_wait(o_free(x), (mine.segs - 1) & 1, abort_flag)) return false;
-          ++mine.segs;
-        }
-        tc_fence_after();
-        const int stage = uniform(mine.stage), n_mma = uniform(mine.steps);
-        const uint64_t dv = desc_at(dv0, stage * kTileStep);
-        const uint32_t to = tm + (2 + x) * kTile, ts = tm + x * kTile;
-        const uint32_t acc = uniform(mine.fresh ? 0 : 1);
-        if (elect_one()) {
-          if (n_mma == kTile / 16) {
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              umma_bf16_tmem_a(to, ts + kk * 8, desc_at(dv, kk * (2048 >> 4)), idesc_pv,
-                               kk > 0 ? 1u : acc);
-          } else {
-#pragma unroll 1
-            for (int kk = 0; kk < n_mma; ++kk)
-              umma_bf16_tmem_a(to, ts + kk * 8, desc_at(dv, kk * (2048 >> 4)), idesc_pv,
-                               kk > 0 ? 1u : acc);
-          }
-          if (mine.frees) umma_commit(v_empty(stage));
-          if (mine.ends) umma_commit(pv_done(x));
-        }
-        mine.steps = 0;
-        return true;
-      };
-      auto next_step = [&]() {
-        const Owed t = mine;
-        mine = other;
-        other = t;
-        x ^= 1;
-        ++step;
-      };
+      // the PV that an x owes: its MMAs (16 keys each, 0: none), the stage and parity of
+      // its V tile, and whether it is the x's first of the segment (overwrites O_x), the
+      // last one, the last user of the V tile
+      constexpr int kMmas = 15, kStageAt = 4, kParity = 64, kFresh = 128, kEnds = 256, kFrees = 512;
+      int mine = 0, other = 0;               // of this step's x and of the other one
+      int segs = 0, segs_other = 0;          // segments that have begun to overwrite O_x
+      int p_parity = 0, p_other = 0;         // of p_full(x), of the next PV
+      bool ok = true, two = false, ended = false;
+      int x = 0, step = 0, i = 0, steps = 0, whole = 0, flush = 0;
+      int ks = 0, kp = 0, vs = 0, vp = 0;    // stage and parity of the next K and V tile
       Seg sg = {};
-      for (int n = 0; ok; ++n) {
-        if (!read_seg(n, sg)) {
-          ok = false;
-          break;
+      for (int n = 0;; ) {
+        if (i == steps && !ended) {          // the next segment
+          ok = read_seg(n, sg);
+          if (!ok) break;
+          seg_done(n);
+          ++n;
+          ended = sg.head < 0;
+          two = sg.ntok > p.tile_tokens;
+          steps = ended ? 0 : (two ? 2 : 1) * (sg.t1 - sg.t0);
+          whole = sg.ctx / kTile;
+          i = 0;
         }
-        seg_done(n);
-        if (sg.head < 0) break;
-        if (step < sg.step0) {       // a step left out
-          ok = issue_pv();
-          next_step();
-        }
-        const bool two = sg.ntok > p.tile_tokens;
-        const int steps = (two ? 2 : 1) * (sg.t1 - sg.t0), whole = sg.ctx / kTile;
+        if (ended && flush++ == 2) break;
+        // ---- the x's last PV
+        const int w = uniform(mine);
+        if (w & kMmas) {
+          const int mmas = w & kMmas, stage = (w >> kStageAt) & 3;
+          ok = warp_wait(v_full(stage), (w & kParity) ? 1 : 0, abort_flag) &&
+               warp_wait(p_full(x), p_parity, abort_flag);
+          // what the last segment left in O_x must have been read out
+          if (ok && (w & kFresh)) {
+            ok = segs == 0 || warp_wait(o_free(x), (segs - 1) & 1, abort_flag);
+            ++segs;
+          }
+          if (!ok) break;
+          p_parity ^= 1;
+          tc_fence_after();
+          const uint64_t dv = desc_at(dv0, stage * kTileStep);
+          const uint32_t to = tm + (2 + x) * kTile, ts = tm + x * kTile;
+          if (elect_one()) {
+            if (mmas == kTile / 16) {
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                umma_bf16_tmem_a(to, ts + kk * 8, desc_at(dv, kk * (2048 >> 4)), idesc_pv,
+                                 kk > 0 || !(w & kFresh));
+            } else {
 #pragma unroll 1
-        for (int i = 0; ok && i < steps; ++i) {
-          if (!issue_pv()) {
-            ok = false;
-            break;
+              for (int kk = 0; kk < mmas; ++kk)
+                umma_bf16_tmem_a(to, ts + kk * 8, desc_at(dv, kk * (2048 >> 4)), idesc_pv,
+                                 kk > 0 || !(w & kFresh));
+            }
+            if (w & kFrees) umma_commit(v_empty(stage));
+            if (w & kEnds) umma_commit(pv_done(x));
           }
+          mine = 0;
+        }
+        // ---- S of the step, unless it is left out (step0 is one further) or the walk is over
+        if (!ended && step >= sg.step0) {
           const int qt = sg.qtile + (two ? x : 0);
-          if ((i < (two ? 2 : 1) && !warp_wait(q_full(qt & 1), (qt >> 1) & 1, abort_flag)) ||
-              !warp_wait(k_full(ks), kp, abort_flag)) {
-            ok = false;
-            break;
-          }
+          ok = (i >= (two ? 2 : 1) || warp_wait(q_full(qt & 1), (qt >> 1) & 1, abort_flag)) &&
+               warp_wait(k_full(ks), kp, abort_flag);
+          if (!ok) break;
           tc_fence_after();
           const int tile = sg.t0 + (two ? i >> 1 : i);
           const int rows = tile < whole ? kTile : tile_keys(sg.ctx, sg.drafts, tile).rows;
@@ -817,12 +789,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (frees) umma_commit(k_empty(ks));
             if (i >= steps - (two ? 2 : 1)) umma_commit(q_empty(qt & 1));
           }
-          mine.steps = rows / 16;
-          mine.fresh = i < 2;
-          mine.ends = i >= steps - 2;
-          mine.frees = frees;
-          mine.stage = vs;
-          mine.parity = vp;
+          mine = rows / 16 | vs << kStageAt | (vp ? kParity : 0) | (i < 2 ? kFresh : 0) |
+                 (i >= steps - 2 ? kEnds : 0) | (frees ? kFrees : 0);
           if (frees) {
             if (++ks == kKStages) {
               ks = 0;
@@ -833,13 +801,19 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
               vp ^= 1;
             }
           }
-          next_step();
+          ++i;
         }
-      }
-      if (ok) {
-        ok = issue_pv();
-        next_step();
-        ok = ok && issue_pv();
+        ++step;
+        x ^= 1;
+        int t = mine;
+        mine = other;
+        other = t;
+        t = segs;
+        segs = segs_other;
+        segs_other = t;
+        t = p_parity;
+        p_parity = p_other;
+        p_other = t;
       }
       if (!ok) fail();
       // every issued MMA completes before TMEM is freed
@@ -895,42 +869,6 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           break;
         }
         ++steps_seen;
-        if (tk.drafts > 0) {
-          // drafted V values that are not finite must not meet the weights of
-          // rows that do not see them (0 * NaN); the live threads share the V rows
-          const int vt = tbase + i;
-          if (!warp_wait(v_full(vt % kVStages), (vt / kVStages) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          for (int u = row; u < tk.drafts; u += 32 * live_warps) {
-            const uint32_t v_row = sV(vt % kVStages) + (tk.at + u) * 128;
-            uint32_t inf = 0u;
-#pragma unroll 1
-            for (int e = 0; e < 16; ++e) {
-              const uint4 v = lds128(v_row + (e >> 3) * kRegion + (e & 7) * 16);
-              // an all-ones exponent carries into the sign bit
-              inf |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
-                     ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
-            }
-            if (inf & 0x80008000u) {
-              // the flag first: a warpgroup that already finds zeros here sees it too
-              seg_at(n)->bad = 1;
-              __threadfence_block();
-#pragma unroll 1
-              for (int e = 0; e < 64; ++e) {
-                const uint32_t a = v_row + (e >> 5) * kRegion + (e & 31) * 4;
-                uint32_t v;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-                if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
-                if ((v & 0x7f800000u) == 0x7f800000u) v &= 0xffffu;
-                asm volatile("st.shared.u32 [%0], %1;" :: "r"(a), "r"(v) : "memory");
-              }
-              fence_proxy_async_smem();
-            }
-          }
-          __syncwarp();
-        }
         {
           tc_fence_after();
           const uint32_t ts = tmem_s(x) + lane_off;
@@ -966,17 +904,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           // The scores are read twice, 32 columns at a time in short loops: code that
           // holds the whole row in registers is four times as long and its
           // instruction fetches cost more than the second read.
-          float s0[32], s1[32];
           float mt = -INFINITY;
-          tmem_ld32(ts, s0);
 #pragma unroll 1
-          for (int cc = 0; cc < 4; cc += 2) {
+          for (int cc = 0; cc < 4; ++cc) {
+            float s[32];
+            tmem_ld32(ts + cc * 32, s);
             tmem_wait_ld();
-            tmem_ld32(ts + cc * 32 + 32, s1);
-            mt = fmaxf(mt, max32(s0));
-            tmem_wait_ld();
-            tmem_ld32(ts + ((cc * 32 + 64) & 127), s0);   // the last one starts the second read
-            mt = fmaxf(mt, max32(s1));
+            mt = fmaxf(mt, max32(s));
           }
           const bool grow =
               mt != -INFINITY && (m_used == -INFINITY || (mt - m_used) * c > kRescaleThreshold);
@@ -1005,8 +939,12 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           // a row that has seen nothing yet keeps weights of 0: exp2(-inf - 0)
           const float mc = m_used == -INFINITY ? 0.f : m_used * c;
           float2 rs2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          auto weigh = [&](const float (&s)[32], int cc) {
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            float s[32];
             uint32_t pk[16];
+            tmem_ld32(ts + cc * 32, s);
+            tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float2 xx =
@@ -1016,19 +954,44 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
               pk[e] = float2_to_bf16x2(pp.x, pp.y);
             }
             tmem_st16_u(ts + cc * 16, pk);   // over scores that have been read
-          };
-#pragma unroll 1
-          for (int cc = 0; cc < 4; cc += 2) {
-            tmem_wait_ld();
-            tmem_ld32(ts + cc * 32 + 32, s1);
-            weigh(s0, cc);
-            tmem_wait_ld();
-            if (cc == 0) tmem_ld32(ts + 64, s0);
-            weigh(s1, cc + 1);
           }
           l_sum += (rs2[0].x + rs2[0].y) + (rs2[1].x + rs2[1].y);
           tmem_wait_st();
           tc_fence_before();
+        }
+        if (!whole) {
+          // V values that are not finite must not meet the weights (of 0) of rows that
+          // do not see them; the live threads share the 16-byte pieces of the tile's
+          // rows behind the cached ones
+          const int vt = tbase + i;
+          if (!warp_wait(v_full(vt % kVStages), (vt / kVStages) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t v0 = sV(vt % kVStages);
+#pragma unroll 1
+          for (int e = tk.cached * 16 + row; e < tk.rows * 16; e += 32 * live_warps) {
+            // piece e & 15 of row e / 16 (swizzled among themselves: any order will do)
+            const uint32_t at = v0 + ((e >> 3) & 1) * kRegion + (e >> 4) * 128 + (e & 7) * 16;
+            uint4 v = lds128(at);
+            // an all-ones exponent carries into the sign bit
+            const uint32_t inf =
+                ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+            if (inf & 0x80008000u) {
+              // the flag first: a warpgroup that already finds zeros here sees it too
+              if ((e >> 4) >= tk.at && (e >> 4) < tk.at + tk.drafts) seg_at(n)->bad = 1;
+              __threadfence_block();
+              auto finite = [](uint32_t w) {
+                if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+                if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+                return w;
+              };
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(at), "r"(finite(v.x)),
+                           "r"(finite(v.y)), "r"(finite(v.z)), "r"(finite(v.w)) : "memory");
+              fence_proxy_async_smem();
+            }
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive_count(p_full(x), arrivals);
@@ -1361,17 +1324,26 @@ cudaError_t launch_tree_decode(const TreeDecodeArgs &a, cudaStream_t stream) {
   if (p.box_rows > kTile) p.box_rows = kTile;
   const uint64_t cache_rows = static_cast<uint64_t>(a.num_blocks) * a.block_size;
   const uint64_t cache_bytes = static_cast<uint64_t>(a.num_kv_heads) * kHD * 2;
-  CUtensorMap tq, tk, tv, tkg, tvg, tkd, tvd;
-  const uint32_t kv_box = p.box_rows > 0 ? p.box_rows : 8;
-  if (!box_map(&tq, a.q, a.total_q, a.num_q_heads, static_cast<uint64_t>(a.num_q_heads) * kHD * 2,
-               group, p.box_tokens) ||
-      !box_map(&tk, a.k_cache, cache_rows, a.num_kv_heads, cache_bytes, 1, kv_box) ||
-      !box_map(&tv, a.v_cache, cache_rows, a.num_kv_heads, cache_bytes, 1, kv_box) ||
-      !rows_map(&tkg, a.k_cache, cache_rows, a.num_kv_heads, cache_bytes) ||
-      !rows_map(&tvg, a.v_cache, cache_rows, a.num_kv_heads, cache_bytes) ||
-      !rows_map(&tkd, a.key, a.total_q, a.num_kv_heads, a.key_stride * 2) ||
-      !rows_map(&tvd, a.value, a.total_q, a.num_kv_heads, a.value_stride * 2))
-    return cudaErrorInvalidValue;
+  CUtensorMap tq, tk, tv, tkp, tvp, tkd, tvd;
+  const uint64_t hkv = a.num_kv_heads, rows_q = a.total_q;
+  bool maps = box_map(&tq, a.q, rows_q, a.num_q_heads, static_cast<uint64_t>(a.num_q_heads) * kHD * 2,
+                      group, p.box_tokens);
+  if (p.box_rows > 0) {
+    maps = maps && box_map(&tk, a.k_cache, cache_rows, hkv, cache_bytes, 1, p.box_rows) &&
+           box_map(&tv, a.v_cache, cache_rows, hkv, cache_bytes, 1, p.box_rows) &&
+           box_map(&tkp, a.k_cache, cache_rows, hkv, cache_bytes, 1, 8) &&
+           box_map(&tvp, a.v_cache, cache_rows, hkv, cache_bytes, 1, 8) &&
+           box_map(&tkd, a.key, rows_q, hkv, a.key_stride * 2, 1, 8) &&
+           box_map(&tvd, a.value, rows_q, hkv, a.value_stride * 2, 1, 8);
+  } else {
+    maps = maps && rows_map(&tk, a.k_cache, cache_rows, hkv, cache_bytes) &&
+           rows_map(&tv, a.v_cache, cache_rows, hkv, cache_bytes) &&
+           rows_map(&tkd, a.key, rows_q, hkv, a.key_stride * 2) &&
+           rows_map(&tvd, a.value, rows_q, hkv, a.value_stride * 2);
+    tkp = tk;
+    tvp = tv;
+  }
+  if (!maps) return cudaErrorInvalidValue;
   const TreeWs ws = tree_ws(a.max_seqlen_q, group, grid);
   uint8_t *w = static_cast<uint8_t *>(a.workspace);
   p.out = static_cast<__nv_bfloat16 *>(a.out);
@@ -1399,7 +1371,7 @@ cudaError_t launch_tree_decode(const TreeDecodeArgs &a, cudaStream_t stream) {
   p.ml = reinterpret_cast<float2 *>(w + ws.ml);
   p.po = reinterpret_cast<float *>(w + ws.po);
   p.err = a.err;
-  tree_decode_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, tkg, tvg, tkd, tvd, p);
+  tree_decode_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, tkp, tvp, tkd, tvd, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
