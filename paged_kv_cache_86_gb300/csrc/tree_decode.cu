@@ -513,75 +513,107 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tma_prefetch_desc(map_part);
         tma_prefetch_desc(map_draft);
       }
+      // The rows of a tile are looked up one tile ahead: the block table's latency
+      // passes while the tile before waits for its stage and is issued. Lane l holds
+      // the first row of the tile's l-th box, or the four rows of its l-th gather.
+      struct Rows {
+        int4 r;
+        int rows;     // of the tile, to be loaded
+        int step;     // rows a copy
+        int draft;    // first copy of drafts
+        int head;     // KV head; -1: no tile
+        bool whole;
+      };
       Seg sg;
-      for (int n = 0; ok; ++n) {
-        ok = read_seg(n, sg);
-        if (!ok) break;
-        seg_done(n);
-        if (sg.head < 0) break;
-        const int32_t *bt = p.block_tables + static_cast<int64_t>(sg.seq) * p.max_blocks_per_seq;
+      int n = -1, j = 0;
+      sg.t1 = 0;
+      auto look_up = [&](Rows &t) -> bool {   // the walk's next tile
+        t.head = -1;
+        if (j >= sg.t1) {
+          if (!read_seg(++n, sg)) return false;
+          seg_done(n);
+          j = sg.t0;
+          if (sg.head < 0) return true;
+        }
+        const TileKeys tk = tile_keys(sg.ctx, sg.drafts, j);
+        t.head = sg.head;
+        t.whole = tk.cached == kTile;
+        t.rows = tk.rows;
+        t.step = !boxes ? 4 : t.whole ? p.box_rows : 8;
+        t.draft = tk.drafts > 0 ? tk.at / t.step : kTile;
+        t.r = make_int4(oob_row, oob_row, oob_row, oob_row);
+        const int k0 = t.step * lane;
+        if (tk.drafts > 0 && k0 >= tk.at) {
+          const int u = k0 - tk.at, first = sg.q0 + tk.u0;
+          t.r.x = u < tk.drafts ? first + u : p.total_q;
+          t.r.y = u + 1 < tk.drafts ? first + u + 1 : p.total_q;
+          t.r.z = u + 2 < tk.drafts ? first + u + 2 : p.total_q;
+          t.r.w = u + 3 < tk.drafts ? first + u + 3 : p.total_q;
+        } else {
+          const int32_t *bt = p.block_tables + static_cast<int64_t>(sg.seq) * p.max_blocks_per_seq;
 #pragma unroll 1
-        for (int j = sg.t0; j < sg.t1; ++j) {
-          const TileKeys tk = tile_keys(sg.ctx, sg.drafts, j);
-          // lane l holds the first row of the tile's l-th box, or the four rows of its
-          // l-th gather
-          const int step = !boxes ? 4 : tk.cached == kTile ? p.box_rows : 8;   // rows a copy
-          const int k0 = step * lane;
-          int4 r = make_int4(oob_row, oob_row, oob_row, oob_row);
-          if (tk.drafts > 0 && k0 >= tk.at) {
-            const int u = k0 - tk.at, first = sg.q0 + tk.u0;
-            r.x = u < tk.drafts ? first + u : p.total_q;
-            r.y = u + 1 < tk.drafts ? first + u + 1 : p.total_q;
-            r.z = u + 2 < tk.drafts ? first + u + 2 : p.total_q;
-            r.w = u + 3 < tk.drafts ? first + u + 3 : p.total_q;
+          for (int e = (boxes ? 1 : 4) - 1; e >= 0; --e) {   // r.x last
+            t.r.w = t.r.z;
+            t.r.z = t.r.y;
+            t.r.y = t.r.x;
+            t.r.x = oob_row;
+            const int key = j * kTile + k0 + e;
+            if (k0 + e < tk.cached) {
+              const int blk = __ldg(bt + key / p.block_size);
+              if (blk >= 0 && blk < p.num_blocks)
+                t.r.x = blk * p.block_size + key % p.block_size;
+              else if (is_k)
+                raise_error(p.err, PKV_DEVERR_BLOCK_ID);
+            }
+          }
+        }
+        ++j;
+        return true;
+      };
+      Rows next;
+      ok = look_up(next);
+      while (ok && next.head >= 0) {
+        const Rows t = next;
+        ok = look_up(next) && warp_wait(empty0 + 8 * stage, parity, abort_flag);
+        if (!ok) break;
+        const uint32_t full = full0 + 8 * stage;
+        uint32_t dst = dst0 + stage * kTileBytes;
+        if (elect_one()) mbar_arrive_expect_tx(full, t.rows * kHD * 2);
+        const int copies = t.rows / t.step, dst_step = t.step * 128;
+        const CUtensorMap *map = t.whole ? map_whole : map_part;
+        int b = 0;
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {     // cached rows, drafts
+          const int end = part == 0 ? min(t.draft, copies) : copies;
+          if (boxes) {
+#pragma unroll 1
+            for (; b < end; ++b, dst += dst_step) {
+              const int row = __shfl_sync(0xffffffffu, t.r.x, b);
+              if (elect_one()) {
+                tma_load_3d(dst, map, 0, t.head, row, full);
+                tma_load_3d(dst + kRegion, map, 64, t.head, row, full);
+              }
+            }
           } else {
 #pragma unroll 1
-            for (int e = (boxes ? 1 : 4) - 1; e >= 0; --e) {   // r.x last
-              r.w = r.z;
-              r.z = r.y;
-              r.y = r.x;
-              r.x = oob_row;
-              const int key = j * kTile + k0 + e;
-              if (k0 + e < tk.cached) {
-                const int blk = __ldg(bt + key / p.block_size);
-                if (blk >= 0 && blk < p.num_blocks)
-                  r.x = blk * p.block_size + key % p.block_size;
-                else if (is_k)
-                  raise_error(p.err, PKV_DEVERR_BLOCK_ID);
+            for (; b < end; ++b, dst += dst_step) {
+              int4 q;
+              q.x = __shfl_sync(0xffffffffu, t.r.x, b);
+              q.y = __shfl_sync(0xffffffffu, t.r.y, b);
+              q.z = __shfl_sync(0xffffffffu, t.r.z, b);
+              q.w = __shfl_sync(0xffffffffu, t.r.w, b);
+              if (elect_one()) {
+                tma_gather4(dst, map, t.head * kHD, q, full);
+                tma_gather4(dst + kRegion, map, t.head * kHD + 64, q, full);
               }
             }
           }
-          ok = warp_wait(empty0 + 8 * stage, parity, abort_flag);
-          if (!ok) break;
-          const uint32_t full = full0 + 8 * stage;
-          uint32_t dst = dst0 + stage * kTileBytes;
-          if (elect_one()) mbar_arrive_expect_tx(full, tk.rows * kHD * 2);
-          const int first_draft = tk.drafts > 0 ? tk.at : kTile;
-#pragma unroll 1
-          for (int b = 0; b * step < tk.rows; ++b) {
-            const CUtensorMap *map =
-                b * step >= first_draft ? map_draft : tk.cached == kTile ? map_whole : map_part;
-            int4 q;
-            q.x = __shfl_sync(0xffffffffu, r.x, b);
-            q.y = __shfl_sync(0xffffffffu, r.y, b);
-            q.z = __shfl_sync(0xffffffffu, r.z, b);
-            q.w = __shfl_sync(0xffffffffu, r.w, b);
-            if (elect_one()) {
-              if (boxes) {
-                tma_load_3d(dst, map, 0, sg.head, q.x, full);
-                tma_load_3d(dst + kRegion, map, 64, sg.head, q.x, full);
-              } else {
-                tma_gather4(dst, map, sg.head * kHD, q, full);
-                tma_gather4(dst + kRegion, map, sg.head * kHD + 64, q, full);
-              }
-            }
-            dst += step * 128;
-          }
-          ++issued;
-          if (++stage == stages) {
-            stage = 0;
-            parity ^= 1;
-          }
+          map = map_draft;
+        }
+        ++issued;
+        if (++stage == stages) {
+          stage = 0;
+          parity ^= 1;
         }
       }
       if (!ok) fail();
@@ -710,13 +742,15 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       constexpr uint32_t kTileStep = kTileBytes >> 4;
       const uint32_t tm = uniform(static_cast<int>(tmem));
       const uint64_t dq0 = desc_kmajor(sQ, 0), dk0 = desc_kmajor(sK(0), 0), dv0 = desc_v_mnmajor(sV(0));
-      // the PV that an x owes: its MMAs (16 keys each, 0: none), the stage and parity of
+      // The PV that an x owes: its MMAs (16 keys each, 0: none), the stage and parity of
       // its V tile, and whether it is the x's first of the segment (overwrites O_x), the
-      // last one, the last user of the V tile
-      constexpr int kMmas = 15, kStageAt = 4, kParity = 64, kFresh = 128, kEnds = 256, kFrees = 512;
+      // last one, the last user of the V tile, or one whose V tile x = 0 has waited for.
+      constexpr int kMmas = 15, kStageAt = 4, kParity = 64, kFresh = 128, kEnds = 256, kFrees = 512,
+                    kWaited = 1024, kPv = 2047;
+      // What an x keeps: the parity of p_full(x) and, once a segment has overwritten
+      // O_x, that of o_free(x).
+      constexpr int kPParity = 1 << 12, kOUsed = 1 << 13, kOParity = 1 << 14;
       int mine = 0, other = 0;               // of this step's x and of the other one
-      int segs = 0, segs_other = 0;          // segments that have begun to overwrite O_x
-      int p_parity = 0, p_other = 0;         // of p_full(x), of the next PV
       bool ok = true, two = false, ended = false;
       int x = 0, step = 0, i = 0, steps = 0, whole = 0, flush = 0;
       int ks = 0, kp = 0, vs = 0, vp = 0;    // stage and parity of the next K and V tile
@@ -738,15 +772,19 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int w = uniform(mine);
         if (w & kMmas) {
           const int mmas = w & kMmas, stage = (w >> kStageAt) & 3;
-          ok = warp_wait(v_full(stage), (w & kParity) ? 1 : 0, abort_flag) &&
-               warp_wait(p_full(x), p_parity, abort_flag);
+          ok = ((w & kWaited) || warp_wait(v_full(stage), (w & kParity) ? 1 : 0, abort_flag)) &&
+               warp_wait(p_full(x), (w & kPParity) ? 1 : 0, abort_flag);
+          int keep = (w & ~kPv) ^ kPParity;
           // what the last segment left in O_x must have been read out
           if (ok && (w & kFresh)) {
-            ok = segs == 0 || warp_wait(o_free(x), (segs - 1) & 1, abort_flag);
-            ++segs;
+            if (w & kOUsed) {
+              ok = warp_wait(o_free(x), (w & kOParity) ? 1 : 0, abort_flag);
+              keep ^= kOParity;
+            }
+            keep |= kOUsed;
           }
           if (!ok) break;
-          p_parity ^= 1;
+          mine = keep;
           tc_fence_after();
           const uint64_t dv = desc_at(dv0, stage * kTileStep);
           const uint32_t to = tm + (2 + x) * kTile, ts = tm + x * kTile;
@@ -765,13 +803,12 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (w & kFrees) umma_commit(v_empty(stage));
             if (w & kEnds) umma_commit(pv_done(x));
           }
-          mine = 0;
         }
         // ---- S of the step, unless it is left out (step0 is one further) or the walk is over
         if (!ended && step >= sg.step0) {
           const int qt = sg.qtile + (two ? x : 0);
           ok = (i >= (two ? 2 : 1) || warp_wait(q_full(qt & 1), (qt >> 1) & 1, abort_flag)) &&
-               warp_wait(k_full(ks), kp, abort_flag);
+               ((two && x == 1) || warp_wait(k_full(ks), kp, abort_flag));
           if (!ok) break;
           tc_fence_after();
           const int tile = sg.t0 + (two ? i >> 1 : i);
@@ -789,8 +826,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (frees) umma_commit(k_empty(ks));
             if (i >= steps - (two ? 2 : 1)) umma_commit(q_empty(qt & 1));
           }
-          mine = rows / 16 | vs << kStageAt | (vp ? kParity : 0) | (i < 2 ? kFresh : 0) |
-                 (i >= steps - 2 ? kEnds : 0) | (frees ? kFrees : 0);
+          mine |= rows / 16 | vs << kStageAt | (vp ? kParity : 0) | (i < 2 ? kFresh : 0) |
+                  (i >= steps - 2 ? kEnds : 0) | (frees ? kFrees : 0) | (two && x == 1 ? kWaited : 0);
           if (frees) {
             if (++ks == kKStages) {
               ks = 0;
@@ -805,15 +842,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         ++step;
         x ^= 1;
-        int t = mine;
+        const int t = mine;
         mine = other;
         other = t;
-        t = segs;
-        segs = segs_other;
-        segs_other = t;
-        t = p_parity;
-        p_parity = p_other;
-        p_other = t;
       }
       if (!ok) fail();
       // every issued MMA completes before TMEM is freed
