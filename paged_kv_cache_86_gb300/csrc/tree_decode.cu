@@ -1157,14 +1157,30 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // eight pieces; with more, the CTA's eight warps share the row's pieces, so that
 // no warp waits for more than a few loads in turn.
 constexpr int kCombineWarps = 8;
+constexpr int kBatch = 6;
 
-__global__ void __launch_bounds__(kCombineWarps * 32, 2) tree_combine_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kCombineWarps * 32, 4)
+tree_combine_kernel(const TreeParams p, const int num_bounds) {
   __shared__ float2 s_ml[kCombineWarps];
   __shared__ float4 s_o[kCombineWarps][32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Boundary b = p.bounds[blockIdx.x];
-  if (b.row0 < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // CTA x takes the x-th boundary that has something to merge: with few streams the
+  // grid has fewer CTAs than there are boundaries
+  int left = blockIdx.x, index = -1;
+  for (int b0 = 0; b0 < num_bounds && index < 0; b0 += 32) {
+    const bool cut = b0 + lane < num_bounds && p.bounds[b0 + lane].row0 >= 0;
+    unsigned mask = __ballot_sync(0xffffffffu, cut);
+    const int n = __popc(mask);
+    if (left < n) {
+      for (; left > 0; --left) mask &= mask - 1;
+      index = b0 + __ffs(mask) - 1;
+    } else {
+      left -= n;
+    }
+  }
+  if (index < 0) return;
+  const Boundary b = p.bounds[index];
   const int rows = b.ntok * p.group;
   const bool shared_row = b.last - b.first >= kCombineWarps;
   const int share = shared_row ? kCombineWarps : 1;   // warps on a row
@@ -1174,12 +1190,12 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2) tree_combine_kernel(con
   for (int row = row0; row < rows; row += row_step) {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    // eight pieces' loads in flight at a time
-    for (int c0 = b.first + part; c0 <= b.last; c0 += 8 * share) {
-      float2 ml[8];
-      float4 v[8];
+    // a batch of pieces' loads in flight at a time
+    for (int c0 = b.first + part; c0 <= b.last; c0 += kBatch * share) {
+      float2 ml[kBatch];
+      float4 v[kBatch];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < kBatch; ++j) {
         const int c = min(c0 + j * share, b.last);
         const int64_t rec = static_cast<int64_t>(2 * c + (c == b.first ? 1 : 0)) * p.rows_cap + row;
         ml[j] = p.ml[rec];
@@ -1187,7 +1203,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2) tree_combine_kernel(con
       }
       float mt = m;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < kBatch; ++j)
         if (c0 + j * share <= b.last) mt = fmaxf(mt, ml[j].x);
       if (mt == -INFINITY) continue;
       const float a = m == -INFINITY ? 0.f : ex2(m - mt);
@@ -1195,7 +1211,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2) tree_combine_kernel(con
       o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
       m = mt;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < kBatch; ++j) {
         // nothing of a piece of which the row sees nothing
         if (c0 + j * share > b.last || ml[j].x == -INFINITY) continue;
         const float w = ex2(ml[j].x - m);
@@ -1406,7 +1422,15 @@ cudaError_t launch_tree_decode(const TreeDecodeArgs &a, cudaStream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, p.rows_cap < 32 ? p.rows_cap : 32);
+  // at most one merge a stream and one a range boundary
+  const int64_t streams = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads *
+                          ((a.max_seqlen_q + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens));
+  const int merges = streams < grid ? static_cast<int>(streams) : grid;
+  // four CTAs an SM in all (all resident at once: with 32 a merge the launch alone
+  // took 8 us), shared among the merges; more than one a row helps nobody
+  int share = 4 * grid / merges;
+  share = share < p.rows_cap ? share : p.rows_cap;
+  cfg.gridDim = dim3(merges, share > 0 ? share : 1);
   cfg.blockDim = dim3(kCombineWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1414,7 +1438,7 @@ cudaError_t launch_tree_decode(const TreeDecodeArgs &a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_combine_kernel, p);
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel, p, grid);
 }
 
 }  // namespace pkv
