@@ -515,9 +515,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       }
       // The rows of a tile are looked up one tile ahead: the block table's latency
       // passes while the tile before waits for its stage and is issued. Lane l holds
-      // the first row of the tile's l-th box, or the four rows of its l-th gather.
+      // what belongs to the first row of the tile's l-th box, or to the four rows of its
+      // l-th gather; rows are worked out when the tile is issued, not waited for here.
       struct Rows {
-        int4 r;
+        int4 r;       // the lane's block ids as read, or its rows of the drafts
+        bool drafted;
+        int key;      // first key of the lane's copy
+        int left;     // cached keys from there on
         int rows;     // of the tile, to be loaded
         int step;     // rows a copy
         int draft;    // first copy of drafts
@@ -541,9 +545,10 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         t.rows = tk.rows;
         t.step = !boxes ? 4 : t.whole ? p.box_rows : 8;
         t.draft = tk.drafts > 0 ? tk.at / t.step : kTile;
-        t.r = make_int4(oob_row, oob_row, oob_row, oob_row);
         const int k0 = t.step * lane;
-        if (tk.drafts > 0 && k0 >= tk.at) {
+        t.key = j * kTile + k0;
+        t.drafted = tk.drafts > 0 && k0 >= tk.at;
+        if (t.drafted) {
           const int u = k0 - tk.at, first = sg.q0 + tk.u0;
           t.r.x = u < tk.drafts ? first + u : p.total_q;
           t.r.y = u + 1 < tk.drafts ? first + u + 1 : p.total_q;
@@ -551,20 +556,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           t.r.w = u + 3 < tk.drafts ? first + u + 3 : p.total_q;
         } else {
           const int32_t *bt = p.block_tables + static_cast<int64_t>(sg.seq) * p.max_blocks_per_seq;
-#pragma unroll 1
-          for (int e = (boxes ? 1 : 4) - 1; e >= 0; --e) {   // r.x last
-            t.r.w = t.r.z;
-            t.r.z = t.r.y;
-            t.r.y = t.r.x;
-            t.r.x = oob_row;
-            const int key = j * kTile + k0 + e;
-            if (k0 + e < tk.cached) {
-              const int blk = __ldg(bt + key / p.block_size);
-              if (blk >= 0 && blk < p.num_blocks)
-                t.r.x = blk * p.block_size + key % p.block_size;
-              else if (is_k)
-                raise_error(p.err, PKV_DEVERR_BLOCK_ID);
-            }
+          t.left = tk.cached - k0;
+          t.r = make_int4(0, 0, 0, 0);
+          if (t.left > 0) t.r.x = __ldg(bt + t.key / p.block_size);
+          if (!boxes) {
+            if (t.left > 1) t.r.y = __ldg(bt + (t.key + 1) / p.block_size);
+            if (t.left > 2) t.r.z = __ldg(bt + (t.key + 2) / p.block_size);
+            if (t.left > 3) t.r.w = __ldg(bt + (t.key + 3) / p.block_size);
           }
         }
         ++j;
@@ -573,7 +571,22 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       Rows next;
       ok = look_up(next);
       while (ok && next.head >= 0) {
-        const Rows t = next;
+        Rows t = next;
+        if (!t.drafted) {
+          auto row = [&](int blk, int e) {   // of the lane's e-th key
+            if (e >= t.left) return oob_row;
+            if (blk >= 0 && blk < p.num_blocks)
+              return blk * p.block_size + (t.key + e) % p.block_size;
+            if (is_k) raise_error(p.err, PKV_DEVERR_BLOCK_ID);
+            return oob_row;
+          };
+          t.r.x = row(t.r.x, 0);
+          if (!boxes) {
+            t.r.y = row(t.r.y, 1);
+            t.r.z = row(t.r.z, 2);
+            t.r.w = row(t.r.w, 3);
+          }
+        }
         ok = look_up(next) && warp_wait(empty0 + 8 * stage, parity, abort_flag);
         if (!ok) break;
         const uint32_t full = full0 + 8 * stage;
@@ -735,12 +748,14 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         warp_wait(q_full(s & 1), (s >> 1) & 1, never);
     } else if (warp == kWarpMma) {
       // ---------------------------------------------------------- MMA issuer
-      // The warp's own instructions are on the path of every tile, so there are few:
-      // one copy for both x, ring positions counted up, descriptors that differ by adds.
+      // One elected lane runs the whole role. Its instructions are on the path of every
+      // tile, so there are few: one copy for both x, ring positions counted up,
+      // descriptors that differ by adds, waits without a vote.
+      if (elect_one()) {
       constexpr uint32_t idesc_s = umma_idesc_bf16(kTile, 0, false);            // N is added
       constexpr uint32_t idesc_pv = umma_idesc_bf16(kTile, kHD, true);          // B (V) MN-major
       constexpr uint32_t kTileStep = kTileBytes >> 4;
-      const uint32_t tm = uniform(static_cast<int>(tmem));
+      const uint32_t tm = tmem;
       const uint64_t dq0 = desc_kmajor(sQ, 0), dk0 = desc_kmajor(sK(0), 0), dv0 = desc_v_mnmajor(sV(0));
       // The PV that an x owes: its MMAs (16 keys each, 0: none), the stage and parity of
       // its V tile, and whether it is the x's first of the segment (overwrites O_x), the
@@ -757,9 +772,18 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       Seg sg = {};
       for (int n = 0;; ) {
         if (i == steps && !ended) {          // the next segment
-          ok = read_seg(n, sg);
+          ok = poll(seg_full(n % kSegRing), (n / kSegRing) & 1, abort_flag);
           if (!ok) break;
-          seg_done(n);
+          const volatile Seg *v = seg_at(n);
+          sg.head = v->head;
+          sg.ctx = v->ctx;
+          sg.drafts = v->drafts;
+          sg.ntok = v->ntok;
+          sg.t0 = v->t0;
+          sg.t1 = v->t1;
+          sg.step0 = v->step0;
+          sg.qtile = v->qtile;
+          mbar_arrive(seg_empty(n % kSegRing));
           ++n;
           ended = sg.head < 0;
           two = sg.ntok > p.tile_tokens;
@@ -769,16 +793,16 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         if (ended && flush++ == 2) break;
         // ---- the x's last PV
-        const int w = uniform(mine);
+        const int w = mine;
         if (w & kMmas) {
           const int mmas = w & kMmas, stage = (w >> kStageAt) & 3;
-          ok = ((w & kWaited) || warp_wait(v_full(stage), (w & kParity) ? 1 : 0, abort_flag)) &&
-               warp_wait(p_full(x), (w & kPParity) ? 1 : 0, abort_flag);
+          ok = ((w & kWaited) || poll(v_full(stage), (w & kParity) ? 1 : 0, abort_flag)) &&
+               poll(p_full(x), (w & kPParity) ? 1 : 0, abort_flag);
           int keep = (w & ~kPv) ^ kPParity;
           // what the last segment left in O_x must have been read out
           if (ok && (w & kFresh)) {
             if (w & kOUsed) {
-              ok = warp_wait(o_free(x), (w & kOParity) ? 1 : 0, abort_flag);
+              ok = poll(o_free(x), (w & kOParity) ? 1 : 0, abort_flag);
               keep ^= kOParity;
             }
             keep |= kOUsed;
@@ -788,7 +812,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           tc_fence_after();
           const uint64_t dv = desc_at(dv0, stage * kTileStep);
           const uint32_t to = tm + (2 + x) * kTile, ts = tm + x * kTile;
-          if (elect_one()) {
+          {
             if (mmas == kTile / 16) {
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk)
@@ -807,8 +831,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // ---- S of the step, unless it is left out (step0 is one further) or the walk is over
         if (!ended && step >= sg.step0) {
           const int qt = sg.qtile + (two ? x : 0);
-          ok = (i >= (two ? 2 : 1) || warp_wait(q_full(qt & 1), (qt >> 1) & 1, abort_flag)) &&
-               ((two && x == 1) || warp_wait(k_full(ks), kp, abort_flag));
+          ok = (i >= (two ? 2 : 1) || poll(q_full(qt & 1), (qt >> 1) & 1, abort_flag)) &&
+               ((two && x == 1) || poll(k_full(ks), kp, abort_flag));
           if (!ok) break;
           tc_fence_after();
           const int tile = sg.t0 + (two ? i >> 1 : i);
@@ -817,7 +841,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           const uint64_t dq = desc_at(dq0, (qt & 1) * kTileStep), dk = desc_at(dk0, ks * kTileStep);
           const uint32_t ts = tm + x * kTile;
           const bool frees = !two || x == 1;
-          if (elect_one()) {
+          {
 #pragma unroll
             for (int kk = 0; kk < kHD / 16; ++kk)
               umma_bf16(ts, desc_at(dq, kmajor_step(kk)), desc_at(dk, kmajor_step(kk)), idesc,
@@ -846,10 +870,15 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         mine = other;
         other = t;
       }
-      if (!ok) fail();
+      if (!ok) {
+        *abort_flag = 1;
+        raise_error(p.err, PKV_DEVERR_TIMEOUT);
+      }
       // every issued MMA completes before TMEM is freed
-      if (elect_one()) umma_commit(drained);
-      warp_wait(drained, 0, never);
+      umma_commit(drained);
+      poll(drained, 0, never);
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------ softmax 0 / 1
