@@ -85,7 +85,8 @@ constexpr int kOffBar = kOffSeg + kSegRing * kSegBytes;
 // full/free, drained, seg full/empty
 constexpr int kNumBars = 4 + 2 * kKStages + 2 * kVStages + 10 + 3 + 2 * kSegRing;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;        // TMEM address, abort flag, start
-constexpr int kOffQ = (kOffMisc + 32 + 1023) / 1024 * 1024;   // two Q tiles
+constexpr int kOffRows = (kOffMisc + 32 + 15) / 16 * 16;      // int4[2][32], of the K and V loaders
+constexpr int kOffQ = (kOffRows + 2 * 32 * 16 + 1023) / 1024 * 1024;   // two Q tiles
 constexpr int kOffK = kOffQ + 2 * kTileBytes;
 constexpr int kOffV = kOffK + kKStages * kTileBytes;
 constexpr int kSmemBytes = kOffV + kVStages * kTileBytes;
@@ -136,6 +137,7 @@ struct TreeParams {
   int box_tokens;    // tokens of a Q box: box_tokens * group rows, a multiple of 8
   int tile_tokens;   // tokens of an MMA row tile
   int block_size;
+  uint32_t bs_mul, bs_half, bs_shift;   // n / block_size, see block_of
   int num_blocks;
   int box_rows;      // rows of a K/V box; 0: gathers only
   float scale_log2;  // |scale| * log2 e, or 1 with flip == 0
@@ -295,6 +297,12 @@ __device__ __forceinline__ void mbar_arrive_count(uint32_t bar, uint32_t n) {
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int *abort) {
   return __all_sync(0xffffffffu, poll(bar, parity, abort));
+}
+
+// key / block_size without a division.
+__device__ __forceinline__ int block_of(const TreeParams &p, int key) {
+  const uint32_t n = key, t = __umulhi(n, p.bs_mul);
+  return static_cast<int>((t + ((n - t) >> p.bs_half)) >> p.bs_shift);
 }
 
 // Lengths of sequence i, checked: drafts == 0 when there is nothing to do.
@@ -520,7 +528,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       struct Rows {
         int4 r;       // the lane's block ids as read, or its rows of the drafts
         bool drafted;
-        int key;      // first key of the lane's copy
+        int key, off; // first key of the lane's copy, and its place in its block
         int left;     // cached keys from there on
         int rows;     // of the tile, to be loaded
         int step;     // rows a copy
@@ -558,16 +566,19 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           const int32_t *bt = p.block_tables + static_cast<int64_t>(sg.seq) * p.max_blocks_per_seq;
           t.left = tk.cached - k0;
           t.r = make_int4(0, 0, 0, 0);
-          if (t.left > 0) t.r.x = __ldg(bt + t.key / p.block_size);
+          const int blk = block_of(p, t.key);
+          t.off = t.key - blk * p.block_size;
+          if (t.left > 0) t.r.x = __ldg(bt + blk);
           if (!boxes) {
-            if (t.left > 1) t.r.y = __ldg(bt + (t.key + 1) / p.block_size);
-            if (t.left > 2) t.r.z = __ldg(bt + (t.key + 2) / p.block_size);
-            if (t.left > 3) t.r.w = __ldg(bt + (t.key + 3) / p.block_size);
+            if (t.left > 1) t.r.y = __ldg(bt + block_of(p, t.key + 1));
+            if (t.left > 2) t.r.z = __ldg(bt + block_of(p, t.key + 2));
+            if (t.left > 3) t.r.w = __ldg(bt + block_of(p, t.key + 3));
           }
         }
         ++j;
         return true;
       };
+      int4 *rows_smem = reinterpret_cast<int4 *>(smem + kOffRows) + (is_k ? 0 : 32);
       Rows next;
       ok = look_up(next);
       while (ok && next.head >= 0) {
@@ -575,8 +586,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (!t.drafted) {
           auto row = [&](int blk, int e) {   // of the lane's e-th key
             if (e >= t.left) return oob_row;
-            if (blk >= 0 && blk < p.num_blocks)
-              return blk * p.block_size + (t.key + e) % p.block_size;
+            const int off = e == 0 ? t.off : t.key + e - block_of(p, t.key + e) * p.block_size;
+            if (blk >= 0 && blk < p.num_blocks) return blk * p.block_size + off;
             if (is_k) raise_error(p.err, PKV_DEVERR_BLOCK_ID);
             return oob_row;
           };
@@ -589,40 +600,38 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         ok = look_up(next) && warp_wait(empty0 + 8 * stage, parity, abort_flag);
         if (!ok) break;
-        const uint32_t full = full0 + 8 * stage;
-        uint32_t dst = dst0 + stage * kTileBytes;
-        if (elect_one()) mbar_arrive_expect_tx(full, t.rows * kHD * 2);
-        const int copies = t.rows / t.step, dst_step = t.step * 128;
-        const CUtensorMap *map = t.whole ? map_whole : map_part;
-        int b = 0;
+        // one lane issues the copies, from the rows of all lanes in shared memory
+        rows_smem[lane] = t.r;
+        __syncwarp();
+        if (elect_one()) {
+          const uint32_t full = full0 + 8 * stage;
+          uint32_t dst = dst0 + stage * kTileBytes;
+          mbar_arrive_expect_tx(full, t.rows * kHD * 2);
+          const int copies = t.rows / t.step, dst_step = t.step * 128;
+          const CUtensorMap *map = t.whole ? map_whole : map_part;
+          int b = 0;
 #pragma unroll 1
-        for (int part = 0; part < 2; ++part) {     // cached rows, drafts
-          const int end = part == 0 ? min(t.draft, copies) : copies;
-          if (boxes) {
+          for (int part = 0; part < 2; ++part) {     // cached rows, drafts
+            const int end = part == 0 ? min(t.draft, copies) : copies;
+            if (boxes) {
 #pragma unroll 1
-            for (; b < end; ++b, dst += dst_step) {
-              const int row = __shfl_sync(0xffffffffu, t.r.x, b);
-              if (elect_one()) {
+              for (; b < end; ++b, dst += dst_step) {
+                const int row = rows_smem[b].x;
                 tma_load_3d(dst, map, 0, t.head, row, full);
                 tma_load_3d(dst + kRegion, map, 64, t.head, row, full);
               }
-            }
-          } else {
+            } else {
 #pragma unroll 1
-            for (; b < end; ++b, dst += dst_step) {
-              int4 q;
-              q.x = __shfl_sync(0xffffffffu, t.r.x, b);
-              q.y = __shfl_sync(0xffffffffu, t.r.y, b);
-              q.z = __shfl_sync(0xffffffffu, t.r.z, b);
-              q.w = __shfl_sync(0xffffffffu, t.r.w, b);
-              if (elect_one()) {
+              for (; b < end; ++b, dst += dst_step) {
+                const int4 q = rows_smem[b];
                 tma_gather4(dst, map, t.head * kHD, q, full);
                 tma_gather4(dst + kRegion, map, t.head * kHD + 64, q, full);
               }
             }
+            map = map_draft;
           }
-          map = map_draft;
         }
+        __syncwarp();
         ++issued;
         if (++stage == stages) {
           stage = 0;
@@ -1439,6 +1448,13 @@ cudaError_t launch_tree_decode(const TreeDecodeArgs &a, cudaStream_t stream) {
   p.num_kv_heads = a.num_kv_heads;
   p.group = group;
   p.block_size = a.block_size;
+  // division by d = block_size with 2^(l-1) < d <= 2^l, m = 2^32 (2^l - d) / d + 1
+  // (Granlund and Montgomery, "Division by Invariant Integers using Multiplication")
+  int l = 0;
+  while ((int64_t(1) << l) < a.block_size) ++l;
+  p.bs_mul = static_cast<uint32_t>((((int64_t(1) << l) - a.block_size) << 32) / a.block_size + 1);
+  p.bs_half = l > 0 ? 1 : 0;
+  p.bs_shift = l > 0 ? l - 1 : 0;
   p.num_blocks = a.num_blocks;
   p.flip = a.scale > 0.f ? 1.f : a.scale < 0.f ? -1.f : 0.f;
   p.scale_log2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
