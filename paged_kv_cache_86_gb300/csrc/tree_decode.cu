@@ -217,13 +217,16 @@ __device__ __forceinline__ void umma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tme
       :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-__device__ __forceinline__ void tmem_st16_u(uint32_t taddr, const uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_st32_u(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
       :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
          "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
-         "r"(v[14]), "r"(v[15])
+         "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
+         "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
 
@@ -801,13 +804,25 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           i = 0;
         }
         if (ended && flush++ == 2) break;
+        // ---- what S of the step needs, unless it is left out (step0 is one further) or
+        // the walk is over: worked out before the wait for the weights, so that PV and S
+        // go to the tensor core one behind the other
+        const bool scores = !ended && step >= sg.step0;
+        const int qt = sg.qtile + (two ? x : 0);
+        const int tile = sg.t0 + (two ? i >> 1 : i);
+        const int rows = !scores || tile < whole ? kTile : tile_keys(sg.ctx, sg.drafts, tile).rows;
+        const uint32_t idesc = idesc_s | (static_cast<uint32_t>(rows >> 3) << 17);
+        const uint64_t dq = desc_at(dq0, (qt & 1) * kTileStep), dk = desc_at(dk0, ks * kTileStep);
+        const uint32_t to = tm + (2 + x) * kTile, ts = tm + x * kTile;
+        const bool frees = !two || x == 1;
+        const bool k_there = (two && x == 1) || mbar_test_wait(k_full(ks), kp);
         // ---- the x's last PV
         const int w = mine;
         if (w & kMmas) {
           const int mmas = w & kMmas, stage = (w >> kStageAt) & 3;
-          ok = ((w & kWaited) || poll(v_full(stage), (w & kParity) ? 1 : 0, abort_flag)) &&
-               poll(p_full(x), (w & kPParity) ? 1 : 0, abort_flag);
+          const uint64_t dv = desc_at(dv0, stage * kTileStep);
           int keep = (w & ~kPv) ^ kPParity;
+          ok = (w & kWaited) || poll(v_full(stage), (w & kParity) ? 1 : 0, abort_flag);
           // what the last segment left in O_x must have been read out
           if (ok && (w & kFresh)) {
             if (w & kOUsed) {
@@ -816,49 +831,37 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             keep |= kOUsed;
           }
-          if (!ok) break;
           mine = keep;
-          tc_fence_after();
-          const uint64_t dv = desc_at(dv0, stage * kTileStep);
-          const uint32_t to = tm + (2 + x) * kTile, ts = tm + x * kTile;
-          {
-            if (mmas == kTile / 16) {
-#pragma unroll
-              for (int kk = 0; kk < kTile / 16; ++kk)
-                umma_bf16_tmem_a(to, ts + kk * 8, desc_at(dv, kk * (2048 >> 4)), idesc_pv,
-                                 kk > 0 || !(w & kFresh));
-            } else {
-#pragma unroll 1
-              for (int kk = 0; kk < mmas; ++kk)
-                umma_bf16_tmem_a(to, ts + kk * 8, desc_at(dv, kk * (2048 >> 4)), idesc_pv,
-                                 kk > 0 || !(w & kFresh));
-            }
-            if (w & kFrees) umma_commit(v_empty(stage));
-            if (w & kEnds) umma_commit(pv_done(x));
-          }
-        }
-        // ---- S of the step, unless it is left out (step0 is one further) or the walk is over
-        if (!ended && step >= sg.step0) {
-          const int qt = sg.qtile + (two ? x : 0);
-          ok = (i >= (two ? 2 : 1) || poll(q_full(qt & 1), (qt >> 1) & 1, abort_flag)) &&
-               ((two && x == 1) || poll(k_full(ks), kp, abort_flag));
+          ok = ok && poll(p_full(x), (w & kPParity) ? 1 : 0, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          const int tile = sg.t0 + (two ? i >> 1 : i);
-          const int rows = tile < whole ? kTile : tile_keys(sg.ctx, sg.drafts, tile).rows;
-          const uint32_t idesc = idesc_s | (static_cast<uint32_t>(rows >> 3) << 17);
-          const uint64_t dq = desc_at(dq0, (qt & 1) * kTileStep), dk = desc_at(dk0, ks * kTileStep);
-          const uint32_t ts = tm + x * kTile;
-          const bool frees = !two || x == 1;
-          {
+          if (mmas == kTile / 16) {
 #pragma unroll
-            for (int kk = 0; kk < kHD / 16; ++kk)
-              umma_bf16(ts, desc_at(dq, kmajor_step(kk)), desc_at(dk, kmajor_step(kk)), idesc,
-                        kk > 0 ? 1u : 0u);
-            umma_commit(s_full(x));
-            if (frees) umma_commit(k_empty(ks));
-            if (i >= steps - (two ? 2 : 1)) umma_commit(q_empty(qt & 1));
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              umma_bf16_tmem_a(to, ts + kk * 8, desc_at(dv, kk * (2048 >> 4)), idesc_pv,
+                               kk > 0 || !(w & kFresh));
+          } else {
+#pragma unroll 1
+            for (int kk = 0; kk < mmas; ++kk)
+              umma_bf16_tmem_a(to, ts + kk * 8, desc_at(dv, kk * (2048 >> 4)), idesc_pv,
+                               kk > 0 || !(w & kFresh));
           }
+          if (w & kFrees) umma_commit(v_empty(stage));
+          if (w & kEnds) umma_commit(pv_done(x));
+        }
+        // ---- S of the step
+        if (scores) {
+          ok = (i >= (two ? 2 : 1) || poll(q_full(qt & 1), (qt >> 1) & 1, abort_flag)) &&
+               (k_there || poll(k_full(ks), kp, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kHD / 16; ++kk)
+            umma_bf16(ts, desc_at(dq, kmajor_step(kk)), desc_at(dk, kmajor_step(kk)), idesc,
+                      kk > 0 ? 1u : 0u);
+          umma_commit(s_full(x));
+          if (frees) umma_commit(k_empty(ks));
+          if (i >= steps - (two ? 2 : 1)) umma_commit(q_empty(qt & 1));
           mine |= rows / 16 | vs << kStageAt | (vp ? kParity : 0) | (i < 2 ? kFresh : 0) |
                   (i >= steps - 2 ? kEnds : 0) | (frees ? kFrees : 0) | (two && x == 1 ? kWaited : 0);
           if (frees) {
@@ -975,11 +978,12 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           // instruction fetches cost more than the second read.
           float mt = -INFINITY;
 #pragma unroll 1
-          for (int cc = 0; cc < 4; ++cc) {
-            float s[32];
-            tmem_ld32(ts + cc * 32, s);
+          for (int cc = 0; cc < 4; cc += 2) {
+            float s0[32], s1[32];
+            tmem_ld32(ts + cc * 32, s0);
+            tmem_ld32(ts + cc * 32 + 32, s1);
             tmem_wait_ld();
-            mt = fmaxf(mt, max32(s));
+            mt = fmax3(mt, max32(s0), max32(s1));
           }
           const bool grow =
               mt != -INFINITY && (m_used == -INFINITY || (mt - m_used) * c > kRescaleThreshold);
@@ -1009,20 +1013,22 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           const float mc = m_used == -INFINITY ? 0.f : m_used * c;
           float2 rs2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-          for (int cc = 0; cc < 4; ++cc) {
-            float s[32];
-            uint32_t pk[16];
-            tmem_ld32(ts + cc * 32, s);
+          for (int cc = 0; cc < 4; cc += 2) {
+            float s0[32], s1[32];
+            tmem_ld32(ts + cc * 32, s0);
+            tmem_ld32(ts + cc * 32 + 32, s1);
             tmem_wait_ld();
+            uint32_t pk[32];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 xx =
-                  ffma2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(c, c), make_float2(-mc, -mc));
+            for (int e = 0; e < 32; ++e) {
+              const float2 ss = e < 16 ? make_float2(s0[2 * e], s0[2 * e + 1])
+                                       : make_float2(s1[2 * e - 32], s1[2 * e - 31]);
+              const float2 xx = ffma2(ss, make_float2(c, c), make_float2(-mc, -mc));
               const float2 pp = make_float2(ex2(xx.x), ex2(xx.y));
               rs2[e & 1] = fadd2(rs2[e & 1], pp);
               pk[e] = float2_to_bf16x2(pp.x, pp.y);
             }
-            tmem_st16_u(ts + cc * 16, pk);   // over scores that have been read
+            tmem_st32_u(ts + cc * 16, pk);   // over scores that have been read
           }
           l_sum += (rs2[0].x + rs2[0].y) + (rs2[1].x + rs2[1].y);
           tmem_wait_st();
