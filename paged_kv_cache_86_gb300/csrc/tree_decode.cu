@@ -368,33 +368,19 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     return reinterpret_cast<volatile Seg *>(smem + kOffSeg + (i % kSegRing) * kSegBytes);
   };
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), 1);
-      mbar_init(s_full(s), 1);
-      mbar_init(p_full(s), 4);
-      mbar_init(o_free(s), 4);
-      mbar_init(pv_done(s), 1);
-      mbar_init(wg_end(s), 4);
+  if (warp == kWarpWalk) {
+    // barriers counted 4 (a softmax warpgroup's warps), by ring readers, else 1
+    static_assert(kNumBars <= 64, "two barriers a lane");
+    for (int b = lane; b < kNumBars; b += 32) {
+      const uint32_t bar = bar0 + 8u * b;
+      int count = 1;
+      for (int x = 0; x < 2; ++x)
+        if (bar == p_full(x) || bar == o_free(x) || bar == wg_end(x)) count = 4;
+      if (bar == ml_full || bar == ml_free) count = 4;
+      if (bar >= seg_empty(0) && bar <= seg_empty(kSegRing - 1)) count = kSegReaders;
+      mbar_init(bar, count);
     }
-    for (int s = 0; s < kKStages; ++s) {
-      mbar_init(k_full(s), 1);
-      mbar_init(k_empty(s), 1);
-    }
-    for (int s = 0; s < kVStages; ++s) {
-      mbar_init(v_full(s), 1);
-      mbar_init(v_empty(s), 1);
-    }
-    mbar_init(ml_full, 4);
-    mbar_init(ml_free, 4);
-    mbar_init(drained, 1);
-    for (int i = 0; i < kSegRing; ++i) {
-      mbar_init(seg_full(i), 1);
-      mbar_init(seg_empty(i), kSegReaders);
-    }
-    *abort_flag = 0;
-    *reinterpret_cast<volatile int *>(smem + kOffMisc + 16) = 0;
+    if (lane == 0) *abort_flag = *reinterpret_cast<volatile int *>(smem + kOffMisc + 16) = 0;
     fence_barrier_init();
   }
   if (warp == kWarpMma) {
@@ -1209,22 +1195,35 @@ tree_combine_kernel(const TreeParams p, const int num_bounds) {
   __shared__ float4 s_o[kCombineWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // CTA x takes the x-th boundary that has something to merge: with few streams the
-  // grid has fewer CTAs than there are boundaries
-  int left = blockIdx.x, index = -1;
-  for (int b0 = 0; b0 < num_bounds && index < 0; b0 += 32) {
-    const bool cut = b0 + lane < num_bounds && p.bounds[b0 + lane].row0 >= 0;
-    unsigned mask = __ballot_sync(0xffffffffu, cut);
-    const int n = __popc(mask);
-    if (left < n) {
-      for (; left > 0; --left) mask &= mask - 1;
-      index = b0 + __ffs(mask) - 1;
-    } else {
-      left -= n;
+  int index = blockIdx.x;
+  if (static_cast<int>(gridDim.x) < num_bounds) {
+    // few streams, fewer CTAs than boundaries: CTA x takes the x-th boundary that has
+    // something to merge
+    int left = blockIdx.x;
+    index = -1;
+    for (int b0 = 0; b0 < num_bounds && index < 0; b0 += 256) {
+      bool cut[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int b = b0 + 32 * j + lane;
+        cut[j] = b < num_bounds && p.bounds[b].row0 >= 0;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        unsigned mask = __ballot_sync(0xffffffffu, cut[j]);
+        const int n = __popc(mask);
+        if (index < 0 && left < n) {
+          for (; left > 0; --left) mask &= mask - 1;
+          index = b0 + 32 * j + __ffs(mask) - 1;
+        } else {
+          left -= n;
+        }
+      }
     }
+    if (index < 0) return;
   }
-  if (index < 0) return;
   const Boundary b = p.bounds[index];
+  if (b.row0 < 0) return;
   const int rows = b.ntok * p.group;
   const bool shared_row = b.last - b.first >= kCombineWarps;
   const int share = shared_row ? kCombineWarps : 1;   // warps on a row
