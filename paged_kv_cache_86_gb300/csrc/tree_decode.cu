@@ -279,26 +279,34 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map
 constexpr uint32_t kSuspendNs = 1000000u;
 constexpr uint32_t kMaxPolls = 1u << 19;
 
-__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, const volatile int *abort) {
-#pragma unroll 1
-  for (uint32_t n = 0; n < kMaxPolls; ++n) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(bar), "r"(parity), "r"(kSuspendNs) : "memory");
-    if (ok) return true;
-    if (*abort) return false;
-  }
-  return false;
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t abort) {
+  uint32_t ok;
+  // two instructions when the phase is over
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 n, f;\n\t"
+      "mov.b32 %0, 1;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.b32 n, 0;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "@p bra DONE;\n\t"
+      "ld.volatile.shared.b32 f, [%4];\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.ne.b32 q, f, 0;\n\t"
+      "setp.ge.or.u32 q, n, %5, q;\n\t"
+      "@!q bra AGAIN;\n\t"
+      "mov.b32 %0, 0;\n\t"
+      "DONE:\n\t}"
+      : "=&r"(ok) : "r"(bar), "r"(parity), "r"(kSuspendNs), "r"(abort), "r"(kMaxPolls) : "memory");
+  return ok != 0;
 }
 
 __device__ __forceinline__ void mbar_arrive_count(uint32_t bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(n) : "memory");
 }
 
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int *abort) {
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
   return __all_sync(0xffffffffu, poll(bar, parity, abort));
 }
 
@@ -360,9 +368,10 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   auto seg_full = [&](int i) { return bar0 + 8u * (kBx + 13 + i); };
   auto seg_empty = [&](int i) { return bar0 + 8u * (kBx + 13 + kSegRing + i); };
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + kOffMisc);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
+  volatile int *abort_word = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
+  const uint32_t abort_flag = base + kOffMisc + 4;
   volatile int *start = reinterpret_cast<volatile int *>(smem + kOffMisc + 8);  // first sequence, tile
-  const volatile int *never = reinterpret_cast<volatile int *>(smem + kOffMisc + 16);  // stays 0
+  const uint32_t never = base + kOffMisc + 16;   // stays 0
   float2 *ml = reinterpret_cast<float2 *>(smem + kOffMl);
   auto seg_at = [&](int i) {
     return reinterpret_cast<volatile Seg *>(smem + kOffSeg + (i % kSegRing) * kSegBytes);
@@ -380,7 +389,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       if (bar >= seg_empty(0) && bar <= seg_empty(kSegRing - 1)) count = kSegReaders;
       mbar_init(bar, count);
     }
-    if (lane == 0) *abort_flag = *reinterpret_cast<volatile int *>(smem + kOffMisc + 16) = 0;
+    if (lane == 0) *abort_word = *reinterpret_cast<volatile int *>(smem + kOffMisc + 16) = 0;
     fence_barrier_init();
   }
   if (warp == kWarpMma) {
@@ -461,7 +470,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   auto sV = [&](int s) { return base + kOffV + s * kTileBytes; };
   auto fail = [&]() {   // a whole warp
     if (lane == 0) {
-      *abort_flag = 1;
+      *abort_word = 1;
       raise_error(p.err, PKV_DEVERR_TIMEOUT);
     }
     __syncwarp();
@@ -789,6 +798,66 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           whole = sg.ctx / kTile;
           i = 0;
         }
+        // ---- two steps at a time inside a segment: whole tiles, neither the first nor
+        // the last PV of an x, so nothing is decided on the way
+        if (x == 0 && i >= 4 && i + 4 <= steps && step >= sg.step0 &&
+            sg.t0 + (two ? (i + 1) >> 1 : i + 1) < whole) {
+          int ps = (mine >> kStageAt) & 3, pp = (mine & kParity) ? 1 : 0;   // V of the owed PVs
+          int parity = (mine & kPParity) ? 1 : 0, parity1 = (other & kPParity) ? 1 : 0;
+          const uint32_t q0 = (sg.qtile & 1) * kTileStep, q1 = ((sg.qtile + (two ? 1 : 0)) & 1) * kTileStep;
+          int stage0 = 0, stage_p0 = 0, stage1 = 0, stage_p1 = 0;
+          auto pv_s = [&](const int y, const uint32_t q, bool wait, bool free, int &p_par) -> bool {
+            if (wait && !poll(v_full(ps), pp, abort_flag)) return false;
+            if (!poll(p_full(y), p_par, abort_flag)) return false;
+            p_par ^= 1;
+            tc_fence_after();
+            const uint64_t dv = desc_at(dv0, ps * kTileStep);
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              umma_bf16_tmem_a(tm + (2 + y) * kTile, tm + y * kTile + kk * 8,
+                               desc_at(dv, kk * (2048 >> 4)), idesc_pv, 1u);
+            if (free) {
+              umma_commit(v_empty(ps));
+              if (++ps == kVStages) {
+                ps = 0;
+                pp ^= 1;
+              }
+            }
+            if (wait && !poll(k_full(ks), kp, abort_flag)) return false;
+            const uint64_t dq = desc_at(dq0, q), dk = desc_at(dk0, ks * kTileStep);
+            constexpr uint32_t idesc = idesc_s | ((kTile >> 3) << 17);
+#pragma unroll
+            for (int kk = 0; kk < kHD / 16; ++kk)
+              umma_bf16(tm + y * kTile, desc_at(dq, kmajor_step(kk)), desc_at(dk, kmajor_step(kk)),
+                        idesc, kk > 0 ? 1u : 0u);
+            umma_commit(s_full(y));
+            (y ? stage1 : stage0) = vs;
+            (y ? stage_p1 : stage_p0) = vp;
+            if (free) {
+              umma_commit(k_empty(ks));
+              if (++ks == kKStages) {
+                ks = 0;
+                kp ^= 1;
+              }
+              if (++vs == kVStages) {
+                vs = 0;
+                vp ^= 1;
+              }
+            }
+            return true;
+          };
+          do {
+            ok = pv_s(0, q0, true, !two, parity) && pv_s(1, q1, !two, true, parity1);
+            i += 2;
+            step += 2;
+          } while (ok && i + 4 <= steps && sg.t0 + (two ? (i + 1) >> 1 : i + 1) < whole);
+          if (!ok) break;
+          mine = (mine & (kOUsed | kOParity)) | (parity ? kPParity : 0) | kTile / 16 |
+                 stage0 << kStageAt | (stage_p0 ? kParity : 0) | (two ? 0 : kFrees);
+          other = (other & (kOUsed | kOParity)) | (parity1 ? kPParity : 0) | kTile / 16 |
+                  stage1 << kStageAt | (stage_p1 ? kParity : 0) | kFrees | (two ? kWaited : 0);
+          continue;
+        }
         if (ended && flush++ == 2) break;
         // ---- what S of the step needs, unless it is left out (step0 is one further) or
         // the walk is over: worked out before the wait for the weights, so that PV and S
@@ -869,7 +938,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         other = t;
       }
       if (!ok) {
-        *abort_flag = 1;
+        *abort_word = 1;
         raise_error(p.err, PKV_DEVERR_TIMEOUT);
       }
       // every issued MMA completes before TMEM is freed
