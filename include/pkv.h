@@ -511,7 +511,8 @@ pkv_status pkv_plan_slots(const int32_t *context_lens, const int32_t *new_lens, 
  * A link that is neither -1 nor an earlier node counts as -1 and sets
  * PKV_DEVERR_TREE; a tree that is longer than max_seqlen_q or ends beyond
  * total_q is skipped and sets PKV_DEVERR_LENGTH. Rows behind the last tree are
- * left as they are. max_seqlen_q <= 65535 * 128.
+ * left as they are. max_seqlen_q <= 65535 * 128. The two outputs must not be
+ * the same array nor one of the inputs (PKV_ERR_ARG).
  *
  * pkv_tree_decode: for every drafted row t of sequence i and query head g, with
  * G = num_q_heads / num_kv_heads and h = g / G,
@@ -522,8 +523,9 @@ pkv_status pkv_plan_slots(const int32_t *context_lens, const int32_t *new_lens, 
  * Any bit pattern is allowed: it need not be a tree, and a row that sees
  * nothing (no bit set, no cached token) is zero. What a row does not see has no
  * part in its result, whatever bits it holds.
- *   out, q          [total_q, num_q_heads, 128] bf16, contiguous; rows behind
- *                   cu_seqlens_q[num_seqs] are left as they are.
+ *   out, q          [total_q, num_q_heads, 128] bf16, contiguous; rows of out
+ *                   behind cu_seqlens_q[num_seqs] are left as they are, and out
+ *                   overlaps none of the inputs.
  *   key, value      the drafted rows, num_kv_heads * 128 contiguous values at
  *                   token strides of their own (multiples of 8 elements).
  *   cu_seqlens_q    [num_seqs + 1] int32, non-decreasing from 0; at most

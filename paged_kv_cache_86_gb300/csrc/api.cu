@@ -743,6 +743,10 @@ pkv_status pkv_tree_masks(const int32_t *parents, const int32_t *cu_seqlens_q,
   if (mask_words < (int64_t(max_seqlen_q) + 31) / 32) return PKV_ERR_ARG;
   if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
   if (!parents || !cu_seqlens_q || !context_lens || !tree_mask || !positions) return PKV_ERR_ARG;
+  // CTAs read the inputs while others write the outputs
+  for (const void *in : {parents, cu_seqlens_q, context_lens})
+    if (tree_mask == in || positions == in) return PKV_ERR_ARG;
+  if (tree_mask == positions) return PKV_ERR_ARG;
   cudaError_t e;
   uint32_t *err = pkv::device_error_word(&e);
   if (!err) return PKV_ERR_CUDA;

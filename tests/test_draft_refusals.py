@@ -96,6 +96,15 @@ def test_masks_status(lib, change, status):
     assert masks(lib, **change) == status
 
 
+@pytest.mark.parametrize("out,name", [("mask", "par"), ("mask", "cu"), ("mask", "ctx"), ("pos", "par"),
+                                      ("pos", "cu"), ("pos", "ctx"), ("pos", "mask")])
+def test_masks_outputs_over_inputs(lib, out, name):
+    """CTAs read what others would be writing."""
+    at = dict(par=A, cu=A + 4096, ctx=A + 8192, mask=A + 12288, pos=A + 16384)
+    at[out] = at[name]
+    assert masks(lib, **at) == ARG
+
+
 def tree(lib, **kw):
     a = dict(out=A, q=A, key=A, value=A, ks=1536, vs=1536, kc=A, vc=A, bt=A, mb=4, ctx=A, cu=A,
              mask=A, words=1, s=2, total=8, mq=8, mc=64, hq=8, hkv=2, d=128, bs=16, nb=4,
