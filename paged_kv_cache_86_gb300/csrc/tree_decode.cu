@@ -53,6 +53,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "pkv_device.cuh"
@@ -1465,13 +1466,18 @@ size_t tree_decode_workspace_bytes(int max_seqlen_q, int num_q_heads, int num_kv
 }
 
 cudaError_t launch_tree_decode(const TreeDecodeArgs &a, cudaStream_t stream) {
-  static std::once_flag attr_once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(attr_once, [] {
-    attr_err = cudaFuncSetAttribute(tree_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kSmemBytes);
-  });
-  if (attr_err != cudaSuccess) return attr_err;
+  // once a device: the attribute belongs to the device's copy of the kernel
+  static std::atomic<uint64_t> attr_set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t dev_bit = uint64_t(1) << (dev & 63);
+  if (dev > 63 || !(attr_set.load() & dev_bit)) {
+    e = cudaFuncSetAttribute(tree_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemBytes);
+    if (e != cudaSuccess) return e;
+    attr_set.fetch_or(dev_bit);
+  }
   const int grid = decode_tc_grid();
   if (grid <= 0) return cudaErrorInvalidValue;
   const int group = a.num_q_heads / a.num_kv_heads;
@@ -1538,7 +1544,7 @@ cudaError_t launch_tree_decode(const TreeDecodeArgs &a, cudaStream_t stream) {
   p.po = reinterpret_cast<float *>(w + ws.po);
   p.err = a.err;
   tree_decode_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, tkp, tvp, tkd, tvd, p);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   // at most one merge a stream and one a range boundary
