@@ -606,28 +606,43 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           const uint32_t full = full0 + 8 * stage;
           uint32_t dst = dst0 + stage * kTileBytes;
           mbar_arrive_expect_tx(full, t.rows * kHD * 2);
-          const int copies = t.rows / t.step, dst_step = t.step * 128;
+          const int copies = t.rows / t.step;
           const CUtensorMap *map = t.whole ? map_whole : map_part;
-          int b = 0;
+          if (boxes) {
+            const int dst_step = t.step * 128;
+            int b = 0;
 #pragma unroll 1
-          for (int part = 0; part < 2; ++part) {     // cached rows, drafts
-            const int end = part == 0 ? min(t.draft, copies) : copies;
-            if (boxes) {
+            for (int part = 0; part < 2; ++part) {     // cached rows, drafts
+              const int end = part == 0 ? min(t.draft, copies) : copies;
 #pragma unroll 1
               for (; b < end; ++b, dst += dst_step) {
                 const int row = rows_smem[b].x;
                 tma_load_3d(dst, map, 0, t.head, row, full);
                 tma_load_3d(dst + kRegion, map, 64, t.head, row, full);
               }
-            } else {
-#pragma unroll 1
-              for (; b < end; ++b, dst += dst_step) {
-                const int4 q = rows_smem[b];
-                tma_gather4(dst, map, t.head * kHD, q, full);
-                tma_gather4(dst + kRegion, map, t.head * kHD + 64, q, full);
-              }
+              map = map_draft;
             }
-            map = map_draft;
+          } else {
+            // 64 gathers a tile: their issue bounds the loader, so the rows of four
+            // are read together (336 -> 251 us for 256 sequences; one at a time waits for
+            // shared memory each time, eight are longer code: 283 us). The drafts begin
+            // at an even one.
+            const int x0 = t.head * kHD, x1 = x0 + 64;
+#pragma unroll 1
+            for (int b = 0; b < copies; b += 4, dst += 4 * 512) {
+              const int4 r0 = rows_smem[b], r1 = rows_smem[b + 1], r2 = rows_smem[b + 2],
+                         r3 = rows_smem[b + 3];
+              const CUtensorMap *ma = b < t.draft ? map : map_draft;
+              const CUtensorMap *mb = b + 2 < t.draft ? map : map_draft;
+              tma_gather4(dst, ma, x0, r0, full);
+              tma_gather4(dst + kRegion, ma, x1, r0, full);
+              tma_gather4(dst + 512, ma, x0, r1, full);
+              tma_gather4(dst + 512 + kRegion, ma, x1, r1, full);
+              tma_gather4(dst + 1024, mb, x0, r2, full);
+              tma_gather4(dst + 1024 + kRegion, mb, x1, r2, full);
+              tma_gather4(dst + 1536, mb, x0, r3, full);
+              tma_gather4(dst + 1536 + kRegion, mb, x1, r3, full);
+            }
           }
         }
         __syncwarp();
