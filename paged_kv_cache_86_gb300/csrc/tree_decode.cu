@@ -1001,11 +1001,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const bool whole = sg.t0 + i < whole_tiles;
         TileKeys tk;
         tk.drafts = 0;
+        int cols = 4;               // 32-column pieces that hold keys, in pairs
         const int32_t *mask_row = p.tree_mask + q_row * p.mask_words;
         if (!whole) {
           tk = tile_keys(sg.ctx, sg.drafts, sg.t0 + i);
           if (live && tk.drafts > 0)
             asm volatile("prefetch.global.L1 [%0];" :: "l"(mask_row + (tk.u0 >> 5)));
+          cols = (tk.rows + 63) >> 6 << 1;
         }
         if (!warp_wait(s_full(x), steps_seen & 1, abort_flag)) {
           ok = false;
@@ -1019,7 +1021,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // a negative or zero scale and the columns the row does not see, back
             // into TMEM, so that what follows is the same code for every tile
 #pragma unroll 1
-            for (int cc = 0; cc < 4; ++cc) {
+            for (int cc = 0; cc < cols; ++cc) {
               uint32_t word = 0xffffffffu;             // the row's visible columns of the 32
               if (!whole) {
                 const int left = tk.cached - 32 * cc;
@@ -1049,7 +1051,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           // instruction fetches cost more than the second read.
           float mt = -INFINITY;
 #pragma unroll 1
-          for (int cc = 0; cc < 4; cc += 2) {
+          for (int cc = 0; cc < cols; cc += 2) {
             float s0[32], s1[32];
             tmem_ld32(ts + cc * 32, s0);
             tmem_ld32(ts + cc * 32 + 32, s1);
@@ -1084,7 +1086,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           const float mc = m_used == -INFINITY ? 0.f : m_used * c;
           float2 rs2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-          for (int cc = 0; cc < 4; cc += 2) {
+          for (int cc = 0; cc < cols; cc += 2) {
             float s0[32], s1[32];
             tmem_ld32(ts + cc * 32, s0);
             tmem_ld32(ts + cc * 32 + 32, s1);
