@@ -513,6 +513,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       const CUtensorMap *map_draft = is_k ? &tm_kd : &tm_vd;
       const int oob_row = p.num_blocks * p.block_size;
       const bool boxes = p.box_rows > 0;
+      const int box_shift = __ffs(p.box_rows) - 1;
       int issued = 0, stage = 0, parity = 1;   // the first round finds every stage empty
       bool ok = true;
       if (lane == 0) {
@@ -530,7 +531,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         int key, off; // first key of the lane's copy, and its place in its block
         int left;     // cached keys from there on
         int rows;     // of the tile, to be loaded
-        int step;     // rows a copy
+        int shift;    // log2 of the rows a copy
         int draft;    // first copy of drafts
         int head;     // KV head; -1: no tile
         bool whole;
@@ -550,9 +551,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         t.head = sg.head;
         t.whole = tk.cached == kTile;
         t.rows = tk.rows;
-        t.step = !boxes ? 4 : t.whole ? p.box_rows : 8;
-        t.draft = tk.drafts > 0 ? tk.at / t.step : kTile;
-        const int k0 = t.step * lane;
+        t.shift = !boxes ? 2 : t.whole ? box_shift : 3;
+        t.draft = tk.drafts > 0 ? tk.at >> t.shift : kTile;
+        const int k0 = lane << t.shift;
         t.key = j * kTile + k0;
         t.drafted = tk.drafts > 0 && k0 >= tk.at;
         if (t.drafted) {
@@ -579,8 +580,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       };
       int4 *rows_smem = reinterpret_cast<int4 *>(smem + kOffRows) + (is_k ? 0 : 32);
       Rows next;
-      ok = look_up(next);
-      while (ok && next.head >= 0) {
+      next.head = -1;
+      next.drafted = true;
+      do {                                   // the first turn only looks up
         Rows t = next;
         if (!t.drafted) {
           auto row = [&](int blk, int e) {   // of the lane's e-th key
@@ -597,7 +599,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             t.r.w = row(t.r.w, 3);
           }
         }
-        ok = look_up(next) && warp_wait(empty0 + 8 * stage, parity, abort_flag);
+        ok = look_up(next);
+        if (t.head < 0) continue;
+        ok = ok && warp_wait(empty0 + 8 * stage, parity, abort_flag);
         if (!ok) break;
         // one lane issues the copies, from the rows of all lanes in shared memory
         rows_smem[lane] = t.r;
@@ -606,10 +610,10 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           const uint32_t full = full0 + 8 * stage;
           uint32_t dst = dst0 + stage * kTileBytes;
           mbar_arrive_expect_tx(full, t.rows * kHD * 2);
-          const int copies = t.rows / t.step;
+          const int copies = t.rows >> t.shift;
           const CUtensorMap *map = t.whole ? map_whole : map_part;
           if (boxes) {
-            const int dst_step = t.step * 128;
+            const int dst_step = 128 << t.shift;
             int b = 0;
 #pragma unroll 1
             for (int part = 0; part < 2; ++part) {     // cached rows, drafts
@@ -651,8 +655,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           stage = 0;
           parity ^= 1;
         }
-      }
+      } while (ok && next.head >= 0);
       if (!ok) fail();
+#pragma unroll 1
       for (int j = max(0, issued - stages); j < issued; ++j)   // the last copies must land
         warp_wait(full0 + 8 * (j % stages), (j / stages) & 1, never);
     } else if (warp == kWarpWalk) {
@@ -710,15 +715,6 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           step += two ? 2 * tiles : tiles;
           off += tiles;
           left -= tiles;
-          // the stream that the range start cuts is merged at its first cut
-          if (first_seg && sg.t0 > 0 && range_of(lo - sg.t0) == bid - 1) {
-            bd.row0 = sg.q0 + sg.tok0;
-            bd.ntok = sg.ntok;
-            bd.head = head;
-            bd.first = bid - 1;
-            bd.last = range_of(lo - sg.t0 + nt - 1);
-          }
-          first_seg = false;
         }
         ok = n < kSegRing || warp_wait(seg_empty(n % kSegRing), ((n / kSegRing) - 1) & 1, abort_flag);
         if (!ok) break;
@@ -742,12 +738,13 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         __syncwarp();
         ++n;
         // Q tiles: box_tokens * group rows a box
+#pragma unroll 1
         for (int x = 0; more && x < (two ? 2 : 1); ++x) {
           const int s = qtiles & 1, round = qtiles >> 1;
           ok = round == 0 || warp_wait(q_empty(s), (round - 1) & 1, abort_flag);
           if (!ok) break;
           const int tok = min(p.tile_tokens, sg.ntok - x * p.tile_tokens);
-          const int boxes = (tok + p.box_tokens - 1) / p.box_tokens;
+          const int boxes = (tok + p.box_tokens - 1) >> (__ffs(p.box_tokens) - 1);
           const int box_rows = p.box_tokens * p.group;
           if (elect_one()) mbar_arrive_expect_tx(q_full(s), boxes * box_rows * kHD * 2);
           uint32_t dst = sQ + s * kTileBytes;
@@ -764,9 +761,23 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           ++q_issued;
           ++qtiles;
         }
+        // the stream that the range start cuts is merged at its first cut (worked out
+        // here, when the other roles have their work)
+        if (first_seg && sg.t0 > 0) {
+#pragma unroll 1
+          for (int e = 0; e < 2; ++e) {
+            const int r = range_of(lo - sg.t0 + (e ? nt - 1 : 0));
+            if (e) bd.last = r; else bd.first = r;
+          }
+          bd.ntok = sg.ntok;
+          bd.head = head;
+          if (bd.first == bid - 1) bd.row0 = sg.q0 + sg.tok0;
+        }
+        first_seg = false;
       }
       if (lane == 0) p.bounds[bid] = bd;
       if (!ok) fail();
+#pragma unroll 1
       for (int s = max(0, q_issued - 2); s < q_issued; ++s)   // drain
         warp_wait(q_full(s & 1), (s >> 1) & 1, never);
     } else if (warp == kWarpMma) {
