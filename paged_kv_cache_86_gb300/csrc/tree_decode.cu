@@ -39,13 +39,27 @@
 // core's operand type asks for. O is rescaled only when a row's maximum grows by
 // over 2^8.
 //
-// Loads (warp 8 K, warp 10 V, warp 11 Q and the walk): TMA boxes when the block size is a multiple of 8 (whole
-// tiles in boxes of up to a block, partial tiles and drafts in boxes of 8 rows),
-// else TMA row gathers, four rows an instruction. Rows of a tile that are no key
-// of the sequence may be other rows of a block or other sequences' drafts, and
-// drafts that a row does not see may hold anything: their scores are masked, and
-// V values among them that are not finite are set to zero in shared memory (0 * NaN
-// is not 0), those of drafts to be added back at the end for the rows that see them.
+// Loads (warp 8 K, warp 10 V, warp 11 Q and the walk; warp 9 issues the MMAs): TMA boxes
+// when the block size is a multiple of 8 (whole tiles in boxes of up to a block, partial
+// tiles and drafts in boxes of 8 rows), else TMA row gathers, four rows an instruction: 256
+// ragged sequences take 227 us at block size 16, 254 at 12 and at 1. Rows of a tile that
+// are no key of the sequence may be other rows of a block or other sequences' drafts, and
+// drafts that a row does not see may hold anything: their scores are masked, and V values
+// among them that are not finite are set to zero in shared memory (0 * NaN is not 0),
+// those of drafts to be added back at the end for the rows that see them.
+//
+// What a tile costs besides its loads is instructions, fetched by eleven warps that each
+// do something else: the kernel follows its code size more than its arithmetic (256 ragged
+// sequences: 297 us at 129 KB of code, 251 at 72 KB; 225 -> 221 us from 95 to 82 KB, 233 us
+// when the two softmax passes are unrolled). Hence one copy of each role for both x, short
+// loops, elected lanes and waits that hardware suspends.
+//
+// Measured, attention and combine, with floors of bytes at 6.78 TB/s (bf16 products at 1912
+// TFLOP/s): 64 sequences U[128, 4096] x 16 drafts, 16 / 8 heads 96 us (81); 256 lognormal
+// sequences x U[1, 32] drafts, 32 / 8 heads 222-226 us (194; DRAM traffic 1.29 GB read, the
+// tensor pipe 30 % active); 8 x 32768 cached tokens x 64 drafts, 32 / 8 heads 212-217 us
+// (160, 144 by products), 238 us at the 1.7 GHz that the power limit leaves in long runs;
+// one sequence of 5000 tokens 14 us (1). The combine is 4 to 9 us of it.
 //
 // Every wait is bounded; on a timeout the CTA records PKV_DEVERR_TIMEOUT,
 // drains its copies and MMAs, frees its TMEM and exits.
@@ -67,9 +81,10 @@ constexpr int kTile = 128;
 constexpr int kHD = 128;
 constexpr int kRegion = 16384;       // 128 rows x 64 dims, 128-byte swizzle
 constexpr int kTileBytes = 2 * kRegion;
-// a V tile waits for its weights, a K tile for nothing
-constexpr int kKStages = 2;
-constexpr int kVStages = 3;
+// Five tiles fit. 64 sequences of 16 drafts: 96.0 us with three of K, 97.9 with three of V;
+// 1 x 32768 33.7 / 34.2, 8 x 64 drafts 216.8 / 216.3, 256 ragged sequences the same.
+constexpr int kKStages = 3;
+constexpr int kVStages = 2;
 constexpr int kThreads = 384;        // softmax 0 (warps 0-3), softmax 1 (4-7), loaders + MMA (8-11)
 constexpr int kWarpK = 8, kWarpMma = 9, kWarpV = 10, kWarpWalk = 11;
 constexpr int kTmemCols = 512;
@@ -244,10 +259,9 @@ __device__ __forceinline__ float max32(const float (&v)[32]) {
   return fmaxf(fmax3(a[0], a[1], a[2]), a[3]);
 }
 
-// One lane of a converged warp. Operands of TMA copies and MMAs live in uniform
-// registers: inside `if (elect_one())`, in warp-uniform control flow, the compiler
-// keeps them there, and an MMA costs 4 instructions; under `lane == 0` it costs 10
-// and a copy with operands that differ by lane a loop over the lanes.
+// One lane of a converged warp. Copies and MMAs take operands that are the same for the
+// warp: inside `if (elect_one())`, in warp-uniform control flow, the compiler knows that
+// they are, under `lane == 0` it does not (64 sequences 136 -> 117 us, 256 372 -> 289 us).
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(
@@ -273,16 +287,17 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
-// Wait for the phase with the given parity: suspended in hardware for up to
-// kSuspendNs at a time (it measured up to 4 us), because a dozen warps that poll
-// take shared-memory cycles from the MMAs' operands. Gives up when *abort becomes non-zero or after
-// kMaxPolls polls.
+// Wait for the phase with the given parity: suspended in hardware for up to kSuspendNs
+// at a time (it measured up to 4 us), because a dozen warps that poll take
+// shared-memory cycles from the MMAs' operands (256 sequences: 361-429 us polling, 327
+// suspended). Gives up when *abort becomes non-zero or after kMaxPolls polls, two
+// seconds or so.
 constexpr uint32_t kSuspendNs = 1000000u;
 constexpr uint32_t kMaxPolls = 1u << 19;
 
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t abort) {
   uint32_t ok;
-  // two instructions when the phase is over
+  // nothing but the first try when the phase is over
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .b32 n, f;\n\t"
       "mov.b32 %0, 1;\n\t"
@@ -1197,7 +1212,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           __nv_bfloat16 *orow = p.out + (q_row * p.num_q_heads + sg.head * p.group + r_head) * kHD;
           const int64_t rec = static_cast<int64_t>(sg.slot) * p.rows_cap +
                               tok_x * p.group + row;   // partial record's row
-          if (sg.slot >= 0 && live) 
+          if (sg.slot >= 0 && live)
             p.ml[rec] = make_float2(m_all == -INFINITY ? -INFINITY : m_all * c, l_sum);
 #pragma unroll 1
           for (int cc = 0; cc < 4; ++cc) {
@@ -1283,7 +1298,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // of a row. A stream's pieces lie in CTAs first .. last, in record 2c + 1 of the
 // first (it starts there) and 2c of the others. A warp merges a row of up to
 // eight pieces; with more, the CTA's eight warps share the row's pieces, so that
-// no warp waits for more than a few loads in turn.
+// no warp waits for more than a few loads in turn (one sequence of 5000 tokens, 38
+// pieces a row: 14.4 us shared, 22.0 not; 256 sequences, two or three pieces: 254 us
+// shared, 225 not). Bound by the latency of that chain: lengths, pieces, output.
 constexpr int kCombineWarps = 8;
 constexpr int kBatch = 6;
 
@@ -1296,7 +1313,7 @@ tree_combine_kernel(const TreeParams p, const int num_bounds) {
   int index = blockIdx.x;
   if (static_cast<int>(gridDim.x) < num_bounds) {
     // few streams, fewer CTAs than boundaries: CTA x takes the x-th boundary that has
-    // something to merge
+    // something to merge (searched for only then: it costs 1 us of 97)
     int left = blockIdx.x;
     index = -1;
     for (int b0 = 0; b0 < num_bounds && index < 0; b0 += 256) {
@@ -1580,7 +1597,8 @@ cudaError_t launch_tree_decode(const TreeDecodeArgs &a, cudaStream_t stream) {
                           ((a.max_seqlen_q + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens));
   const int merges = streams < grid ? static_cast<int>(streams) : grid;
   // four CTAs an SM in all (all resident at once: with 32 a merge the launch alone
-  // took 8 us), shared among the merges; more than one a row helps nobody
+  // took 8 us), shared among the merges; more than one a row helps nobody. 64 x 16
+  // drafts: 109 us with one an SM, 105.7 with two, 104.5 with four, 104.7 with eight
   int share = 4 * grid / merges;
   share = share < p.rows_cap ? share : p.rows_cap;
   cfg.gridDim = dim3(merges, share > 0 ? share : 1);
