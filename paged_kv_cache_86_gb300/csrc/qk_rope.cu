@@ -18,10 +18,11 @@
 // access is 16 bytes. A warp stays with one token, so the angles are loaded
 // once and serve all the rows it handles.
 //
-// Measured, 32 / 8 heads of 128 with the store: 16384 tokens 74.5 us = 5.5 TB/s (its
-// 411 MB at 6.78 TB/s: 60.6 us), 512 tokens 5.2 us, 8 tokens 2.4 us (the launch). Two rows' loads
-// in flight a lane, or loads and stores that evict first, gave 72.5 and 71.2 us; not
-// kept: the first costs the small calls, the second evicts what the next kernel reads.
+// Measured, 32 / 8 heads of 128 with the store: 16384 tokens 69.2 us = 5.9 TB/s (its
+// 411 MB at 6.78 TB/s: 60.6 us), 512 tokens 4.1 us, 8 tokens 2.5 us (the launch). What
+// counts is warps in flight: 28 an SM (72 registers) took 74.5 us, 24 85; the next row
+// loaded ahead costs registers and took 92. Stores that evict first save 3 us more but
+// evict what the next kernel reads.
 #include <cuda_runtime.h>
 
 #include "pkv_device.cuh"
@@ -54,8 +55,10 @@ __device__ __forceinline__ uint4 pack(const Chunk &c) {
                     float2_to_bf16x2(c.v[4], c.v[5]), float2_to_bf16x2(c.v[6], c.v[7]));
 }
 
-// kD: head_dim. kInter: interleaved pairs.
-template <int kD, bool kInter>
+// kD: head_dim. kInter: interleaved pairs. kMany: the angles are read again for each row
+// (from L1) instead of held in 16 registers, so that 36 warps an SM are resident
+// instead of 32.
+template <int kD, bool kInter, bool kMany>
 __global__ void __launch_bounds__(kWarps * 32) qk_rope_kernel(const QkRopeArgs a) {
   constexpr int kLanes = kD / 16;          // lanes of a row
   constexpr int kRows = 32 / kLanes;       // rows a warp handles at once
@@ -82,23 +85,21 @@ __global__ void __launch_bounds__(kWarps * 32) qk_rope_kernel(const QkRopeArgs a
   // the lane's two chunks of 8 values, in elements of the row
   const int c0 = (l < turn ? l : 2 * l) * 8;
   const int c1 = l < turn ? c0 + turn * 8 : c0 + 8;
+  const float *angles = a.cos_sin + static_cast<int64_t>(pos) * a.rotary_dim;
   float cs[8], sn[8];
-  if (l < turn) {
-    const float *row = a.cos_sin + static_cast<int64_t>(pos) * a.rotary_dim;
+  auto load_angles = [&]() {
     const int half = a.rotary_dim / 2;
     // neox: pair i is (c0 + i, c1 + i); interleaved: pairs c0/2 + 0..3 and c1/2 + 0..3
     const int p0 = kInter ? c0 / 2 : c0, p1 = kInter ? c1 / 2 : c0 + 4;
-    *reinterpret_cast<float4 *>(cs) = __ldg(reinterpret_cast<const float4 *>(row + p0));
-    *reinterpret_cast<float4 *>(cs + 4) = __ldg(reinterpret_cast<const float4 *>(row + p1));
-    *reinterpret_cast<float4 *>(sn) = __ldg(reinterpret_cast<const float4 *>(row + half + p0));
-    *reinterpret_cast<float4 *>(sn + 4) = __ldg(reinterpret_cast<const float4 *>(row + half + p1));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      cs[i] = 1.f;
-      sn[i] = 0.f;
-    }
-  }
+    *reinterpret_cast<float4 *>(cs) = __ldg(reinterpret_cast<const float4 *>(angles + p0));
+    *reinterpret_cast<float4 *>(cs + 4) = __ldg(reinterpret_cast<const float4 *>(angles + p1));
+    *reinterpret_cast<float4 *>(sn) = __ldg(reinterpret_cast<const float4 *>(angles + half + p0));
+    *reinterpret_cast<float4 *>(sn + 4) =
+        __ldg(reinterpret_cast<const float4 *>(angles + half + p1));
+  };
+  if (!kMany && l < turn) load_angles();
+  // the lanes of this lane's row
+  const unsigned row_lanes = ((1u << kLanes) - 1u) << (sub * kLanes);
   const int heads = a.num_q_heads + a.num_kv_heads;
   const int rows = heads + (a.v != nullptr ? a.num_kv_heads : 0);
   for (int r0 = part * kRows; r0 < rows; r0 += a.parts * kRows) {
@@ -124,14 +125,19 @@ __global__ void __launch_bounds__(kWarps * 32) qk_rope_kernel(const QkRopeArgs a
       x0 = *reinterpret_cast<const uint4 *>(src + c0);
       x1 = *reinterpret_cast<const uint4 *>(src + c1);
     }
-    Chunk u = unpack(x0), z = unpack(x1);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss += u.v[i] * u.v[i] + z.v[i] * z.v[i];
-#pragma unroll
-    for (int off = kLanes / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
     if (dst == nullptr) continue;
+    if (r >= heads || (w == nullptr && l >= turn)) {   // bit for bit
+      *reinterpret_cast<uint4 *>(dst + c0) = x0;
+      *reinterpret_cast<uint4 *>(dst + c1) = x1;
+      continue;
+    }
+    Chunk u = unpack(x0), z = unpack(x1);
     if (w != nullptr) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss += u.v[i] * u.v[i] + z.v[i] * z.v[i];
+#pragma unroll
+      for (int off = kLanes / 2; off >= 1; off >>= 1) ss += __shfl_xor_sync(row_lanes, ss, off);
       const float inv = rsqrtf(ss * (1.f / kD) + a.eps);
       const Chunk w0 = unpack(__ldg(reinterpret_cast<const uint4 *>(w + c0)));
       const Chunk w1 = unpack(__ldg(reinterpret_cast<const uint4 *>(w + c1)));
@@ -141,7 +147,8 @@ __global__ void __launch_bounds__(kWarps * 32) qk_rope_kernel(const QkRopeArgs a
         z.v[i] *= inv * w1.v[i];
       }
     }
-    if (r < heads && l < turn) {
+    if (l < turn) {
+      if (kMany) load_angles();
       if constexpr (kInter) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -160,18 +167,25 @@ __global__ void __launch_bounds__(kWarps * 32) qk_rope_kernel(const QkRopeArgs a
         }
       }
     }
-    const bool as_is = r >= heads || (w == nullptr && l >= turn);
-    *reinterpret_cast<uint4 *>(dst + c0) = as_is ? x0 : pack(u);
-    *reinterpret_cast<uint4 *>(dst + c1) = as_is ? x1 : pack(z);
+    *reinterpret_cast<uint4 *>(dst + c0) = pack(u);
+    *reinterpret_cast<uint4 *>(dst + c1) = pack(z);
   }
 }
 
-template <int kD>
+template <int kD, bool kMany>
 void launch(const QkRopeArgs &a, unsigned grid, cudaStream_t stream) {
   if (a.interleaved)
-    qk_rope_kernel<kD, true><<<grid, kWarps * 32, 0, stream>>>(a);
+    qk_rope_kernel<kD, true, kMany><<<grid, kWarps * 32, 0, stream>>>(a);
   else
-    qk_rope_kernel<kD, false><<<grid, kWarps * 32, 0, stream>>>(a);
+    qk_rope_kernel<kD, false, kMany><<<grid, kWarps * 32, 0, stream>>>(a);
+}
+
+template <int kD>
+void launch(const QkRopeArgs &a, unsigned grid, bool many, cudaStream_t stream) {
+  if (many)
+    launch<kD, true>(a, grid, stream);
+  else
+    launch<kD, false>(a, grid, stream);
 }
 
 }  // namespace
@@ -184,21 +198,36 @@ cudaError_t launch_qk_rope(QkRopeArgs a, int head_dim, cudaStream_t stream) {
   // With few tokens a token's rows are spread over up to one warp a pass, until
   // kWarpsPerSm warps an SM are busy; with many, a warp takes all the rows of its
   // token and loads its angles once. 32 / 8 heads, us at 8 / 512 / 1024 / 2048 / 16384
-  // tokens: 2.4 / 5.2 / 5.6 / 8.6 / 74.5; never spread 7.6 / 8.1 / 8.8 / 10.7 / 74.5; always
-  // 2.4 / 5.2 / 7.2 / 11.9 / 115.6; up to 16 warps 2.4 / 4.8 / 6.8 / 10.7 / 74.6, up to
-  // 64 2.5 / 5.1 / 7.3 / 9.3 / 74.5.
+  // tokens, with 28 warps resident: 2.4 / 5.2 / 5.6 / 8.6 / 74.5; never spread 7.6 / 8.1 /
+  // 8.8 / 10.7 / 74.5; always 2.4 / 5.2 / 7.2 / 11.9 / 115.6; up to 16 warps an SM 2.4 / 4.8 /
+  // 6.8 / 10.7 / 74.6, up to 64 2.5 / 5.1 / 7.3 / 9.3 / 74.5.
   const int rows = a.num_q_heads + (a.v != nullptr ? 2 : 1) * a.num_kv_heads;
   const int passes = (rows + 512 / head_dim - 1) / (512 / head_dim);
   const int64_t want = static_cast<int64_t>(sm_count(dev)) * kWarpsPerSm;
   int64_t parts = want / a.num_tokens;
   parts = parts < 1 ? 1 : parts > passes ? passes : parts;
+  // More tokens than resident warps: the last wave of warps may be nearly empty, so of one
+  // warp a token, two, and one with kMany (36 resident instead of 32) the one is taken
+  // whose waves cost least, by what a wave measured: 32 / 8 heads, us at 5200 / 6000 /
+  // 8192 / 12000 / 16384 / 20000 tokens: one 31.8 / 34.0 / 38.7 / 54.9 / 72.6 / 88.2, two
+  // 27.9 / 30.3 / 39.6 / 54.0 / 72.1 / 87.9, kMany 24.4 / 35.5 / 39.9 / 57.3 / 69.2 / 84.4. Few passes
+  // are not divided: the angles would be loaded for too few rows.
+  bool many = false;
+  if (a.num_tokens > want) {
+    auto waves = [](int64_t warps, int64_t resident) { return (warps + resident - 1) / resident; };
+    const int64_t one = 200 * waves(a.num_tokens, want);
+    const int64_t two = passes < 8 ? one : 103 * waves(2 * int64_t(a.num_tokens), want);
+    const int64_t more = 229 * waves(a.num_tokens, want * 9 / 8);
+    many = more < one && more <= two;
+    if (!many && two < one) parts = 2;
+  }
   a.parts = static_cast<int>(parts);
   const int64_t warps = static_cast<int64_t>(a.num_tokens) * a.parts;
   const unsigned grid = static_cast<unsigned>((warps + kWarps - 1) / kWarps);
   if (warps > (static_cast<int64_t>(1) << 33)) return cudaErrorInvalidValue;
-  if (head_dim == 64) launch<64>(a, grid, stream);
-  else if (head_dim == 128) launch<128>(a, grid, stream);
-  else launch<256>(a, grid, stream);
+  if (head_dim == 64) launch<64>(a, grid, many, stream);
+  else if (head_dim == 128) launch<128>(a, grid, many, stream);
+  else launch<256>(a, grid, many, stream);
   return cudaGetLastError();
 }
 

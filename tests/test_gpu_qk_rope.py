@@ -113,6 +113,34 @@ def test_store_writes_the_slots_and_nothing_else(tokens, hq, hkv, d, rotary, int
     assert bool((k[rest] == 3.0).all()) and bool((v[rest] == 4.0).all())
 
 
+@pytest.mark.parametrize("tokens,hq,hkv,d,rotary,inter,qn,kn", [
+    # more tokens than warps fit the GPU: one warp a token in fewer, fuller waves, or two
+    (5003, 3, 1, 64, 64, False, True, True),
+    (5003, 2, 1, 256, 128, True, False, True),
+    (10001, 4, 2, 128, 64, True, True, False),
+    (10001, 4, 2, 128, 128, False, False, False),
+    (6007, 14, 2, 256, 256, False, True, True),
+    (6007, 28, 4, 128, 128, True, True, True),
+])
+def test_more_tokens_than_resident_warps(tokens, hq, hkv, d, rotary, inter, qn, kn):
+    x, g = inputs(tokens, hq, hkv, d, rotary, qn, kn, seed=12)
+    kc = torch.full((tokens // 16 + 2, 16, hkv, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    vc = torch.full_like(kc, 4.0)
+    slots = torch.randperm(tokens + 1, generator=torch.Generator().manual_seed(4))[:tokens]
+    q = pkv.qk_norm_rope_store(g["q"], g["k"], g["v"], kc, vc, i32(slots), g["pos"], g["table"],
+                               g["qw"], g["kw"], 1e-6, inter)
+    q2, k2 = pkv.qk_norm_rope(g["q"], g["k"], g["pos"], g["table"], g["qw"], g["kw"], 1e-6, inter)
+    assert pkv.get_device_errors() == 0
+    assert_rows(q, reference(x["q"], x["qw"], 1e-6, x["pos"], x["table"], inter))
+    assert_rows(k2, reference(x["k"], x["kw"], 1e-6, x["pos"], x["table"], inter))
+    at = slots.cuda()
+    assert torch.equal(q, q2) and torch.equal(kc.flatten(0, 1)[at], k2)
+    assert torch.equal(vc.flatten(0, 1)[at], g["v"])
+    rest = torch.ones(kc.shape[0] * 16, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert bool((kc.flatten(0, 1)[rest] == 3.0).all()) and bool((vc.flatten(0, 1)[rest] == 4.0).all())
+
+
 def test_in_place_and_strided_outputs():
     x, g = inputs(40, 8, 2, 128, 128, True, True, seed=7)
     q, k = pkv.qk_norm_rope(g["q"], g["k"], g["pos"], g["table"], g["qw"], g["kw"])
