@@ -1303,6 +1303,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // shared, 225 not). Bound by the latency of that chain: lengths, pieces, output.
 constexpr int kCombineWarps = 8;
 constexpr int kBatch = 6;
+constexpr int kPieces = 3;
 
 __global__ void __launch_bounds__(kCombineWarps * 32, 4)
 tree_combine_kernel(const TreeParams p, const int num_bounds) {
@@ -1345,6 +1346,54 @@ tree_combine_kernel(const TreeParams p, const int num_bounds) {
   const int part = shared_row ? warp : 0;
   const int row0 = shared_row ? blockIdx.y : blockIdx.y * kCombineWarps + warp;
   const int row_step = gridDim.y * (shared_row ? 1 : kCombineWarps);
+  auto finish = [&](int row, float l, float4 o) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int tok = row / p.group, g = row - tok * p.group;
+    uint2 w;
+    w.x = float2_to_bf16x2(o.x * inv, o.y * inv);
+    w.y = float2_to_bf16x2(o.z * inv, o.w * inv);
+    reinterpret_cast<uint2 *>(p.out + ((static_cast<int64_t>(b.row0) + tok) * p.num_q_heads +
+                                       b.head * p.group + g) * kHD)[lane] = w;
+  };
+  if (b.last - b.first < kPieces) {
+    // few pieces: two rows' loads in flight
+    for (int row = row0; row < rows; row += 2 * row_step) {
+      float2 ml[2][kPieces];
+      float4 v[2][kPieces];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          const int c = min(b.first + j, b.last);
+          const int64_t rec = static_cast<int64_t>(2 * c + (c == b.first ? 1 : 0)) * p.rows_cap +
+                              min(row + e * row_step, rows - 1);
+          ml[e][j] = p.ml[rec];
+          v[e][j] = reinterpret_cast<const float4 *>(p.po + rec * kHD)[lane];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j)
+          if (b.first + j <= b.last) m = fmaxf(m, ml[e][j].x);
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          // nothing of a piece of which the row sees nothing
+          if (b.first + j > b.last || ml[e][j].x == -INFINITY) continue;
+          const float w = ex2(ml[e][j].x - m);
+          l += w * ml[e][j].y;
+          o.x += w * v[e][j].x;
+          o.y += w * v[e][j].y;
+          o.z += w * v[e][j].z;
+          o.w += w * v[e][j].w;
+        }
+        if (row + e * row_step < rows) finish(row + e * row_step, l, o);
+      }
+    }
+    return;
+  }
   for (int row = row0; row < rows; row += row_step) {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1406,13 +1455,7 @@ tree_combine_kernel(const TreeParams p, const int num_bounds) {
       __syncthreads();
       if (warp != 0) continue;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int tok = row / p.group, g = row - tok * p.group;
-    uint2 w;
-    w.x = float2_to_bf16x2(o.x * inv, o.y * inv);
-    w.y = float2_to_bf16x2(o.z * inv, o.w * inv);
-    reinterpret_cast<uint2 *>(p.out + ((static_cast<int64_t>(b.row0) + tok) * p.num_q_heads +
-                                       b.head * p.group + g) * kHD)[lane] = w;
+    finish(row, l, o);
   }
 }
 
