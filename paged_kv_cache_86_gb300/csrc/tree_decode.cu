@@ -799,7 +799,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       // ---------------------------------------------------------- MMA issuer
       // One elected lane runs the whole role. Its instructions are on the path of every
       // tile, so there are few: one copy for both x, ring positions counted up,
-      // descriptors that differ by adds, waits without a vote.
+      // descriptors that differ by adds, waits without a vote. MMAs are issued by twos: the
+      // tensor core takes longer than a turn of the loop, and the code is 2 KB shorter
+      // than unrolled.
       if (elect_one()) {
       constexpr uint32_t idesc_s = umma_idesc_bf16(kTile, 0, false);            // N is added
       constexpr uint32_t idesc_pv = umma_idesc_bf16(kTile, kHD, true);          // B (V) MN-major
@@ -854,7 +856,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             p_par ^= 1;
             tc_fence_after();
             const uint64_t dv = desc_at(dv0, ps * kTileStep);
-#pragma unroll
+#pragma unroll 2
             for (int kk = 0; kk < kTile / 16; ++kk)
               umma_bf16_tmem_a(tm + (2 + y) * kTile, tm + y * kTile + kk * 8,
                                desc_at(dv, kk * (2048 >> 4)), idesc_pv, 1u);
@@ -868,7 +870,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (wait && !poll(k_full(ks), kp, abort_flag)) return false;
             const uint64_t dq = desc_at(dq0, q), dk = desc_at(dk0, ks * kTileStep);
             constexpr uint32_t idesc = idesc_s | ((kTile >> 3) << 17);
-#pragma unroll
+#pragma unroll 2
             for (int kk = 0; kk < kHD / 16; ++kk)
               umma_bf16(tm + y * kTile, desc_at(dq, kmajor_step(kk)), desc_at(dk, kmajor_step(kk)),
                         idesc, kk > 0 ? 1u : 0u);
@@ -933,7 +935,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           if (!ok) break;
           tc_fence_after();
           if (mmas == kTile / 16) {
-#pragma unroll
+#pragma unroll 2
             for (int kk = 0; kk < kTile / 16; ++kk)
               umma_bf16_tmem_a(to, ts + kk * 8, desc_at(dv, kk * (2048 >> 4)), idesc_pv,
                                kk > 0 || !(w & kFresh));
@@ -952,7 +954,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                (k_there || poll(k_full(ks), kp, abort_flag));
           if (!ok) break;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 2
           for (int kk = 0; kk < kHD / 16; ++kk)
             umma_bf16(ts, desc_at(dq, kmajor_step(kk)), desc_at(dk, kmajor_step(kk)), idesc,
                       kk > 0 ? 1u : 0u);
@@ -1303,7 +1305,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // shared, 225 not). Bound by the latency of that chain: lengths, pieces, output.
 constexpr int kCombineWarps = 8;
 constexpr int kBatch = 6;
-constexpr int kPieces = 3;
+constexpr int kPieces = 4;
 
 __global__ void __launch_bounds__(kCombineWarps * 32, 4)
 tree_combine_kernel(const TreeParams p, const int num_bounds) {
