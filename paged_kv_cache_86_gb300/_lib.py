@@ -10,6 +10,7 @@ missing, loading raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple
@@ -842,6 +843,12 @@ def tree_decode_workspace_size(max_seqlen_q: int, num_q_heads: int, num_kv_heads
                                                      head_dim))
 
 
+@functools.lru_cache(maxsize=256)
+def _tree_workspace(index: int, max_seqlen_q: int, hq: int, hkv: int, d: int) -> int:
+    """The size on device `index`, the current one; at least 256."""
+    return max(load().pkv_tree_decode_workspace_size(max_seqlen_q, hq, hkv, d), 256)
+
+
 def tree_decode(q, key, value, k_cache, v_cache, block_tables, context_lens, cu_seqlens_q,
                 tree_mask, scale: float, max_seqlen_q: int, max_context_len: int | None = None,
                 out=None, workspace=None, stream=None) -> torch.Tensor:
@@ -894,11 +901,10 @@ def tree_decode(q, key, value, k_cache, v_cache, block_tables, context_lens, cu_
     lib = _lib or load()
     ctx, st = _enter(index, stream)
     try:
-        out = _out_like(out, q) if out is not None else torch.empty(q.shape, dtype=_BF16,
-                                                                    device=q.device)
+        out = _out_like(out, q) if out is not None else torch.empty_like(q)
         if workspace is None:
-            need = lib.pkv_tree_decode_workspace_size(max_seqlen_q, hq, hkv, d)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(_tree_workspace(index, int(max_seqlen_q), hq, hkv, d),
+                                    dtype=torch.uint8, device=q.device)
         elif workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous, on q's device")
         _check(lib.pkv_tree_decode(
