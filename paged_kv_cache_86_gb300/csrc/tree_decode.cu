@@ -417,11 +417,14 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   // ---- the CTA's range: tiles of all sequences (one KV head), counted by every
   // CTA itself; thread t counts sequences [t * per, (t + 1) * per)
   const int pair_tokens = 2 * p.tile_tokens;
+  auto row_groups = [&](int drafts) {   // one but for wide trees
+    return drafts <= pair_tokens ? 1 : (drafts + pair_tokens - 1) / pair_tokens;
+  };
   const int per = (p.num_seqs + kThreads - 1) / kThreads;
   auto seq_cost = [&](int i, bool report) {
     int ctx, drafts, q0;
     if (!seq_lengths(p, i, &ctx, &drafts, &q0) && report) raise_error(p.err, PKV_DEVERR_LENGTH);
-    return drafts == 0 ? 0 : tree_tiles(ctx, drafts) * ((drafts + pair_tokens - 1) / pair_tokens);
+    return drafts == 0 ? 0 : tree_tiles(ctx, drafts) * row_groups(drafts);
   };
   int mine = 0;
   for (int i = threadIdx.x * per; i < min(p.num_seqs, (static_cast<int>(threadIdx.x) + 1) * per); ++i)
@@ -451,9 +454,12 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   const int ctas = min(static_cast<int>(gridDim.x), max(units, 1));
   const int bid = static_cast<int>(blockIdx.x);
   const int per_cta = units / ctas, extra = units - per_cta * ctas;
+  // n / ctas is the high word of n * ceil(2^32 / ctas) while n * ctas < 2^32; here n < ctas^2,
+  // and a GPU has below 1600 SMs. With one CTA extra is 0.
+  const uint32_t ctas_mul = 0xffffffffu / static_cast<uint32_t>(ctas) + 1;
   auto range_lo = [&](int b) {   // floor(b * units / ctas)
     b = min(b, ctas);
-    return b * per_cta + b * extra / ctas;
+    return b * per_cta + static_cast<int>(__umulhi(b * extra, ctas_mul));
   };
   auto range_of = [&](int f) {   // the range that tile f lies in
     int a = 0, b = ctas - 1;
@@ -464,7 +470,8 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     return a;
   };
   const int lo = range_lo(bid), hi = range_lo(bid + 1);
-  const int off0 = lo < hi ? lo % total : -1;   // the range starts at this tile of its head
+  const int head0 = lo < hi ? lo / total : 0;
+  const int off0 = lo < hi ? lo - head0 * total : -1;   // the range starts at this tile of its head
   {
     int at = before + inc - mine;               // this thread's first tile
     if (off0 >= at && off0 < at + mine) {
@@ -681,7 +688,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       int qtiles = 0, q_issued = 0, step = 0, n = 0;
       bool ok = true;
       int left = hi - lo;
-      int head = left > 0 ? lo / total : 0, seq = uniform(left > 0 ? start[0] : 0);
+      int head = head0, seq = uniform(left > 0 ? start[0] : 0);
       int off = uniform(left > 0 ? start[1] : 0);   // tile inside the sequence's row groups
       int seq_base = -32, c_ctx = 0, c_drafts = 0, c_q0 = 0;  // 32 sequences' lengths, one a lane
       Boundary bd;
@@ -709,8 +716,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           sg.drafts = __shfl_sync(0xffffffffu, c_drafts, seq - seq_base);
           sg.q0 = __shfl_sync(0xffffffffu, c_q0, seq - seq_base);
           nt = sg.drafts == 0 ? 0 : tree_tiles(sg.ctx, sg.drafts);
-          const int groups = (sg.drafts + pair_tokens - 1) / pair_tokens;
-          if (off >= nt * groups) {              // the sequence is done (or has no drafts)
+          if (off >= nt * row_groups(sg.drafts)) {              // the sequence is done (or has no drafts)
             ++seq;
             off = 0;
             continue;
@@ -718,7 +724,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         bool two = false;
         if (more) {
-          const int rg = off / nt;
+          const int rg = off < nt ? 0 : off / nt;
           sg.t0 = off - rg * nt;
           sg.t1 = min(nt, sg.t0 + left);
           sg.tok0 = rg * pair_tokens;
@@ -777,19 +783,21 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           ++q_issued;
           ++qtiles;
         }
-        // the stream that the range start cuts is merged at its first cut (worked out
-        // here, when the other roles have their work)
         if (first_seg && sg.t0 > 0) {
-#pragma unroll 1
-          for (int e = 0; e < 2; ++e) {
-            const int r = range_of(lo - sg.t0 + (e ? nt - 1 : 0));
-            if (e) bd.last = r; else bd.first = r;
-          }
+          bd.row0 = sg.q0 + sg.tok0;
           bd.ntok = sg.ntok;
           bd.head = head;
-          if (bd.first == bid - 1) bd.row0 = sg.q0 + sg.tok0;
+          bd.first = lo - sg.t0;
+          bd.last = lo - sg.t0 + nt - 1;
         }
         first_seg = false;
+      }
+      // the stream that the range start cuts is merged at its first cut (worked out last:
+      // nothing waits for it)
+      if (bd.row0 >= 0) {
+        bd.last = range_of(bd.last);
+        if (range_lo(bid - 1) > bd.first) bd.row0 = -1;   // an earlier range cuts it too
+        bd.first = bid - 1;
       }
       if (lane == 0) p.bounds[bid] = bd;
       if (!ok) fail();
