@@ -1240,26 +1240,6 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = oth == 0.f ? o[e] : fmaf(o2[e], oth, o[e]);
             }
-            if (bad && live) {
-              // give back what was taken out of V for the drafts this row sees
-              for (int j = sg.t0; j < sg.t1; ++j) {
-                const TileKeys tk = tile_keys(sg.ctx, sg.drafts, j);
-                for (int u = tk.u0; u < tk.u0 + tk.drafts; ++u) {
-                  const uint32_t w = __ldg(p.tree_mask + q_row * p.mask_words + (u >> 5));
-                  if (!((w >> (u & 31)) & 1u)) continue;
-                  const uint32_t *v = reinterpret_cast<const uint32_t *>(
-                      p.value + (static_cast<int64_t>(sg.q0) + u) * p.value_stride + sg.head * kHD +
-                      cc * 32);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) {
-                    const uint32_t b = __ldg(v + e);
-                    const float2 f = bf16x2_to_float2(b);
-                    if ((b & 0x7f80u) == 0x7f80u) o[2 * e] += f.x;
-                    if ((b & 0x7f800000u) == 0x7f800000u) o[2 * e + 1] += f.y;
-                  }
-                }
-              }
-            }
             if (!live) continue;
             if (sg.slot >= 0) {
               float4 *dst = reinterpret_cast<float4 *>(p.po + rec * kHD + cc * 32);
@@ -1276,6 +1256,32 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 v.z = float2_to_bf16x2(o[q4 * 8 + 4], o[q4 * 8 + 5]);
                 v.w = float2_to_bf16x2(o[q4 * 8 + 6], o[q4 * 8 + 7]);
                 dst[q4] = v;
+              }
+            }
+          }
+          if (bad && live) {
+            // give back what was taken out of V for the drafts this row sees, to what the
+            // thread has just written: no rounding matters to an infinity or NaN (held in
+            // registers it was 3 KB more code, for nearly no row)
+            asm volatile("" ::: "memory");
+#pragma unroll 1
+            for (int j = sg.t0; j < sg.t1; ++j) {
+              const TileKeys tk = tile_keys(sg.ctx, sg.drafts, j);
+#pragma unroll 1
+              for (int u = tk.u0; u < tk.u0 + tk.drafts; ++u) {
+                const uint32_t w = __ldg(p.tree_mask + q_row * p.mask_words + (u >> 5));
+                if (!((w >> (u & 31)) & 1u)) continue;
+                const __nv_bfloat16 *v =
+                    p.value + (static_cast<int64_t>(sg.q0) + u) * p.value_stride + sg.head * kHD;
+#pragma unroll 1
+                for (int e = 0; e < kHD; ++e) {
+                  const float f = __bfloat162float(v[e]);
+                  if (fabsf(f) < INFINITY) continue;
+                  if (sg.slot >= 0)
+                    p.po[rec * kHD + e] += f;
+                  else
+                    orow[e] = __float2bfloat16(__bfloat162float(orow[e]) + f);
+                }
               }
             }
           }
