@@ -503,19 +503,20 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   // timeout. seg_done() gives the ring entry back.
   auto read_seg = [&](int n, Seg &s) -> bool {
     if (!warp_wait(seg_full(n % kSegRing), (n / kSegRing) & 1, abort_flag)) return false;
-    const volatile Seg *v = seg_at(n);
-    s.head = uniform(v->head);
-    s.ctx = uniform(v->ctx);
-    s.drafts = uniform(v->drafts);
-    s.q0 = uniform(v->q0);
-    s.seq = uniform(v->seq);
-    s.tok0 = uniform(v->tok0);
-    s.ntok = uniform(v->ntok);
-    s.t0 = uniform(v->t0);
-    s.t1 = uniform(v->t1);
-    s.slot = uniform(v->slot);
-    s.step0 = uniform(v->step0);
-    s.qtile = uniform(v->qtile);
+    const uint32_t at = base + kOffSeg + (n % kSegRing) * kSegBytes;
+    const uint4 a = lds128(at), b = lds128(at + 16), c = lds128(at + 32);
+    s.head = uniform(a.x);
+    s.ctx = uniform(a.y);
+    s.drafts = uniform(a.z);
+    s.q0 = uniform(a.w);
+    s.seq = uniform(b.x);
+    s.tok0 = uniform(b.y);
+    s.ntok = uniform(b.z);
+    s.t0 = uniform(b.w);
+    s.t1 = uniform(c.x);
+    s.slot = uniform(c.y);
+    s.step0 = uniform(c.z);
+    s.qtile = uniform(c.w);
     return true;
   };
   auto seg_done = [&](int n) {
@@ -834,15 +835,16 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (i == steps && !ended) {          // the next segment
           ok = poll(seg_full(n % kSegRing), (n / kSegRing) & 1, abort_flag);
           if (!ok) break;
-          const volatile Seg *v = seg_at(n);
-          sg.head = v->head;
-          sg.ctx = v->ctx;
-          sg.drafts = v->drafts;
-          sg.ntok = v->ntok;
-          sg.t0 = v->t0;
-          sg.t1 = v->t1;
-          sg.step0 = v->step0;
-          sg.qtile = v->qtile;
+          const uint32_t at = base + kOffSeg + (n % kSegRing) * kSegBytes;
+          const uint4 a = lds128(at), b = lds128(at + 16), c = lds128(at + 32);
+          sg.head = a.x;
+          sg.ctx = a.y;
+          sg.drafts = a.z;
+          sg.ntok = b.z;
+          sg.t0 = b.w;
+          sg.t1 = c.x;
+          sg.step0 = c.z;
+          sg.qtile = c.w;
           mbar_arrive(seg_empty(n % kSegRing));
           ++n;
           ended = sg.head < 0;
