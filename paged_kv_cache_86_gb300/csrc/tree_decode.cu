@@ -51,16 +51,17 @@
 // What a tile costs besides its loads is instructions, fetched by eleven warps that each
 // do something else: the kernel follows its code size more than its arithmetic (256 ragged
 // sequences: 297 us at 129 KB of code, 251 at 72 KB; later 225 -> 221 us from 95 to 82 KB,
-// and 233 us with the two softmax passes unrolled). Hence one copy of each role for both x, short
-// loops, elected lanes and waits that hardware suspends.
+// and 233 us with the two softmax passes unrolled; the loop that looks for non-finite
+// drafts, unrolled by four, alone costs 2 %). Hence one copy of each role for both x,
+// short loops, elected lanes and waits that hardware suspends.
 //
 // Measured, attention and combine, with floors of bytes at 6.78 TB/s (bf16 products at 1912
-// TFLOP/s): 64 sequences U[128, 4096] x 16 drafts, 16 / 8 heads 96 us (81); 256 lognormal
-// sequences x U[1, 32] drafts, 32 / 8 heads 220-224 us (194; DRAM traffic 1.29 GB read, the
-// tensor pipe 30 % active); 8 x 32768 cached tokens x 64 drafts, 32 / 8 heads 212-217 us
+// TFLOP/s): 64 sequences U[128, 4096] x 16 drafts, 16 / 8 heads 94 us (81); 256 lognormal
+// sequences x U[1, 32] drafts, 32 / 8 heads 220-222 us (194; DRAM traffic 1.29 GB read, the
+// tensor pipe 30 % active); 8 x 32768 cached tokens x 64 drafts, 32 / 8 heads 211-213 us
 // (160, 144 by products), 238 us at the 1.7 GHz that the power limit leaves in long runs;
-// one sequence of 5000 tokens 14 us (1). The combine is 4 to 10 us of it;
-// the loads alone take 87.5 / 205 / 168 us of the first three.
+// one sequence of 5000 tokens 13.7 us (1). The combine is 4 to 10 us of it; the loads alone
+// take 87.5 / 205 / 168 us of the first three.
 //
 // Every wait is bounded; on a timeout the CTA records PKV_DEVERR_TIMEOUT,
 // drains its copies and MMAs, frees its TMEM and exits.
