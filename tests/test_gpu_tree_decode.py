@@ -100,6 +100,27 @@ def test_a_seen_value_that_is_not_finite_reaches_only_the_rows_that_see_it(bad):
     assert torch.equal(~torch.isfinite(out), want)
 
 
+@pytest.mark.parametrize("ctx,drafts,at", [
+    (9000, 6, 4),        # a context cut over the whole GPU: the draft is in the last piece
+    (300, 140, 130),     # drafts over two key tiles and two row tiles
+    (5, 100, 3),
+])
+@pytest.mark.parametrize("bad", [float("nan"), -float("inf")])
+def test_a_seen_value_that_is_not_finite_in_a_cut_sequence(ctx, drafts, at, bad):
+    masks = [np.tril(np.ones((drafts, drafts), bool)), np.eye(9, dtype=bool)]
+    t = Trees(8, 2, 16, [ctx, 700], [drafts, 9], seed=13, masks=masks)
+    t.value[at, 0, 99] = bad
+    out = t.call(pkv, t.device()).cpu()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[at:drafts, 0:4, 99] = True               # the rows that see it, the heads of KV head 0
+    got = out[hit]
+    assert torch.isnan(got).all() if bad != bad else (got == bad).all()
+    # everything else is what it is without that value
+    t.value[at, 0, 99] = 0
+    clean = t.call(pkv, t.device()).cpu()
+    assert torch.equal(out[~hit], clean[~hit])
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.1, 1.5])
 def test_any_scale(scale):
     t = Trees(8, 2, 16, [70, 200], [5, 30], seed=12)
@@ -218,6 +239,35 @@ def test_same_bits_again_and_on_another_stream():
             outs.append(t.call(pkv, d))
     torch.cuda.synchronize()
     assert torch.equal(a, outs[0]) and torch.equal(a, outs[1])
+
+
+def test_calls_and_replays_at_the_same_time_on_two_streams():
+    batches = [Trees(8, 2, 16, [3000, 40], [12, 3], seed=21), Trees(8, 2, 12, [70, 2500], [5, 40], seed=22)]
+    inputs = [t.device() for t in batches]
+    alone = [t.call(pkv, d) for t, d in zip(batches, inputs)]
+    streams = [torch.cuda.Stream() for _ in batches]
+    outs = [torch.empty_like(a) for a in alone]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for t, d, st, o in zip(batches, inputs, streams, outs):
+            t.call(pkv, d, out=o, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, o) for a, o in zip(alone, outs))
+    graphs = []
+    for t, d, o in zip(batches, inputs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            t.call(pkv, d, out=o)
+        graphs.append(g)
+        o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert pkv.get_device_errors() == 0
+    assert all(torch.equal(a, o) for a, o in zip(alone, outs))
 
 
 def test_captured_once_and_replayed_with_other_lengths():
