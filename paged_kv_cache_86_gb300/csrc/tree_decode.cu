@@ -1213,7 +1213,9 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           m_all = fmaxf(m_used, o.x);
           own = m_used == -INFINITY ? 0.f : ex2((m_used - m_all) * c);
           oth = o.x == -INFINITY ? 0.f : ex2((o.x - m_all) * c);
-          l_sum = (m_used == -INFINITY ? 0.f : l_sum * own) + (o.x == -INFINITY ? 0.f : o.y * oth);
+          // maxima pass over NaN, so scores of NaN alone leave a maximum of -inf and a sum of
+          // NaN, which a factor of 0 keeps: a sum of 0, not the maximum, says "sees nothing"
+          l_sum = l_sum * own + o.y * oth;
         }
         ok = ok && warp_wait(pv_done(x), (segs[x] - 1) & 1, abort_flag) &&
              (!merge || warp_wait(pv_done(1 - x), (segs[1 - x] - 1) & 1, abort_flag));
@@ -1400,10 +1402,11 @@ tree_combine_kernel(const TreeParams p, const int num_bounds) {
           if (b.first + j <= b.last) m = fmaxf(m, ml[e][j].x);
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-          // nothing of a piece of which the row sees nothing
-          if (b.first + j > b.last || ml[e][j].x == -INFINITY) continue;
-          const float w = ex2(ml[e][j].x - m);
+          // of a piece without a maximum only the sum counts: 0, or NaN
+          if (b.first + j > b.last) continue;
+          const float w = ml[e][j].x == -INFINITY ? 0.f : ex2(ml[e][j].x - m);
           l += w * ml[e][j].y;
+          if (ml[e][j].x == -INFINITY) continue;
           o.x += w * v[e][j].x;
           o.y += w * v[e][j].y;
           o.z += w * v[e][j].z;
@@ -1432,17 +1435,17 @@ tree_combine_kernel(const TreeParams p, const int num_bounds) {
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
         if (c0 + j * share <= b.last) mt = fmaxf(mt, ml[j].x);
-      if (mt == -INFINITY) continue;
       const float a = m == -INFINITY ? 0.f : ex2(m - mt);
       l *= a;
       o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
       m = mt;
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        // nothing of a piece of which the row sees nothing
-        if (c0 + j * share > b.last || ml[j].x == -INFINITY) continue;
-        const float w = ex2(ml[j].x - m);
+        // of a piece without a maximum only the sum counts: 0, or NaN
+        if (c0 + j * share > b.last) continue;
+        const float w = ml[j].x == -INFINITY ? 0.f : ex2(ml[j].x - m);
         l += w * ml[j].y;
+        if (ml[j].x == -INFINITY) continue;
         o.x += w * v[j].x;
         o.y += w * v[j].y;
         o.z += w * v[j].z;
@@ -1462,8 +1465,7 @@ tree_combine_kernel(const TreeParams p, const int num_bounds) {
 #pragma unroll
         for (int w = 0; w < kCombineWarps; ++w) {
           const float2 ml = s_ml[w];
-          if (ml.x == -INFINITY) continue;
-          const float f = ex2(ml.x - mt);
+          const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mt);
           const float4 v = s_o[w][lane];
           l += f * ml.y;
           o.x += f * v.x;
