@@ -396,13 +396,14 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   };
 
   if (warp == kWarpWalk) {
-    // barriers counted 4 (a softmax warpgroup's warps), by ring readers, else 1
+    // barriers counted 4 (a softmax warpgroup's warps), by ring readers, 2 (pv_done), else 1
     static_assert(kNumBars <= 64, "two barriers a lane");
     for (int b = lane; b < kNumBars; b += 32) {
       const uint32_t bar = bar0 + 8u * b;
       int count = 1;
       for (int x = 0; x < 2; ++x)
         if (bar == p_full(x) || bar == o_free(x) || bar == wg_end(x)) count = 4;
+        else if (bar == pv_done(x)) count = 2;
       if (bar == ml_full || bar == ml_free) count = 4;
       if (bar >= seg_empty(0) && bar <= seg_empty(kSegRing - 1)) count = kSegReaders;
       mbar_init(bar, count);
@@ -958,7 +959,12 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                kk > 0 || !(w & kFresh));
           }
           if (w & kFrees) umma_commit(v_empty(stage));
-          if (w & kEnds) umma_commit(pv_done(x));
+          if (w & kEnds) {
+            umma_commit(pv_done(x));
+            // and an arrival of this thread's own, which has waited for the softmax warps:
+            // what they wrote to the segment (bad) is visible behind pv_done
+            mbar_arrive(pv_done(x));
+          }
         }
         // ---- S of the step
         if (scores) {
@@ -1022,6 +1028,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       }
       if (sg.head < 0) break;
       const bool two = sg.ntok > p.tile_tokens;
+      const bool clean = !two || x == 0;                         // looks for non-finite V
       const int tiles = sg.t1 - sg.t0;
       const int tok_x = two ? x * p.tile_tokens : 0;             // first token of this row tile
       const int ntok_x = min(p.tile_tokens, sg.ntok - tok_x);
@@ -1147,10 +1154,12 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           tmem_wait_st();
           tc_fence_before();
         }
-        if (!whole) {
+        if (clean && !whole) {
           // V values that are not finite must not meet the weights (of 0) of rows that
           // do not see them; the live threads share the 16-byte pieces of the tile's
-          // rows behind the cached ones
+          // rows behind the cached ones. Of a tile that both warpgroups use the first
+          // does it: the MMA warp waits for its weights and issues its PV before the
+          // second's, so both PVs come behind its writes and their proxy fences
           const int vt = tbase + i;
           if (!warp_wait(v_full(vt % kVStages), (vt / kVStages) & 1, abort_flag)) {
             ok = false;
@@ -1167,9 +1176,7 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
                 ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
             if (inf & 0x80008000u) {
-              // the flag first: a warpgroup that already finds zeros here sees it too
               if ((e >> 4) >= tk.at && (e >> 4) < tk.at + tk.drafts) seg_at(n)->bad = 1;
-              __threadfence_block();
               auto finite = [](uint32_t w) {
                 if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
                 if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;

@@ -89,3 +89,38 @@ def test_a_nan_query_that_sees_nothing_is_zero():
     assert pkv.get_device_errors() == 0
     assert torch.count_nonzero(out[:5]) == 0
     check(t, out)
+
+
+@pytest.mark.parametrize("bad", [NAN, -INF])
+@pytest.mark.parametrize("bs", [16, 6])
+@pytest.mark.parametrize("ctx", [0, 100, 300, 9000])
+def test_values_of_drafts_that_two_row_tiles_do_not_see(ctx, bs, bad):
+    # both warpgroups multiply the same V tile, whose odd rows nobody sees
+    masks = []
+    for n in (64, 33, 50):
+        m = np.tril(np.ones((n, n), bool))
+        m[:, 1::2] = False
+        masks.append(m)
+    t = Trees(8, 2, bs, [ctx, 50, 128], [64, 33, 50], seed=36, masks=masks)
+    for a, b in zip(t.cu[:-1], t.cu[1:]):
+        t.value[a + 1:b:2] = bad
+    d = t.device()
+    outs = [t.call(pkv, d) for _ in range(20)]
+    assert pkv.get_device_errors() == 0
+    check(t, outs[0])
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+@pytest.mark.parametrize("at", [0, 31, 32, 63])
+def test_a_value_that_some_rows_of_two_row_tiles_see(at):
+    # the rows of both row tiles that see the draft get its infinity, no others
+    t = Trees(8, 2, 16, [300], [64], seed=37, masks=[np.tril(np.ones((64, 64), bool))])
+    t.value[at, 1, 40] = INF
+    d = t.device()
+    outs = [t.call(pkv, d) for _ in range(20)]
+    assert pkv.get_device_errors() == 0
+    hit = torch.zeros(outs[0].shape, dtype=torch.bool)
+    hit[at:, 4:, 40] = True
+    out = outs[0].cpu()
+    assert bool((out[hit] == INF).all()) and bool(torch.isfinite(out[~hit]).all())
+    assert all(torch.equal(o, outs[0]) for o in outs)
