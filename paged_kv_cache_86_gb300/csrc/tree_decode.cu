@@ -349,6 +349,18 @@ __device__ __forceinline__ bool seq_lengths(const TreeParams &p, int i, int *ctx
   return true;
 }
 
+// Whether a row sees any key. A row without a weight (a sum of 0) is zero if it sees nothing;
+// if all its scores are -inf its softmax is NaN.
+__device__ __forceinline__ bool sees_any(const TreeParams &p, int64_t q_row, int ctx, int drafts) {
+  bool sees = ctx > 0;
+#pragma unroll 1
+  for (int u = 0; u < drafts && !sees; u += 32) {
+    const uint32_t w = __ldg(p.tree_mask + q_row * p.mask_words + (u >> 5));
+    sees = (drafts - u < 32 ? w & ((1u << (drafts - u)) - 1u) : w) != 0;
+  }
+  return sees;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kp,
@@ -1229,14 +1241,20 @@ tree_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc_fence_after();
         const bool bad = seg_at(n)->bad != 0;
         if (ok && warp_live) {
-          const float inv = sg.slot >= 0 ? 1.f : l_sum == 0.f ? 0.f : 1.f / l_sum;
+          // no weight: a partial record has -inf for its maximum if the row sees nothing at
+          // all, else the lowest number, so that the combine can tell
+          float inv = sg.slot >= 0 ? 1.f : 1.f / l_sum, lowest = -INFINITY;
+          if (l_sum == 0.f) {
+            if (live && sees_any(p, q_row, sg.ctx, sg.drafts)) lowest = -3.402823466e38f;
+            if (sg.slot < 0) inv = lowest == -INFINITY ? 0.f : __int_as_float(0x7fc00000);
+          }
           own *= inv;
           oth *= inv;
           __nv_bfloat16 *orow = p.out + (q_row * p.num_q_heads + sg.head * p.group + r_head) * kHD;
           const int64_t rec = static_cast<int64_t>(sg.slot) * p.rows_cap +
                               tok_x * p.group + row;   // partial record's row
           if (sg.slot >= 0 && live)
-            p.ml[rec] = make_float2(m_all == -INFINITY ? -INFINITY : m_all * c, l_sum);
+            p.ml[rec] = make_float2(m_all == -INFINITY ? lowest : m_all * c, l_sum);
 #pragma unroll 1
           for (int cc = 0; cc < 4; ++cc) {
             float o[32];
@@ -1375,8 +1393,9 @@ tree_combine_kernel(const TreeParams p, const int num_bounds) {
   const int part = shared_row ? warp : 0;
   const int row0 = shared_row ? blockIdx.y : blockIdx.y * kCombineWarps + warp;
   const int row_step = gridDim.y * (shared_row ? 1 : kCombineWarps);
-  auto finish = [&](int row, float l, float4 o) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+  auto finish = [&](int row, float m, float l, float4 o) {
+    // no weight: zero for a row that sees nothing, else 0 / 0
+    const float inv = m == -INFINITY && l == 0.f ? 0.f : 1.f / l;
     const int tok = row / p.group, g = row - tok * p.group;
     uint2 w;
     w.x = float2_to_bf16x2(o.x * inv, o.y * inv);
@@ -1419,7 +1438,7 @@ tree_combine_kernel(const TreeParams p, const int num_bounds) {
           o.z += w * v[e][j].z;
           o.w += w * v[e][j].w;
         }
-        if (row + e * row_step < rows) finish(row + e * row_step, l, o);
+        if (row + e * row_step < rows) finish(row + e * row_step, m, l, o);
       }
     }
     return;
@@ -1467,6 +1486,7 @@ tree_combine_kernel(const TreeParams p, const int num_bounds) {
         float mt = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kCombineWarps; ++w) mt = fmaxf(mt, s_ml[w].x);
+        m = mt;
         l = 0.f;
         o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -1484,7 +1504,7 @@ tree_combine_kernel(const TreeParams p, const int num_bounds) {
       __syncthreads();
       if (warp != 0) continue;
     }
-    finish(row, l, o);
+    finish(row, m, l, o);
   }
 }
 

@@ -124,3 +124,24 @@ def test_a_value_that_some_rows_of_two_row_tiles_see(at):
     out = outs[0].cpu()
     assert bool((out[hit] == INF).all()) and bool(torch.isfinite(out[~hit]).all())
     assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+@pytest.mark.parametrize("ctx", [0, 20, 128, 300, 9000])
+def test_rows_whose_scores_are_all_minus_infinity(ctx):
+    # a softmax of nothing but -inf is NaN, a row that sees nothing is zero, and one finite
+    # score takes all the weight
+    masks = [np.tril(np.ones((6, 6), bool)), np.zeros((4, 4), bool), np.eye(3, dtype=bool)]
+    masks[0][3] = False
+    t = Trees(8, 2, 16, [ctx, 0, 300], [6, 4, 3], seed=38, masks=masks)
+    t.q[:, :, 5] = t.q[:, :, 5].abs() + 0.125
+    p = np.arange(ctx)
+    t.k_cache[t.tables[0, p // 16], p % 16, :, 5] = -INF
+    t.key[:5, :, 5] = -INF                       # but not draft 5, which row 5 sees
+    d = t.device()
+    d["tree_mask"][6:10] |= -1 << 4              # bits beyond the tree are nobody's
+    out = t.call(pkv, d)
+    assert pkv.get_device_errors() == 0
+    nan = torch.isnan(out).flatten(1).all(1).tolist()
+    assert nan[:6] == [True, True, True, ctx > 0, True, False]
+    assert torch.count_nonzero(out[6:10]) == 0
+    check(t, out)
