@@ -25,6 +25,8 @@
 // evict what the next kernel reads.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -32,7 +34,6 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kWarpsPerSm = 32;
 
 struct Chunk {
   float v[8];
@@ -56,8 +57,9 @@ __device__ __forceinline__ uint4 pack(const Chunk &c) {
 }
 
 // kD: head_dim. kInter: interleaved pairs. kMany: the angles are read again for each row
-// (from L1) instead of held in 16 registers, so that 36 warps an SM are resident
-// instead of 32.
+// (from L1) instead of held in 16 registers, so that more warps an SM are
+// resident: 36 instead of 32 (52 or 56 registers, 64; launch bounds that ask for as many
+// give 56 and 63, and cost 1-2 % at 6000 and 12000 tokens).
 template <int kD, bool kInter, bool kMany>
 __global__ void __launch_bounds__(kWarps * 32) qk_rope_kernel(const QkRopeArgs a) {
   constexpr int kLanes = kD / 16;          // lanes of a row
@@ -172,6 +174,24 @@ __global__ void __launch_bounds__(kWarps * 32) qk_rope_kernel(const QkRopeArgs a
   }
 }
 
+// Warps of an instance that an SM holds at once, 0 on an error.
+template <int kD, bool kInter, bool kMany>
+int resident() {
+  static const int warps = [] {   // built for one architecture: the same on every device
+    int ctas = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        &ctas, qk_rope_kernel<kD, kInter, kMany>, kWarps * 32, 0);
+    return e == cudaSuccess ? ctas * kWarps : 0;
+  }();
+  return warps;
+}
+
+template <int kD>
+int resident(bool interleaved, bool many) {
+  return interleaved ? (many ? resident<kD, true, true>() : resident<kD, true, false>())
+                     : (many ? resident<kD, false, true>() : resident<kD, false, false>());
+}
+
 template <int kD, bool kMany>
 void launch(const QkRopeArgs &a, unsigned grid, cudaStream_t stream) {
   if (a.interleaved)
@@ -195,29 +215,40 @@ cudaError_t launch_qk_rope(QkRopeArgs a, int head_dim, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // With few tokens a token's rows are spread over up to one warp a pass, until
-  // kWarpsPerSm warps an SM are busy; with many, a warp takes all the rows of its
+  auto held = [&](bool many) {   // warps that the GPU holds at once
+    return int64_t(sm_count(dev)) * (head_dim == 64    ? resident<64>(a.interleaved, many)
+                                     : head_dim == 128 ? resident<128>(a.interleaved, many)
+                                                       : resident<256>(a.interleaved, many));
+  };
+  const int64_t want = held(false);
+  if (want == 0) return cudaErrorInvalidDeviceFunction;
+  // With few tokens a token's rows are spread over up to one warp a pass, until the
+  // GPU holds no more; with many, a warp takes all the rows of its
   // token and loads its angles once. 32 / 8 heads, us at 8 / 512 / 1024 / 2048 / 16384
   // tokens, with 28 warps resident: 2.4 / 5.2 / 5.6 / 8.6 / 74.5; never spread 7.6 / 8.1 /
   // 8.8 / 10.7 / 74.5; always 2.4 / 5.2 / 7.2 / 11.9 / 115.6; up to 16 warps an SM 2.4 / 4.8 /
   // 6.8 / 10.7 / 74.6, up to 64 2.5 / 5.1 / 7.3 / 9.3 / 74.5.
   const int rows = a.num_q_heads + (a.v != nullptr ? 2 : 1) * a.num_kv_heads;
   const int passes = (rows + 512 / head_dim - 1) / (512 / head_dim);
-  const int64_t want = static_cast<int64_t>(sm_count(dev)) * kWarpsPerSm;
   int64_t parts = want / a.num_tokens;
   parts = parts < 1 ? 1 : parts > passes ? passes : parts;
   // More tokens than resident warps: the last wave of warps may be nearly empty, so of one
-  // warp a token, two, and one with kMany (36 resident instead of 32) the one is taken
+  // warp a token, two, and one with kMany (more of them resident) the one is taken
   // whose waves cost least, by what a wave measured: 32 / 8 heads, us at 5200 / 6000 /
   // 8192 / 12000 / 16384 / 20000 tokens: one 31.8 / 34.0 / 38.7 / 54.9 / 72.6 / 88.2, two
   // 27.9 / 30.3 / 39.6 / 54.0 / 72.1 / 87.9, kMany 24.4 / 35.5 / 39.9 / 57.3 / 69.2 / 84.4. Few passes
-  // are not divided: the angles would be loaded for too few rows.
+  // are not divided: the angles would be loaded for too few rows. The costs are those of
+  // 32 / 8 heads of 128. With them, of twelve shapes (head dims 64, 128 and 256, 2 / 1 to
+  // 64 / 8 heads, with and without norm, store and interleaving) at 4900 to 32768 tokens the
+  // choice is at most 4 % slower than one warp a token and 6 % slower than the best of the
+  // three (8 / 2 heads of 256, 6000 tokens: 16.2, 15.3 by two); at 8 to 4096 tokens the
+  // parts above are within 8 % of the best of 1, 2, 4, 8 and all.
   bool many = false;
   if (a.num_tokens > want) {
     auto waves = [](int64_t warps, int64_t resident) { return (warps + resident - 1) / resident; };
     const int64_t one = 200 * waves(a.num_tokens, want);
     const int64_t two = passes < 8 ? one : 103 * waves(2 * int64_t(a.num_tokens), want);
-    const int64_t more = 229 * waves(a.num_tokens, want * 9 / 8);
+    const int64_t more = 229 * waves(a.num_tokens, std::max(want, held(true)));
     many = more < one && more <= two;
     if (!many && two < one) parts = 2;
   }
