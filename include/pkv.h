@@ -511,7 +511,8 @@ pkv_status pkv_plan_slots(const int32_t *context_lens, const int32_t *new_lens, 
  * A link that is neither -1 nor an earlier node counts as -1 and sets
  * PKV_DEVERR_TREE; a tree that is longer than max_seqlen_q or ends beyond
  * total_q is skipped and sets PKV_DEVERR_LENGTH. Rows behind the last tree are
- * left as they are. max_seqlen_q <= 65535 * 128. The two outputs must not be
+ * left as they are, and with max_seqlen_q, total_q or num_seqs 0 nothing is done
+ * (the same holds for pkv_tree_decode). max_seqlen_q <= 65535 * 128. The two outputs must not be
  * the same array nor one of the inputs (PKV_ERR_ARG).
  *
  * pkv_tree_decode: for every drafted row t of sequence i and query head g, with
@@ -522,7 +523,10 @@ pkv_status pkv_plan_slots(const int32_t *context_lens, const int32_t *new_lens, 
  *         tree_mask (its K and V are key[u], value[u]).
  * Any bit pattern is allowed: it need not be a tree, and a row that sees
  * nothing (no bit set, no cached token) is zero. What a row does not see has no
- * part in its result, whatever bits it holds.
+ * part in its result, whatever bits it holds. What it sees has, finite or not: a
+ * NaN among its scores makes the row NaN, and so do scores of -inf alone.
+ * Scores, softmax sums and accumulators are fp32; the weights are rounded to
+ * bf16 before their product with V (2^-8 of each at most).
  *   out, q          [total_q, num_q_heads, 128] bf16, contiguous; rows of out
  *                   behind cu_seqlens_q[num_seqs] are left as they are, and out
  *                   overlaps none of the inputs.

@@ -12,8 +12,8 @@
 // between CTAs. Every CTA computes the prefix sums over all requests itself
 // and takes its own 1024 tokens. A new block's id is read from the free list,
 // not from the table, and the token that starts the block writes it to the
-// table, so no CTA reads what another one writes. Measured: 5.3 us for 512 requests of
-// one token, 4.9 us for 32 of 512 (17 CTAs); the bytes would take 0.1 us. It is the chain
+// table, so no CTA reads what another one writes. Measured: 5.4 us for 512 requests of
+// one token, 5.2 us for 32 of 512 (17 CTAs); the bytes would take 0.1 us. It is the chain
 // lengths -> three block scans -> binary search -> table entry -> store.
 #include <cuda_runtime.h>
 
@@ -160,7 +160,7 @@ constexpr int kStagedParents = 1024;
 // Row t of a tree's mask has the bits of t and all its ancestors. Parents come
 // before their children, so the walk from t to the root meets falling indices:
 // each word of the row is complete when the walk leaves it, and is written once.
-// Measured: 4.2 us for one tree of 64 nodes, 4.4 us for 512 of up to 64, the latency of
+// Measured: 4.3 us for one tree of 64 nodes, 4.7 us for 512 of up to 64, the latency of
 // the launch, the links' load and the walk through shared memory.
 __global__ void __launch_bounds__(kNodes) tree_masks_kernel(const TreeMasksArgs a) {
   __shared__ int s_parent[kStagedParents];

@@ -42,7 +42,7 @@
 // Loads (warp 8 K, warp 10 V, warp 11 Q and the walk; warp 9 issues the MMAs): TMA boxes
 // when the block size is a multiple of 8 (whole tiles in boxes of up to a block, partial
 // tiles and drafts in boxes of 8 rows), else TMA row gathers, four rows an instruction: 256
-// ragged sequences take 227 us at block size 16, 254 at 12 and at 1. Rows of a tile that
+// ragged sequences take 221 us at block size 16, 236 at 12 and at 1. Rows of a tile that
 // are no key of the sequence may be other rows of a block or other sequences' drafts, and
 // drafts that a row does not see may hold anything: their scores are masked, and V values
 // among them that are not finite are set to zero in shared memory (0 * NaN is not 0),
@@ -56,15 +56,18 @@
 // short loops, elected lanes and waits that hardware suspends.
 //
 // Measured, attention and combine, with floors of bytes at 6.78 TB/s (bf16 products at 1912
-// TFLOP/s): 64 sequences U[128, 4096] x 16 drafts, 16 / 8 heads 94 us (81); 256 lognormal
-// sequences x U[1, 32] drafts, 32 / 8 heads 220-222 us (194; DRAM traffic 1.29 GB read, the
-// tensor pipe 30 % active); 8 x 32768 cached tokens x 64 drafts, 32 / 8 heads 211-213 us
-// (160, 144 by products), 238 us at the 1.7 GHz that the power limit leaves in long runs;
-// one sequence of 5000 tokens 13.7 us (1). The combine is 4 to 10 us of it; the loads alone
-// take 87.5 / 205 / 168 us of the first three.
+// TFLOP/s): 64 sequences U[128, 4096] x 16 drafts, 16 / 8 heads 94-96 us (81); 256 lognormal
+// sequences x U[1, 32] drafts, 32 / 8 heads 221-223 us (194; DRAM traffic 1.29 GB read, the
+// tensor pipe 31 % active); 8 x 32768 cached tokens x 64 drafts, 32 / 8 heads 213-218 us
+// (160, 144 by products; the tensor pipe 57 % active, exp2 30 %, issue slots 39 %: none is
+// full, each row tile waits for its chain S, softmax, PV), 239-242 us at the 1.7 GHz that
+// the power limit leaves in long runs; one sequence of 5000 tokens 13.5 us (1). The combine
+// is 4 to 10 us of it; the loads alone take 87.5 / 205 / 168 us of the first three.
+// Figures of a choice, here and below, are its sides measured on the kernel of its time.
 //
-// Every wait is bounded; on a timeout the CTA records PKV_DEVERR_TIMEOUT,
-// drains its copies and MMAs, frees its TMEM and exits.
+// Every wait on an mbarrier is bounded; on a timeout the CTA records PKV_DEVERR_TIMEOUT,
+// drains its copies and MMAs, frees its TMEM and exits. (tcgen05.alloc waits, before any
+// of those, until the SM's CTAs of another kernel have freed their TMEM.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -83,7 +86,7 @@ constexpr int kTile = 128;
 constexpr int kHD = 128;
 constexpr int kRegion = 16384;       // 128 rows x 64 dims, 128-byte swizzle
 constexpr int kTileBytes = 2 * kRegion;
-// Five tiles fit. 64 sequences of 16 drafts: 96.0 us with three of K, 97.9 with three of V;
+// Five tiles fit. Three of K against three of V: 64 sequences of 16 drafts 96.0 / 97.9 us,
 // 1 x 32768 33.7 / 34.2, 8 x 64 drafts 216.8 / 216.3, 256 ragged sequences the same.
 constexpr int kKStages = 3;
 constexpr int kVStages = 2;
