@@ -18,6 +18,10 @@
  *   pkv_copy_blocks    copy-on-write of shared cache blocks;
  *   *_fp8              the store, the decode and the decode step over an fp8
  *                      E4M3 cache;
+ *   *_fp8_block        the store, the read-back and the decode over an fp8
+ *                      cache with one scale per (block, KV head);
+ *   *_window           decode and prefill behind a sliding window with first
+ *                      tokens that stay visible;
  *   pkv_mixed_step     a batch of decode requests and prefill chunks;
  *   pkv_qk_norm_rope   head norm and position rotation of q and k, with or
  *                      without the store (pkv_qk_norm_rope_store);
@@ -405,6 +409,135 @@ pkv_status pkv_paged_prefill(void *out, const void *q,
                              int32_t block_size, int32_t num_blocks, float scale,
                              int32_t causal, void *workspace, size_t workspace_bytes,
                              pkv_dtype dtype, void *stream);
+
+/* -------------------------------------------- fp8 KV with block scales --
+ * A cache of E4M3 codes as above, with one scale per (block, KV head) instead
+ * of one per row:
+ *   k_cache, v_cache    [num_blocks, block_size, num_kv_heads, 128] uint8 codes
+ *   k_scales, v_scales  [num_blocks, num_kv_heads] float
+ * A value is e4m3(code) * scale.
+ *
+ * pkv_store_kvcache_fp8_block: the new K/V rows of a round, quantized as they
+ * are written. Sequence i's rows are cu_seqlens_q[i] .. cu_seqlens_q[i+1]-1 of
+ * key / value; they are its last tokens, positions context_lens[i] - n_i ..
+ * context_lens[i] - 1 (so context_lens counts them: the arrays that
+ * pkv_plan_slots writes). For each block they touch and each head, K and V apart:
+ *   e = the smallest integer with max |x| <= 448 * 2^e over the block's new
+ *   finite values, at least -120 and at most 119 (no finite value: -120);
+ *   scale = 2^e where the first new row is row 0 of the block; otherwise the
+ *   block holds older rows of the sequence, scale = max(2^e, the scale it has),
+ *   and where that grows the older codes c become E4M3(c * old / new), which is
+ *   exact except where a code turns subnormal;
+ *   new codes are E4M3(x / scale), rounded to nearest even; an infinite x
+ *   becomes +-448, a NaN the code 0x7F (which reads back as NaN).
+ * Rows of the block behind the last new one are not touched. A block must
+ * appear once among the touched ones (blocks being written are not shared), and
+ * scales that a call reads must be finite and positive.
+ *   key, value    token rows at any stride, as for pkv_store_kvcache.
+ *   cu_seqlens_q  [num_seqs + 1] int32, non-decreasing, ending at or before
+ *                 total_q; rows behind the last sequence are ignored.
+ *   block_tables  [num_seqs, max_blocks_per_seq] int32; context_lens [num_seqs].
+ * A sequence whose lengths do not fit (context_lens[i] under its new rows or
+ * over max_blocks_per_seq * block_size) is skipped (PKV_DEVERR_LENGTH), so is a
+ * block with an id outside [0, num_blocks) (PKV_DEVERR_BLOCK_ID).
+ * Any block_size >= 1, num_kv_heads <= 32767.
+ */
+pkv_status pkv_store_kvcache_fp8_block(const void *key, const void *value,
+                                       int64_t key_token_stride, int64_t value_token_stride,
+                                       void *k_cache, void *v_cache,
+                                       float *k_scales, float *v_scales,
+                                       const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                       const int32_t *cu_seqlens_q, const int32_t *context_lens,
+                                       int32_t num_seqs, int32_t total_q,
+                                       int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, int32_t num_blocks, void *stream);
+
+/* pkv_load_kvcache_fp8_block: the values of that cache, in bf16: position p <
+ * context_lens[i] of sequence i goes to row row_starts[i] + p of key_out /
+ * value_out (rounded to nearest even; exact for the scales that the store
+ * writes, down to 2^-120). Other rows are left as they were. With row_starts
+ * at multiples of a block size the outputs are a bf16 block pool in which
+ * sequence i owns consecutive blocks, which pkv_paged_prefill reads.
+ *   key_out, value_out  num_rows rows of num_kv_heads * 128 values, token
+ *                       strides in elements as for pkv_store_kvcache.
+ *   row_starts          [num_seqs] int32, non-decreasing, each sequence's rows
+ *                       ending at or before the next one's start; rows from
+ *                       num_rows on are not written.
+ * A bad block id (PKV_DEVERR_BLOCK_ID) or a length outside
+ * [0, max_blocks_per_seq * block_size] (PKV_DEVERR_LENGTH) leaves its rows.
+ */
+pkv_status pkv_load_kvcache_fp8_block(void *key_out, void *value_out,
+                                      int64_t key_token_stride, int64_t value_token_stride,
+                                      const void *k_cache, const void *v_cache,
+                                      const float *k_scales, const float *v_scales,
+                                      const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t *context_lens, const int32_t *row_starts,
+                                      int32_t num_seqs, int32_t num_rows,
+                                      int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t block_size, int32_t num_blocks, void *stream);
+
+/* ---------------------------------------------- sliding window with sinks --
+ * Attention that leaves old tokens out: a query at position t sees the keys
+ * p <= t with p < sinks (the first tokens stay visible) or p > t - window (so
+ * window 1 is the token itself; sinks 0 a plain window). window >= 1, sinks >= 0,
+ * both may pass the context. Blocks whose tokens are not seen are not read,
+ * except, in the prefill, the rest of a box of up to 32 rows at an edge.
+ *
+ * pkv_paged_decode_window: pkv_paged_decode over the seen tokens of sequence i,
+ * whose query is at position context_lens[i] - 1.
+ * pkv_paged_decode_fp8_block: the same over an fp8 cache with block scales;
+ * window 0 is the whole context.
+ *   Arguments, graphs and errors as for pkv_paged_decode, except: any
+ *   num_q_heads that is a multiple of num_kv_heads, any block_size >= 1; scale
+ *   > 0; num_blocks * block_size at most 2^31 - 1; out and q must not overlap;
+ *   workspace of pkv_decode_window_workspace_size bytes.
+ *   A token that is not seen, and a row behind the last token, is never touched,
+ *   whatever it holds. A seen key or value that is not finite counts as it does
+ *   in the formula. A row whose seen scores are all -inf is NaN.
+ *   The weights are rounded to bf16 (bf16 cache; the softmax's sum is of the
+ *   rounded ones) or f16 (fp8 cache) before they multiply V; all sums are fp32.
+ *
+ * pkv_paged_prefill_window: pkv_paged_prefill, causal, over the seen keys of
+ * each query row. Arguments, workspace and errors as there, except scale > 0,
+ * max_seqlen_k and num_blocks * block_size at most 2^31 - 512, and out and q
+ * must not overlap. Keys and values that a row does not see never change it,
+ * whatever they hold: rows whose sums come out not finite are computed a second
+ * time from their seen keys alone (slower).
+ */
+size_t pkv_decode_window_workspace_size(int32_t num_seqs, int32_t num_q_heads,
+                                        int32_t num_kv_heads, int32_t head_dim);
+
+pkv_status pkv_paged_decode_window(void *out, const void *q,
+                                   const void *k_cache, const void *v_cache,
+                                   const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t *context_lens, int32_t num_seqs,
+                                   int32_t max_context_len, int32_t window, int32_t sinks,
+                                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                   int32_t block_size, int32_t num_blocks, float scale,
+                                   void *workspace, size_t workspace_bytes,
+                                   pkv_dtype dtype, void *stream);
+
+pkv_status pkv_paged_decode_fp8_block(void *out, const void *q,
+                                      const void *k_cache, const void *v_cache,
+                                      const float *k_scales, const float *v_scales,
+                                      const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t *context_lens, int32_t num_seqs,
+                                      int32_t max_context_len, int32_t window, int32_t sinks,
+                                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t block_size, int32_t num_blocks, float scale,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+pkv_status pkv_paged_prefill_window(void *out, const void *q,
+                                    const void *k_cache, const void *v_cache,
+                                    const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                    int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                    const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                    int32_t num_seqs, int32_t total_q,
+                                    int32_t window, int32_t sinks,
+                                    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                    int32_t block_size, int32_t num_blocks, float scale,
+                                    void *workspace, size_t workspace_bytes,
+                                    pkv_dtype dtype, void *stream);
 
 /* ------------------------------------------------- head norm and rotation --
  * pkv_qk_norm_rope: for every token t and every query head row x of q[t] (with

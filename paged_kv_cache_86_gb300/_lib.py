@@ -31,7 +31,9 @@ EXPORTED = ("pkv_store_kvcache", "pkv_decode_workspace_size", "pkv_paged_decode"
             "pkv_prefill_workspace_size", "pkv_paged_prefill", "pkv_get_device_errors",
             "pkv_status_string", "pkv_version", "pkv_qk_norm_rope", "pkv_qk_norm_rope_store",
             "pkv_plan_slots", "pkv_tree_masks", "pkv_tree_decode_workspace_size",
-            "pkv_tree_decode")
+            "pkv_tree_decode", "pkv_store_kvcache_fp8_block", "pkv_load_kvcache_fp8_block",
+            "pkv_decode_window_workspace_size", "pkv_paged_decode_window",
+            "pkv_paged_decode_fp8_block", "pkv_paged_prefill_window")
 
 
 class PkvError(RuntimeError):
@@ -95,6 +97,21 @@ def load(path: str = LIB_PATH):
         lib.pkv_tree_decode.argtypes = [vp, vp, vp, vp, i64, i64, vp, vp, vp, i32, vp, vp, vp, i32,
                                         i32, i32, i32, i32, i32, i32, i32, i32, i32, f32, vp, sz,
                                         ctypes.c_int, vp]
+        lib.pkv_store_kvcache_fp8_block.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp, i32, vp,
+                                                    vp, i32, i32, i32, i32, i32, i32, vp]
+        lib.pkv_load_kvcache_fp8_block.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp, i32, vp,
+                                                   vp, i32, i32, i32, i32, i32, i32, vp]
+        lib.pkv_decode_window_workspace_size.argtypes = [i32, i32, i32, i32]
+        lib.pkv_decode_window_workspace_size.restype = sz
+        lib.pkv_paged_decode_window.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32,
+                                                i32, i32, i32, i32, i32, f32, vp, sz,
+                                                ctypes.c_int, vp]
+        lib.pkv_paged_decode_fp8_block.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32,
+                                                   i32, i32, i32, i32, i32, i32, i32, f32, vp, sz,
+                                                   vp]
+        lib.pkv_paged_prefill_window.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, vp, i32, i32,
+                                                 i32, i32, i32, i32, i32, i32, i32, i32, f32, vp,
+                                                 sz, ctypes.c_int, vp]
         lib.pkv_get_device_errors.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
         lib.pkv_selftest_bounded_wait.argtypes = [i32, vp, vp]
         lib.pkv_status_string.argtypes = [ctypes.c_int]
@@ -105,7 +122,9 @@ def load(path: str = LIB_PATH):
                      "pkv_paged_decode_fp8", "pkv_decode_step_fp8", "pkv_mixed_step",
                      "pkv_get_device_errors", "pkv_qk_norm_rope", "pkv_qk_norm_rope_store",
                      "pkv_plan_slots", "pkv_tree_masks", "pkv_tree_decode",
-                     "pkv_selftest_bounded_wait"):
+                     "pkv_store_kvcache_fp8_block", "pkv_load_kvcache_fp8_block",
+                     "pkv_paged_decode_window", "pkv_paged_decode_fp8_block",
+                     "pkv_paged_prefill_window", "pkv_selftest_bounded_wait"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -505,7 +524,7 @@ def paged_prefill(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_tables,
 # tests its arguments in one expression of plain attribute reads; only when that
 # fails does it look for the tensor at fault and name it.
 
-_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 # the current stream's handle without building a Stream object (2 us of a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -914,6 +933,273 @@ def tree_decode(q, key, value, k_cache, v_cache, block_tables, context_lens, cu_
             total, int(max_seqlen_q), int(max_context_len), hq, hkv, d, bs, nb, scale,
             workspace.data_ptr(), workspace.numel() * workspace.element_size(), PKV_BF16, st),
             "pkv_tree_decode")
+    finally:
+        _leave(ctx)
+    return out
+
+
+def _row_stride_of(t) -> int:
+    """_row_stride, and -1 for what is no tensor."""
+    try:
+        return _row_stride(t)
+    except AttributeError:
+        return -1
+
+
+def _fp8_block_pool(k_cache, v_cache, k_scales, v_scales):
+    """Sizes of an fp8 pool [NB, bs, Hkv, 128] with scales [NB, Hkv], checked."""
+    try:
+        fine = (k_cache.dtype is _U8 and k_cache.dim() == 4 and k_cache.is_contiguous()
+                and v_cache.dtype is _U8 and v_cache.dim() == 4 and v_cache.is_contiguous()
+                and k_scales.dtype is _F32 and k_scales.dim() == 2 and k_scales.is_contiguous()
+                and v_scales.dtype is _F32 and v_scales.dim() == 2 and v_scales.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        _dense(_U8, 4, k_cache=k_cache, v_cache=v_cache)
+        _dense(_F32, 2, k_scales=k_scales, v_scales=v_scales)
+    shape = k_cache.shape
+    scales = (shape[0], shape[2])
+    if v_cache.shape != shape or k_scales.shape != scales or v_scales.shape != scales:
+        raise ValueError("caches must be [NB, bs, Hkv, D] and their scales [NB, Hkv]")
+    return shape
+
+
+def _tables_and_lens(block_tables, **lens):
+    """block_tables [S, MB] and the named one-dimensional int32 arrays, checked; their layout only."""
+    try:
+        fine = (block_tables.dtype is _I32 and block_tables.dim() == 2
+                and block_tables.is_contiguous()
+                and all(t.dtype is _I32 and t.dim() == 1 and t.is_contiguous()
+                        for t in lens.values()))
+    except AttributeError:
+        fine = False
+    if not fine:
+        _dense(_I32, 2, block_tables=block_tables)
+        _dense(_I32, 1, **lens)
+    return block_tables.shape
+
+
+def _one_device(**tensors) -> int:
+    """The device index that all the named tensors share."""
+    index = -1
+    for t in tensors.values():
+        at = t.get_device()
+        if at < 0 or (index >= 0 and at != index):
+            _refuse_device(**tensors)
+        index = at
+    return index
+
+
+def store_kvcache_fp8_block(key, value, k_cache, v_cache, k_scales, v_scales, block_tables,
+                            cu_seqlens_q, context_lens, stream=None) -> None:
+    """Quantize the new rows key / value [total_q, Hkv, 128] bf16 (token rows may be strided)
+    into the fp8 E4M3 caches [NB, bs, Hkv, 128] (uint8 codes), whose scales [NB, Hkv] float32
+    are one power of two per (block, KV head). Sequence i's rows cu_seqlens_q[i] ..
+    cu_seqlens_q[i + 1] - 1 are its last tokens; context_lens[i] counts them. Where a block
+    holds older tokens and its scale has to grow, their codes are re-expressed."""
+    ks, vs = _row_stride_of(key), _row_stride_of(value)
+    if ks < 0 or vs < 0:
+        _rows(key=key, value=value)
+    nb, bs, hkv, d = _fp8_block_pool(k_cache, v_cache, k_scales, v_scales)
+    s, mb = _tables_and_lens(block_tables, cu_seqlens_q=cu_seqlens_q, context_lens=context_lens)
+    total = key.shape[0]
+    if key.shape != (total, hkv, d) or value.shape != key.shape:
+        raise ValueError("key / value must be [total_q, Hkv, D]")
+    if cu_seqlens_q.shape[0] != s + 1 or context_lens.shape[0] != s:
+        raise ValueError("metadata shape mismatch")
+    index = _one_device(key=key, value=value, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
+                        v_scales=v_scales, block_tables=block_tables, cu_seqlens_q=cu_seqlens_q,
+                        context_lens=context_lens)
+    lib = _lib or load()
+    ctx, st = _enter(index, stream)
+    try:
+        _check(lib.pkv_store_kvcache_fp8_block(
+            key.data_ptr(), value.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), mb,
+            cu_seqlens_q.data_ptr(), context_lens.data_ptr(), s, total, hkv, d, bs, nb, st),
+            "pkv_store_kvcache_fp8_block")
+    finally:
+        _leave(ctx)
+
+
+def load_kvcache_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                           row_starts, num_rows: int | None = None, key_out=None, value_out=None,
+                           stream=None):
+    """The tokens of an fp8 cache with block scales back in bf16: position p < context_lens[i]
+    of sequence i goes to row row_starts[i] + p (int32 [S], non-decreasing, rows of one
+    sequence ending before the next one's start). Returns (key, value) [num_rows, Hkv, 128];
+    rows that no sequence has are left as they were. key_out / value_out may be given (token
+    rows may be strided); a bf16 block pool [NB, bs, Hkv, 128] viewed as rows is one."""
+    if (key_out is None) != (value_out is None):
+        raise ValueError("key_out and value_out go together")
+    nb, bs, hkv, d = _fp8_block_pool(k_cache, v_cache, k_scales, v_scales)
+    s, mb = _tables_and_lens(block_tables, context_lens=context_lens, row_starts=row_starts)
+    if context_lens.shape[0] != s or row_starts.shape[0] != s:
+        raise ValueError("metadata shape mismatch")
+    named = dict(k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
+                 block_tables=block_tables, context_lens=context_lens, row_starts=row_starts)
+    if key_out is None:
+        if num_rows is None or num_rows < 0:
+            raise ValueError("num_rows must be given, and not negative, without key_out / value_out")
+        ks = vs = hkv * d
+    else:
+        ks, vs = _row_stride_of(key_out), _row_stride_of(value_out)
+        if ks < 0 or vs < 0:
+            _rows(key_out=key_out, value_out=value_out)
+        if num_rows is None:
+            num_rows = key_out.shape[0]
+        if key_out.shape != (num_rows, hkv, d) or value_out.shape != key_out.shape:
+            raise ValueError("key_out / value_out must be [num_rows, Hkv, D]")
+        named.update(key_out=key_out, value_out=value_out)
+    index = _one_device(**named)
+    lib = _lib or load()
+    ctx, st = _enter(index, stream)
+    try:
+        if key_out is None:
+            key_out = torch.empty((num_rows, hkv, d), dtype=_BF16, device=k_cache.device)
+            value_out = torch.empty((num_rows, hkv, d), dtype=_BF16, device=k_cache.device)
+        _check(lib.pkv_load_kvcache_fp8_block(
+            key_out.data_ptr(), value_out.data_ptr(), ks, vs, k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+            mb, context_lens.data_ptr(), row_starts.data_ptr(), s, num_rows, hkv, d, bs, nb, st),
+            "pkv_load_kvcache_fp8_block")
+    finally:
+        _leave(ctx)
+    return key_out, value_out
+
+
+def decode_window_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                                 head_dim: int = 128) -> int:
+    return int(load().pkv_decode_window_workspace_size(num_seqs, num_q_heads, num_kv_heads,
+                                                       head_dim))
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_window_workspace(index: int, s: int, hq: int, hkv: int, d: int) -> int:
+    """The size on device `index`, the current one; at least 256."""
+    return max(load().pkv_decode_window_workspace_size(s, hq, hkv, d), 256)
+
+
+def _query(q, rows):
+    """q [rows, Hq, D] bf16, dense."""
+    try:
+        fine = q.dtype is _BF16 and q.dim() == 3 and q.is_contiguous()
+    except AttributeError:
+        fine = False
+    if not fine:
+        _dense(_BF16, 3, q=q)
+    if rows is not None and q.shape[0] != rows:
+        raise ValueError("metadata rows must equal the number of sequences")
+    return q.shape
+
+
+def _bf16_pool(k_cache, v_cache):
+    """Sizes of a bf16 pool [NB, bs, Hkv, D], checked."""
+    try:
+        fine = (k_cache.dtype is _BF16 and k_cache.dim() == 4 and k_cache.is_contiguous()
+                and v_cache.dtype is _BF16 and v_cache.dim() == 4 and v_cache.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        _dense(_BF16, 4, k_cache=k_cache, v_cache=v_cache)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache / v_cache shape mismatch")
+    return k_cache.shape
+
+
+def _workspace_for(workspace, need: int, q):
+    """The caller's workspace (checked) or a new one of `need` bytes."""
+    if workspace is None:
+        return torch.empty(need, dtype=_U8, device=q.device)
+    if workspace.get_device() != q.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on q's device")
+    return workspace
+
+
+def paged_decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                           scale: float, window: int = 0, sinks: int = 0,
+                           max_context_len: int | None = None, out=None, workspace=None,
+                           stream=None) -> torch.Tensor:
+    """Decode attention over fp8 E4M3 caches [NB, bs, Hkv, 128] with scales [NB, Hkv], one
+    query row q [S, Hq, 128] per sequence. window 0: over the whole context; otherwise over
+    the last `window` tokens and the first `sinks`. Returns out [S, Hq, 128] bf16."""
+    nb, bs, hkv, d = _fp8_block_pool(k_cache, v_cache, k_scales, v_scales)
+    s, mb = _tables_and_lens(block_tables, context_lens=context_lens)
+    _, hq, dq = _query(q, s)
+    if dq != d or context_lens.shape[0] != s:
+        raise ValueError("q / cache / metadata shape mismatch")
+    index = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
+                        v_scales=v_scales, block_tables=block_tables, context_lens=context_lens)
+    lib = _lib or load()
+    ctx, st = _enter(index, stream)
+    try:
+        out = _out_like(out, q) if out is not None else torch.empty_like(q)
+        workspace = _workspace_for(workspace, _decode_window_workspace(index, s, hq, hkv, d), q)
+        _check(lib.pkv_paged_decode_fp8_block(
+            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), mb,
+            context_lens.data_ptr(), s, mb * bs if max_context_len is None else max_context_len,
+            window, sinks, hq, hkv, d, bs, nb, scale, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), st), "pkv_paged_decode_fp8_block")
+    finally:
+        _leave(ctx)
+    return out
+
+
+def paged_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale: float,
+                        window: int, sinks: int = 0, max_context_len: int | None = None, out=None,
+                        workspace=None, stream=None) -> torch.Tensor:
+    """Decode attention over the last `window` tokens and the first `sinks` of each sequence
+    in bf16 caches [NB, bs, Hkv, 128], one query row q [S, Hq, 128] per sequence. Returns out
+    [S, Hq, 128] bf16."""
+    nb, bs, hkv, d = _bf16_pool(k_cache, v_cache)
+    s, mb = _tables_and_lens(block_tables, context_lens=context_lens)
+    _, hq, dq = _query(q, s)
+    if dq != d or context_lens.shape[0] != s:
+        raise ValueError("q / cache / metadata shape mismatch")
+    index = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                        context_lens=context_lens)
+    lib = _lib or load()
+    ctx, st = _enter(index, stream)
+    try:
+        out = _out_like(out, q) if out is not None else torch.empty_like(q)
+        workspace = _workspace_for(workspace, _decode_window_workspace(index, s, hq, hkv, d), q)
+        _check(lib.pkv_paged_decode_window(
+            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_tables.data_ptr(), mb, context_lens.data_ptr(), s,
+            mb * bs if max_context_len is None else max_context_len, window, sinks, hq, hkv, d,
+            bs, nb, scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            PKV_BF16, st), "pkv_paged_decode_window")
+    finally:
+        _leave(ctx)
+    return out
+
+
+def paged_prefill_window(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_tables,
+                         scale: float, window: int, sinks: int, max_seqlen_q: int,
+                         max_seqlen_k: int, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Causal chunked-prefill attention in which the row at position t sees the keys p <= t
+    with p < sinks or p > t - window; otherwise as paged_prefill. Returns out
+    [total_q, Hq, 128] bf16; rows behind cu_seqlens_q[-1] are not written."""
+    nb, bs, hkv, d = _bf16_pool(k_cache, v_cache)
+    s, mb = _tables_and_lens(block_tables, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
+    total, hq, dq = _query(q, None)
+    if dq != d or cu_seqlens_q.shape[0] != s + 1 or cu_seqlens_k.shape[0] != s + 1:
+        raise ValueError("q / cache / metadata shape mismatch")
+    index = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                        cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
+    lib = _lib or load()
+    ctx, st = _enter(index, stream)
+    try:
+        out = _out_like(out, q) if out is not None else torch.empty_like(q)
+        workspace = _workspace_for(workspace, 256, q)
+        _check(lib.pkv_paged_prefill_window(
+            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), max_seqlen_q, max_seqlen_k,
+            block_tables.data_ptr(), mb, s, total, window, sinks, hq, hkv, d, bs, nb, scale,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), PKV_BF16, st),
+            "pkv_paged_prefill_window")
     finally:
         _leave(ctx)
     return out

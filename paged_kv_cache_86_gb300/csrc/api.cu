@@ -842,6 +842,274 @@ pkv_status pkv_tree_decode(void *out, const void *q, const void *key, const void
   return from_cuda(pkv::launch_tree_decode(a, static_cast<cudaStream_t>(stream)));
 }
 
+// Bytes [a, a + n) and [b, b + n) have some in common.
+static bool overlap(const void *a, const void *b, int64_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < static_cast<uint64_t>(n) : x - y < static_cast<uint64_t>(n);
+}
+
+// What every call over a cache with block scales asks of its pool.
+static pkv_status fp8_block_shape(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
+                                  int32_t block_size, int32_t num_blocks,
+                                  int32_t max_blocks_per_seq) {
+  if (num_seqs < 0 || num_kv_heads < 1 || block_size < 1 || num_blocks < 1 ||
+      max_blocks_per_seq < 0)
+    return PKV_ERR_ARG;
+  if (head_dim != 128 || num_kv_heads > 32767) return PKV_ERR_SHAPE;
+  return PKV_OK;
+}
+
+pkv_status pkv_store_kvcache_fp8_block(const void *key, const void *value,
+                                       int64_t key_token_stride, int64_t value_token_stride,
+                                       void *k_cache, void *v_cache, float *k_scales,
+                                       float *v_scales, const int32_t *block_tables,
+                                       int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
+                                       const int32_t *context_lens, int32_t num_seqs,
+                                       int32_t total_q, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, int32_t num_blocks, void *stream) {
+  pkv_status st = fp8_block_shape(num_seqs, num_kv_heads, head_dim, block_size, num_blocks,
+                                  max_blocks_per_seq);
+  if (st != PKV_OK) return st;
+  if (total_q < 0) return PKV_ERR_ARG;
+  if (num_seqs == 0 || total_q == 0) return PKV_OK;
+  if (!key || !value || !k_cache || !v_cache || !k_scales || !v_scales || !cu_seqlens_q ||
+      !context_lens || (!block_tables && max_blocks_per_seq > 0))
+    return PKV_ERR_ARG;
+  const int64_t row = int64_t(num_kv_heads) * head_dim;
+  if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      key_token_stride < row || value_token_stride < row || key_token_stride % 8 != 0 ||
+      value_token_stride % 8 != 0)
+    return PKV_ERR_ARG;
+  if (k_cache == v_cache || k_scales == v_scales) return PKV_ERR_ARG;
+  cudaError_t e;
+  pkv::Fp8BlockStoreArgs a;
+  a.err = pkv::device_error_word(&e);
+  if (!a.err) return PKV_ERR_CUDA;
+  a.key = static_cast<const __nv_bfloat16 *>(key);
+  a.value = static_cast<const __nv_bfloat16 *>(value);
+  a.key_stride = key_token_stride;
+  a.value_stride = value_token_stride;
+  a.k_cache = static_cast<uint8_t *>(k_cache);
+  a.v_cache = static_cast<uint8_t *>(v_cache);
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.block_tables = block_tables;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.context_lens = context_lens;
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  return from_cuda(pkv::launch_store_fp8_block(a, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_load_kvcache_fp8_block(void *key_out, void *value_out, int64_t key_token_stride,
+                                      int64_t value_token_stride, const void *k_cache,
+                                      const void *v_cache, const float *k_scales,
+                                      const float *v_scales, const int32_t *block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                      const int32_t *row_starts, int32_t num_seqs,
+                                      int32_t num_rows, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t block_size, int32_t num_blocks, void *stream) {
+  pkv_status st = fp8_block_shape(num_seqs, num_kv_heads, head_dim, block_size, num_blocks,
+                                  max_blocks_per_seq);
+  if (st != PKV_OK) return st;
+  if (num_rows < 0) return PKV_ERR_ARG;
+  if (num_seqs == 0 || num_rows == 0) return PKV_OK;
+  if (!key_out || !value_out || !k_cache || !v_cache || !k_scales || !v_scales || !context_lens ||
+      !row_starts || (!block_tables && max_blocks_per_seq > 0))
+    return PKV_ERR_ARG;
+  const int64_t row = int64_t(num_kv_heads) * head_dim;
+  if (!aligned16(key_out) || !aligned16(value_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      key_token_stride < row || value_token_stride < row || key_token_stride % 8 != 0 ||
+      value_token_stride % 8 != 0)
+    return PKV_ERR_ARG;
+  if (key_out == value_out) return PKV_ERR_ARG;
+  cudaError_t e;
+  pkv::Fp8BlockLoadArgs a;
+  a.err = pkv::device_error_word(&e);
+  if (!a.err) return PKV_ERR_CUDA;
+  a.key_out = static_cast<__nv_bfloat16 *>(key_out);
+  a.value_out = static_cast<__nv_bfloat16 *>(value_out);
+  a.key_stride = key_token_stride;
+  a.value_stride = value_token_stride;
+  a.k_cache = static_cast<const uint8_t *>(k_cache);
+  a.v_cache = static_cast<const uint8_t *>(v_cache);
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.block_tables = block_tables;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.context_lens = context_lens;
+  a.row_starts = row_starts;
+  a.num_seqs = num_seqs;
+  a.num_rows = num_rows;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  return from_cuda(pkv::launch_load_fp8_block(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pkv_decode_window_workspace_size(int32_t num_seqs, int32_t num_q_heads,
+                                        int32_t num_kv_heads, int32_t head_dim) {
+  if (num_seqs < 0 || num_q_heads < 1 || num_kv_heads < 1 || head_dim != 128 ||
+      num_q_heads % num_kv_heads != 0)
+    return 0;
+  return pkv::decode_warp_workspace_bytes(num_seqs, num_q_heads, num_kv_heads);
+}
+
+// Shared body of pkv_paged_decode_fp8_block (with scales) and pkv_paged_decode_window.
+static pkv_status decode_warp_call(void *out, const void *q, const void *k_cache,
+                                   const void *v_cache, bool fp8, const float *k_scales,
+                                   const float *v_scales, const int32_t *block_tables,
+                                   int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                   int32_t num_seqs, int32_t max_context_len, int32_t window,
+                                   int32_t sinks, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                   float scale, void *workspace, size_t workspace_bytes,
+                                   void *stream) {
+  if (num_seqs < 0 || num_q_heads < 1 || num_kv_heads < 1 || block_size < 1 || num_blocks < 1 ||
+      max_blocks_per_seq < 0 || max_context_len < 0 || window < 0 || sinks < 0 ||
+      !(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f))
+    return PKV_ERR_ARG;
+  if (head_dim != 128 || num_q_heads % num_kv_heads != 0) return PKV_ERR_SHAPE;
+  if (int64_t(max_context_len) > int64_t(max_blocks_per_seq) * block_size ||
+      int64_t(num_blocks) * block_size > 0x7fffffffll ||   // cache rows are numbered in int32
+      !pkv::decode_warp_fits(num_seqs, max_context_len, num_q_heads))
+    return PKV_ERR_ARG;
+  if (num_seqs == 0) return PKV_OK;
+  if (!out || !q || !k_cache || !v_cache || !context_lens ||
+      (!block_tables && max_blocks_per_seq > 0) || (fp8 && (!k_scales || !v_scales)))
+    return PKV_ERR_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      overlap(out, q, int64_t(num_seqs) * num_q_heads * head_dim * 2))
+    return PKV_ERR_ARG;
+  const size_t need = pkv::decode_warp_workspace_bytes(num_seqs, num_q_heads, num_kv_heads);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < need || workspace_bytes < 256)
+    return PKV_ERR_WORKSPACE;
+  if (need == 0) return PKV_ERR_CUDA;
+  cudaError_t e;
+  pkv::DecodeWarpArgs a;
+  a.err = pkv::device_error_word(&e);
+  if (!a.err) return PKV_ERR_CUDA;
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.block_tables = block_tables;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.context_lens = context_lens;
+  a.num_seqs = num_seqs;
+  a.max_context_len = max_context_len;
+  a.window = window;
+  a.sinks = sinks;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.scale = scale;
+  a.workspace = workspace;
+  return from_cuda(pkv::launch_decode_warp(a, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_paged_decode_fp8_block(void *out, const void *q, const void *k_cache,
+                                      const void *v_cache, const float *k_scales,
+                                      const float *v_scales, const int32_t *block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                      int32_t num_seqs, int32_t max_context_len, int32_t window,
+                                      int32_t sinks, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                      float scale, void *workspace, size_t workspace_bytes,
+                                      void *stream) {
+  return decode_warp_call(out, q, k_cache, v_cache, true, k_scales, v_scales, block_tables,
+                          max_blocks_per_seq, context_lens, num_seqs, max_context_len, window,
+                          sinks, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                          scale, workspace, workspace_bytes, stream);
+}
+
+pkv_status pkv_paged_decode_window(void *out, const void *q, const void *k_cache,
+                                   const void *v_cache, const int32_t *block_tables,
+                                   int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                   int32_t num_seqs, int32_t max_context_len, int32_t window,
+                                   int32_t sinks, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                   float scale, void *workspace, size_t workspace_bytes,
+                                   pkv_dtype dtype, void *stream) {
+  if (dtype != PKV_BF16) return PKV_ERR_DTYPE;
+  if (window < 1) return PKV_ERR_ARG;
+  return decode_warp_call(out, q, k_cache, v_cache, false, nullptr, nullptr, block_tables,
+                          max_blocks_per_seq, context_lens, num_seqs, max_context_len, window,
+                          sinks, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                          scale, workspace, workspace_bytes, stream);
+}
+
+pkv_status pkv_paged_prefill_window(void *out, const void *q, const void *k_cache,
+                                    const void *v_cache, const int32_t *cu_seqlens_q,
+                                    const int32_t *cu_seqlens_k, int32_t max_seqlen_q,
+                                    int32_t max_seqlen_k, const int32_t *block_tables,
+                                    int32_t max_blocks_per_seq, int32_t num_seqs, int32_t total_q,
+                                    int32_t window, int32_t sinks, int32_t num_q_heads,
+                                    int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                    int32_t num_blocks, float scale, void *workspace,
+                                    size_t workspace_bytes, pkv_dtype dtype, void *stream) {
+  if (dtype != PKV_BF16) return PKV_ERR_DTYPE;
+  if (num_seqs < 0 || total_q < 0 || num_q_heads < 1 || num_kv_heads < 1 || block_size < 1 ||
+      num_blocks < 1 || max_blocks_per_seq < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 ||
+      window < 1 || sinks < 0 || !(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f))
+    return PKV_ERR_ARG;
+  if (head_dim != 128 || !pkv::prefill_supported(num_q_heads, num_kv_heads, block_size))
+    return PKV_ERR_SHAPE;
+  if (int64_t(max_seqlen_k) > int64_t(max_blocks_per_seq) * block_size ||
+      // positions and cache rows, a tile past the last one included, are int32
+      max_seqlen_k > 0x7fffffff - 512 || int64_t(num_blocks) * block_size > 0x7fffffffll - 512)
+    return PKV_ERR_ARG;
+  if (num_seqs > 65535 || num_q_heads > 65535 ||
+      (int64_t(max_seqlen_q) + 127) / 128 > 65535 ||
+      !prefill_items_fit(max_seqlen_q, num_q_heads, num_kv_heads, num_seqs))
+    return PKV_ERR_ARG;
+  if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
+  if (!out || !q || !k_cache || !v_cache || !cu_seqlens_q || !cu_seqlens_k ||
+      (!block_tables && max_blocks_per_seq > 0))
+    return PKV_ERR_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < pkv::kPrefillWorkspace)
+    return PKV_ERR_WORKSPACE;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      overlap(out, q, int64_t(total_q) * num_q_heads * head_dim * 2))
+    return PKV_ERR_ARG;
+  cudaError_t e;
+  uint32_t *err = pkv::device_error_word(&e);
+  if (!err) return PKV_ERR_CUDA;
+  pkv::PrefillArgs a;
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.cu_seqlens_k = cu_seqlens_k;
+  a.max_seqlen_q = max_seqlen_q;
+  a.max_seqlen_k = max_seqlen_k;
+  a.block_tables = block_tables;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.scale = scale;
+  a.causal = 1;
+  a.err = err;
+  a.workspace = workspace;
+  a.window = window;
+  a.sinks = sinks;
+  return from_cuda(pkv::launch_paged_prefill(a, static_cast<cudaStream_t>(stream)));
+}
+
 pkv_status pkv_get_device_errors(void *stream, uint32_t *bits) {
   cudaError_t e;
   uint32_t *err = pkv::device_error_word(&e);

@@ -161,6 +161,9 @@ struct PrefillArgs {
   // CTAs of the persistent kernel (0: one per SM); items are claimed from the
   // work ticket, so two launches sharing one ticket split the items between them
   int max_ctas = 0;
+  // sliding window (0: none; causal only) behind the first `sinks` keys
+  int32_t window = 0;
+  int32_t sinks = 0;
 };
 
 constexpr size_t kPrefillWorkspace = 256;
@@ -274,5 +277,82 @@ bool tree_decode_fits(int num_seqs, int max_seqlen_q, int max_context_len, int n
 // 0 without a device.
 size_t tree_decode_workspace_bytes(int max_seqlen_q, int num_q_heads, int num_kv_heads);
 cudaError_t launch_tree_decode(const TreeDecodeArgs &a, cudaStream_t stream);
+
+// ---- fp8 cache with block scales (fp8_block.cu)
+// Caches [NB, bs, Hkv, 128] E4M3 codes, scales [NB, Hkv]; strides in elements of
+// the bf16 rows.
+struct Fp8BlockStoreArgs {
+  const __nv_bfloat16 *key;
+  const __nv_bfloat16 *value;
+  int64_t key_stride;
+  int64_t value_stride;
+  uint8_t *k_cache;
+  uint8_t *v_cache;
+  float *k_scales;
+  float *v_scales;
+  const int32_t *block_tables;
+  int32_t max_blocks_per_seq;
+  const int32_t *cu_seqlens_q;
+  const int32_t *context_lens;         // the new tokens included
+  int32_t num_seqs;
+  int32_t total_q;
+  int32_t num_kv_heads;
+  int32_t block_size;
+  int32_t num_blocks;
+  uint32_t *err;
+};
+cudaError_t launch_store_fp8_block(const Fp8BlockStoreArgs &a, cudaStream_t stream);
+
+struct Fp8BlockLoadArgs {
+  __nv_bfloat16 *key_out;
+  __nv_bfloat16 *value_out;
+  int64_t key_stride;
+  int64_t value_stride;
+  const uint8_t *k_cache;
+  const uint8_t *v_cache;
+  const float *k_scales;
+  const float *v_scales;
+  const int32_t *block_tables;
+  int32_t max_blocks_per_seq;
+  const int32_t *context_lens;
+  const int32_t *row_starts;
+  int32_t num_seqs;
+  int32_t num_rows;
+  int32_t num_kv_heads;
+  int32_t block_size;
+  int32_t num_blocks;
+  uint32_t *err;
+};
+cudaError_t launch_load_fp8_block(const Fp8BlockLoadArgs &a, cudaStream_t stream);
+
+// ---- decode by independent warps (decode_warp.cu): fp8 caches with block scales
+// (k_scales != nullptr) or bf16 caches, with an optional window and sinks
+struct DecodeWarpArgs {
+  void *out;
+  const void *q;
+  const void *k_cache;
+  const void *v_cache;
+  const float *k_scales;
+  const float *v_scales;
+  const int32_t *block_tables;
+  int32_t max_blocks_per_seq;
+  const int32_t *context_lens;
+  int32_t num_seqs;
+  int32_t max_context_len;
+  int32_t window;                      // 0: the whole context
+  int32_t sinks;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t block_size;
+  int32_t num_blocks;
+  float scale;
+  void *workspace;
+  uint32_t *err;
+};
+// 0 without a device.
+size_t decode_warp_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads);
+// Tiles of all sequences and output rows are numbered in 32 bits: whether the bounds allow it.
+bool decode_warp_fits(int num_seqs, int max_context_len, int num_q_heads);
+cudaError_t launch_decode_warp(const DecodeWarpArgs &a, cudaStream_t stream);
 
 }  // namespace pkv

@@ -68,6 +68,8 @@ constexpr int kItemRing = 4;         // work items handed from the Q/K loader to
 // q, k/v full/empty, s/p/pv x2, q_empty, o_free x2, item full/empty x kItemRing
 constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 9 + 2 * kItemRing;
 constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16 + 4 * kItemRing + 1024;
+// with a window, tiles start at a box: smaller boxes leave fewer keys that no row sees
+constexpr int kWinBoxRows = 32;
 constexpr int kItemReaders = 1 + 1 + 8;   // V loader, MMA issuer, eight softmax warps
 
 struct PPParams {
@@ -96,6 +98,11 @@ struct PPParams {
   uint32_t *ticket;  // next unclaimed work item (zeroed before the launch)
   float scale_log2;
   uint32_t *err;
+  // sliding-window instances: a row at position t sees the keys <= t that are
+  // below `sinks` or above t - `window`
+  int window;
+  int sinks;
+  const __nv_bfloat16 *q;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -152,10 +159,85 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const v
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 
+// Which keys one query row sees with a window: [0, sinks) and [first, last].
+struct SeenKeys {
+  int sinks, first, last;
+};
+
+// One row by plain arithmetic, for the rows whose sums came out not finite: in the
+// tiles a key that the row does not see has weight 0, and 0 times an infinite or
+// NaN value is NaN. Here such keys are never touched. The whole warp works on the
+// row: a lane a key for the scores, four dims a lane for the output.
+__device__ __noinline__ void recompute_row(const PPParams &p, int seq, int qh, int64_t row, SeenKeys seen) {
+  const int lane = threadIdx.x & 31;
+  const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (row * p.num_q_heads + qh) * kHD);
+  const int32_t *bt = p.block_tables + static_cast<size_t>(seq) * p.max_blocks_per_seq;
+  const int front = min(seen.sinks, seen.first);           // sinks in front of the window
+  const int count = front + seen.last - seen.first + 1;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int base = 0; base < count; base += 32) {
+    const int j = base + lane;
+    int64_t at = -1;                                       // the lane's key: its row of the cache, one head
+    if (j < count) {
+      const int key = j < front ? j : j - front + seen.first;
+      const int blk = __ldg(bt + key / p.block_size);
+      if (blk >= 0 && blk < p.num_blocks)
+        at = (static_cast<int64_t>(blk) * p.block_size + key % p.block_size) * p.num_kv_heads + qh / p.group;
+    }
+    float s = -INFINITY;
+    if (at >= 0) {
+      const uint4 *k = reinterpret_cast<const uint4 *>(p.k_cache + at * (kHD * 2));
+      float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 1
+      for (int i = 0; i < 16; ++i) {
+        const uint4 a = __ldg(q + i), b = __ldg(k + i);
+        acc = ffma2(bf16x2_to_float2(a.x), bf16x2_to_float2(b.x), acc);
+        acc = ffma2(bf16x2_to_float2(a.y), bf16x2_to_float2(b.y), acc);
+        acc = ffma2(bf16x2_to_float2(a.z), bf16x2_to_float2(b.z), acc);
+        acc = ffma2(bf16x2_to_float2(a.w), bf16x2_to_float2(b.w), acc);
+      }
+      s = (acc.x + acc.y) * p.scale_log2;
+    }
+    float top = fmaxf(m, s);
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float f = ex2(m - ref), w = ex2(s - ref);
+    m = top;
+    l = l * f + w;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    const int n = min(32, count - base);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int64_t r = __shfl_sync(0xffffffffu, at, i);
+      const float y = __shfl_sync(0xffffffffu, w, i);
+      if (r < 0) continue;
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p.v_cache + r * (kHD * 2)) + lane);
+      const float2 lo = bf16x2_to_float2(v.x), hi = bf16x2_to_float2(v.y);
+      o.x += y * lo.x;
+      o.y += y * lo.y;
+      o.z += y * hi.x;
+      o.w += y * hi.y;
+    }
+  }
+#pragma unroll
+  for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+  const float inv = 1.f / l;                               // 0 / 0: every seen score is -inf
+  reinterpret_cast<uint2 *>(p.out + (row * p.num_q_heads + qh) * kHD)[lane] =
+      make_uint2(float2_to_bf16x2(o.x * inv, o.y * inv), float2_to_bf16x2(o.z * inv, o.w * inv));
+}
+
 // kGather: the loaders gather K/V rows with cp.async (block sizes that are not
 // a multiple of 8) instead of loading TMA boxes; a separate instance, so that
 // the box path compiles as if the gather did not exist
-template <bool kGather>
+// kWin: a sliding window behind sinks. An item's keys are the sinks, rounded up to
+// whole TMA boxes, and the boxes from the first one that any of its rows sees on:
+// the walk numbers them 0, 1, ... without the gap, so its tiles are as full as the
+// boxes allow (a box start is the only alignment a tile needs), and adds the gap
+// back where a key's position counts.
+template <bool kGather, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const PPParams p) {
@@ -184,6 +266,7 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   const int n_items = n_xt * n_hp * p.num_seqs;
   struct Item {
     int seq, qh_a, r0, q_begin, q_len, k_len, prefix, n_tiles, kvh;
+    int front, gap;   // kWin: the walk's key x is the sequence's key x + (x >= front ? gap : 0)
   };
   auto item_at = [&](int w, Item &it) -> bool {
     it.r0 = (n_xt - 1 - w % n_xt) * xt_rows;
@@ -202,7 +285,17 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     it.prefix = p.causal ? it.k_len - it.q_len : 0;
     const int last_row = min(it.r0 + xt_rows - 1, it.q_len - 1);
     const int key_end = p.causal ? min(it.prefix + last_row + 1, it.k_len) : it.k_len;
-    it.n_tiles = (key_end + kTile - 1) / kTile;
+    it.front = it.gap = 0;
+    if constexpr (kWin) {
+      const int boxes = -p.box_rows;                      // mask of a box start
+      const int first = max(it.prefix + it.r0 - p.window + 1, 0) & boxes;
+      const int front = (p.sinks + p.box_rows - 1) & boxes;
+      if (first > front) {
+        it.front = front;
+        it.gap = first - front;
+      }
+    }
+    it.n_tiles = (key_end - it.gap + kTile - 1) / kTile;
     it.kvh = it.qh_a / p.group;
     return true;
   };
@@ -385,7 +478,8 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             for (int u = 0; u < kTile / 32; ++u) {
               // cache row of key 32u + lane of the tile, -1 for none
               int my_row = -1;
-              const int key_l = j * kTile + 32 * u + lane;
+              int key_l = j * kTile + 32 * u + lane;
+              if constexpr (kWin) key_l += key_l >= it.front ? it.gap : 0;
               if (key_l < it.k_len) {
                 const int blk = __ldg(bt + key_l / p.block_size);
                 if (blk >= 0 && blk < p.num_blocks) my_row = blk * p.block_size + key_l % p.block_size;
@@ -414,7 +508,8 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             const int round = issued / stages;
             int row = oob_row;
             if (lane < pieces) {
-              const int key = j * kTile + lane * R;
+              int key = j * kTile + lane * R;
+              if constexpr (kWin) key += key >= it.front ? it.gap : 0;
               if (key < it.k_len) {
                 const int blk = __ldg(bt + key / p.block_size);
                 if (blk >= 0 && blk < p.num_blocks) row = blk * p.block_size + key % p.block_size;
@@ -562,6 +657,10 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       const int qpos = it.prefix + r0x + r;
       const int visible = p.causal ? min(qpos + 1, it.k_len) : it.k_len;
       float m_used = -INFINITY, l_sum = 0.f;         // running max of raw scores, row sum
+      // kWin, in the walk's numbering: the row sees x < see_front and see_lo <= x < see_hi
+      const int see_front = kWin ? p.sinks : 0;
+      const int see_lo = kWin ? max(qpos - p.window + 1 - it.gap, it.front) : 0;
+      const int see_hi = qpos + 1 - it.gap;
 
       for (int j = 0; ok && j < it.n_tiles; ++j) {
         if (!warp_wait(s_full(x), (tiles_done + j) & 1, abort_flag)) { ok = false; break; }
@@ -573,7 +672,31 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tmem_wait_ld();
 
         const int key0 = j * kTile;
-        if (key0 + kTile > visible) {
+        if constexpr (kWin) {
+          if (key0 + kTile > see_hi) {
+#pragma unroll
+            for (int e = 0; e < kTile; ++e) s[e] = (key0 + e < see_hi) ? s[e] : -INFINITY;
+          }
+          if (max(key0, see_front) < min(see_lo, key0 + kTile)) {
+#pragma unroll
+            for (int e = 0; e < kTile; ++e)
+              s[e] = (key0 + e < see_front || key0 + e >= see_lo) ? s[e] : -INFINITY;
+          }
+          // rows of a box behind the sequence's last key hold whatever the pool does:
+          // zero their values (weight 0 times NaN is NaN); the keys' scores are masked
+          if constexpr (!kGather) {
+            const int real = it.k_len - it.gap - key0;      // the tile's rows of the sequence
+            if (x == 0 && real < kTile && real % p.box_rows != 0) {
+              const int vt = tiles_done + j;
+              if (!warp_wait(v_full(vt % kVStages), (vt / kVStages) & 1, abort_flag)) { ok = false; break; }
+              const int end = (real + p.box_rows - 1) & -p.box_rows;
+              for (int i = real * 16 + r; i < end * 16; i += kTile)   // 16-byte pieces: 8 a row and half
+                *reinterpret_cast<uint4 *>(smem + kOffV + (vt % kVStages) * kTileBytes + ((i >> 3) & 1) * kRegion +
+                                           (i >> 4) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+            }
+          }
+        } else if (key0 + kTile > visible) {
 #pragma unroll
           for (int e = 0; e < kTile; ++e) s[e] = (key0 + e < visible) ? s[e] : -INFINITY;
         }
@@ -604,7 +727,8 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         // P = exp2(s*c - m*c) as bf16 pairs over TMEM columns 0..63 of S_X; the
         // scaling and the row sum run two lanes per instruction (FFMA2 / FADD2).
-        const float mc = m_used * c;
+        // (with a window a row may have seen nothing yet)
+        const float mc = kWin && m_used == -INFINITY ? 0.f : m_used * c;
         float2 rs2[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) rs2[i] = make_float2(0.f, 0.f);
@@ -639,6 +763,7 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       __nv_bfloat16 *orow = p.out + (static_cast<size_t>(it.q_begin) + r0x + r) * p.num_q_heads * kHD +
                             static_cast<size_t>(it.qh_a + x * head_step) * kHD;
       const float inv = (l_sum > 0.f) ? 1.f / l_sum : 0.f;
+      bool again = !(l_sum > 0.f);                     // kWin: the row is computed again below
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
         float o[32];
@@ -660,12 +785,32 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             v.w = float2_to_bf16x2(o[q4 * 8 + 6] * inv, o[q4 * 8 + 7] * inv);
             dst[q4] = v;
           }
+          if constexpr (kWin) {
+            // 0 * x is 0 for finite x, NaN otherwise, and stays NaN in a sum
+            float2 any = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              any = ffma2(make_float2(o[e], o[e + 1]), make_float2(0.f, 0.f), any);
+            again |= !(any.x + any.y == 0.f);
+          }
         }
       }
       if (have) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(o_free(x));
+      }
+      if constexpr (kWin) {
+        if (have && ok) {
+          uint32_t rows = __ballot_sync(0xffffffffu, store && again);
+          while (rows != 0) {
+            const int src = __ffs(rows) - 1;
+            rows &= rows - 1;
+            const int t = __shfl_sync(0xffffffffu, qpos, src);
+            recompute_row(p, it.seq, it.qh_a + x * head_step, static_cast<int64_t>(it.q_begin) + t - it.prefix,
+                          SeenKeys{p.sinks, max(t - p.window + 1, 0), t});
+          }
+        }
       }
       tiles_done += it.n_tiles;
     }
@@ -720,7 +865,8 @@ cudaError_t launch_prefill_pp(const PrefillArgs &a, cudaStream_t stream) {
   static std::once_flag attr_once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(attr_once, [] {
-    for (auto kern : {prefill_pp_kernel<false>, prefill_pp_kernel<true>}) {
+    for (auto kern : {prefill_pp_kernel<false, false>, prefill_pp_kernel<true, false>,
+                      prefill_pp_kernel<false, true>, prefill_pp_kernel<true, true>}) {
       if (attr_err == cudaSuccess)
         attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
       // setmaxnreg.inc waits until the registers it asks for are free; the split
@@ -732,9 +878,13 @@ cudaError_t launch_prefill_pp(const PrefillArgs &a, cudaStream_t stream) {
     }
   });
   if (attr_err != cudaSuccess) return attr_err;
-  auto kern = (a.block_size % 8 != 0) ? prefill_pp_kernel<true> : prefill_pp_kernel<false>;
+  const bool gather = a.block_size % 8 != 0, windowed = a.window > 0;
+  auto kern = gather ? (windowed ? prefill_pp_kernel<true, true> : prefill_pp_kernel<true, false>)
+                     : (windowed ? prefill_pp_kernel<false, true> : prefill_pp_kernel<false, false>);
   int box_rows = a.block_size & -a.block_size;
   if (box_rows > kTile) box_rows = kTile;
+  if (windowed && gather) box_rows = 1;
+  if (windowed && !gather && box_rows > kWinBoxRows) box_rows = kWinBoxRows;
   CUtensorMap tq, tk, tv;
   const uint64_t cache_rows = static_cast<uint64_t>(a.num_blocks) * a.block_size;
   if (!make_map(&tq, a.q, a.total_q, a.num_q_heads, kTile) ||
@@ -764,6 +914,9 @@ cudaError_t launch_prefill_pp(const PrefillArgs &a, cudaStream_t stream) {
   p.err = a.err;
   p.q_tiles = (a.max_seqlen_q + kTile - 1) / kTile;
   p.pair_tiles = (p.group % 2 != 0) ? 1 : 0;
+  p.window = a.window;
+  p.sinks = a.sinks < a.max_seqlen_k ? a.sinks : a.max_seqlen_k;
+  p.q = static_cast<const __nv_bfloat16 *>(a.q);
   p.ticket = static_cast<uint32_t *>(a.workspace);
   if (p.ticket == nullptr) return cudaErrorInvalidValue;
   if (!a.ticket_zeroed)
