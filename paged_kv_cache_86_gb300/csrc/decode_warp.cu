@@ -9,44 +9,57 @@
 // The work is HBM-bound: a key and a value of one KV head are 256 bytes (fp8)
 // and feed the `group` query heads that share them, 4 * 128 * group operations.
 // The tensor core is needed only because the CUDA cores would not keep up with
-// group * 2 operations a byte; its rate is not what counts. So instead of whole
-// tiles through shared memory, with warps meeting at barriers (decode_tcg.cu),
-// a warp loads 16 tokens of one KV head straight into the registers that
-// mma.m16n8k16 takes them from, and nothing is exchanged with another warp
-// before the end of its keys:
+// group * 2 operations a byte; its rate is not what counts. What counts is that
+// no warp waits for another one: decode_tcg.cu feeds the tensor core tiles of all
+// KV heads, and its softmax warps meet once a tile; here a warp owns 16 tokens of
+// one KV head at a time and the mma.m16n8k16 that work on them,
 //   S^T [16 tokens x 8 heads] = K [16 x 128] Q^T      8 MMAs
 //   O^T [128 dims x 8 heads] += V^T [128 x 16] P^T    8 MMAs, P^T from S^T by
 //                                                     two 8x8 transposes
-// The order of the 128 dims inside the contraction is free, and so is the order
-// of O's rows, so both are chosen so that every global load is 16 bytes a lane:
-// of S's contraction a lane holds 16 (fp8) or 8 (bf16) neighbouring dims, and of
-// V's rows the dims of 16 (8) neighbours of four tokens. Codes become f16 (exact)
-// two at a time; scales are applied to the scores and to the weights. Loads of the
-// next tile's K are issued when the tile's S has been computed, V's after its PV,
-// the block table is looked up one tile further ahead.
+// and nothing is exchanged before the end of its keys. Codes become f16 (exact) two
+// at a time; scales are applied to the scores and to the weights.
+//
+// The keys come to the warps in one of two ways. Block sizes that 8 divides: a
+// producer warp copies tiles of all KV heads, which are contiguous in the cache, by
+// TMA into a ring that fills the SM's shared memory (decode_ring_kernel). Others:
+// every warp loads its rows straight into the registers that the MMAs take them
+// from (decode_direct_kernel), whose 128- or 256-byte pieces, read at eight
+// different times, DRAM serves at half the rate: 512 sequences (fp8, 0.59 M tokens)
+// 413 us against 220, behind a window of 1024 (bf16) 422 against 268.
 //
 // Split: the seen tokens of all sequences, in tiles of 16 with kSegTiles of
 // overhead in front of each sequence, are one line that is cut into equal ranges;
-// a warp takes one range of one KV head, the warps of a CTA neighbouring heads, so
-// that a token's heads are read at the same time from one place. A sequence that a
-// cut goes through leaves (m, l, O) records that a second launch merges.
+// a ring (a direct warp) takes one range. A sequence that a cut goes through leaves
+// (m, l, O) records that a second launch merges.
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "pkv_tc.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kHD = 128;
-constexpr int kWarps = 8;                  // of a CTA
-constexpr int kThreads = kWarps * 32;
 constexpr int kTok = 16;                   // tokens of a tile
 constexpr int kSegTiles = 2;               // what starting a sequence costs, in tiles
 constexpr int kMinTiles = 4;               // shortest range
+constexpr int kDirectWarps = 8;            // warps of a CTA, direct loads
+// Warps of a CTA with rings, producers included, and so the registers of a thread
+// (168, 204). With 18 (96 registers, spills; two rings for 8 KV heads instead of
+// one) 512 sequences took 263 us (fp8) and 274 us (bf16, window of 1024), with 12
+// 220 and 268.
+constexpr int kNarrowWarps = 12;           // one tile of 8 query heads a warp
+constexpr int kWideWarps = 10;             // two
+constexpr int kCombineWarps = 8;
+constexpr int kRingBytes = 220 * 1024;     // of all stages of a CTA
+constexpr int kMaxStages = 16;             // of one ring
 constexpr float kLog2e = 1.4426950408889634f;
 // A reference maximum is kept until a score exceeds it by this (log2): weights
 // stay below 2^kGrow (bf16: exact range) and f16 weights, which are also scaled
@@ -82,6 +95,12 @@ struct WarpParams {
   int sinks;
   float scale_log2;
   int ranges;          // most ranges the line is cut into
+  // shared-memory rings (decode_ring_kernel)
+  int unit;            // tokens of a box: 16 or 8
+  int heads_per_cta;   // KV heads of a box
+  int head_groups;     // boxes over all KV heads
+  int rings;           // of a CTA
+  int stages;          // of a ring
   int *plan;           // [0] tiles of a range, [1 ..] starts of the sequences on the line
   float4 *ml;          // records: (m, l, M)
   float *po;           // and O
@@ -137,183 +156,45 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Seen tokens of a sequence, how many positions behind the sinks are left out.
-struct Seen {
-  int n, shift;
-};
 
-__device__ __forceinline__ Seen seen_of(const WarpParams &p, int i, bool report) {
-  int ctx = __ldg(p.context_lens + i);
-  if (ctx < 0 || ctx > p.max_context_len) {
-    if (report) raise_error(p.err, PKV_DEVERR_LENGTH);
-    ctx = min(max(ctx, 0), p.max_context_len);
-  }
-  Seen s{ctx, 0};
-  if (p.window > 0) s.shift = max(max(ctx - p.window, 0) - p.sinks, 0);
-  s.n = ctx - s.shift;
-  return s;
-}
-
-__device__ __forceinline__ int tiles_of(int n) { return (n + kTok - 1) / kTok; }
-__device__ __forceinline__ int cost_of(int n) { return n > 0 ? tiles_of(n) + kSegTiles : 0; }
-
-template <bool kFp8> constexpr int kLoads = kFp8 ? 2 : 4;   // 16-byte loads of a row's part a lane takes
-
-// First dim of the d-th group of neighbours that a lane holds of a K row (and of
-// Q), lane % 4 = kp, and of a V row (and of O), lane / 4 = n.
-template <bool kFp8>
-__device__ __forceinline__ int k_dim(int d, int kp) { return kFp8 ? 64 * d + 16 * kp : 32 * d + 8 * kp; }
-
-// NT: tiles of 8 query heads a warp computes for its KV head
+// The operands of the two products, as a lane of mma.m16n8k16 holds them: fragment
+// row (column of B) g = lane / 4, pair kp = lane % 4. The 128 dims of S's
+// contraction may come in any order, and so may O's rows: a lane takes runs of
+// neighbouring dims, so that it loads 16 bytes at a time.
+//   K, Q: fp8 dims 32 kp + 0 .. 31; bf16 64 j + 16 kp + 0 .. 15, j = 0, 1
+//   V, O: fp8 dims 16 g + 0 .. 15;  bf16 64 j + 8 g + 0 .. 7,   j = 0, 1
 template <bool kFp8, int NT>
-__global__ void __launch_bounds__(kThreads, kFp8 && NT == 1 ? 2 : 1)
-decode_warp_kernel(const WarpParams p) {
-  __shared__ int s_part[kWarps], s_seq[kWarps], s_pos[kWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, kp = lane & 3;       // MMA fragments: row (column of B) g, pair kp
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+struct Heads {
+  static constexpr int kKL = kFp8 ? 2 : 4;   // 16-byte loads of a lane's part of a K row
+  static constexpr int kVL = kFp8 ? 1 : 2;   // and of a V row
 
-  // ---- plan: where this CTA's ranges start on the line of all sequences
-  const int vheads = p.num_kv_heads * p.chunks;
-  const int per = (p.num_seqs + kThreads - 1) / kThreads;
-  const int lo = min(tid * per, p.num_seqs), hi = min(lo + per, p.num_seqs);
-  int mine = 0;
-  for (int i = lo; i < hi; ++i) mine += cost_of(seen_of(p, i, blockIdx.x == 0).n);
-  int inc = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, inc, off);
-    if (lane >= off) inc += o;
+  uint32_t qf[NT][8][2];            // Q^T: element (k, head g) of each of the 8 steps
+  float qmul[NT][2];                // score factor of heads 2 kp, 2 kp + 1
+  float o[NT][8][4];                // O^T
+  // for heads 2 kp, 2 kp + 1: reference maxima of the scores and (fp8) of the scores
+  // plus the log of the values' scale, and the lane's part of the sum of weights
+  float m[NT][2], mw[NT][2], l[NT][2];
+
+  // First dim of the lane's i-th 8 dims.
+  static __device__ __forceinline__ int q_dim(int i, int kp) {
+    return kFp8 ? 32 * kp + 8 * i : 64 * (i >> 1) + 16 * kp + 8 * (i & 1);
   }
-  if (lane == 31) s_part[warp] = inc;
-  if (tid < kWarps) s_seq[tid] = p.num_seqs;
-  __syncthreads();
-  int before = inc - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_part[w];
-    total += s_part[w];
-  }
-  const int range_len = max((total + p.ranges - 1) / p.ranges, kMinTiles);
-  {
-    int at = before;
-    for (int i = lo; i < hi; ++i) {
-      const int end = at + cost_of(seen_of(p, i, false).n);
-      for (int w = 0; w < kWarps; ++w) {
-        const long long first = static_cast<long long>((blockIdx.x * kWarps + w) / vheads) * range_len;
-        if (first >= at && first < end) {
-          s_seq[w] = i;
-          s_pos[w] = at;
-        }
-      }
-      if (blockIdx.x == 0) p.plan[1 + i] = at;
-      at = end;
-    }
-    if (blockIdx.x == 0 && tid == 0) {
-      p.plan[0] = range_len;
-      p.plan[1 + p.num_seqs] = total;
-    }
-  }
-  __syncthreads();
 
-  const int range = (blockIdx.x * kWarps + warp) / vheads;
-  const int vh = (blockIdx.x * kWarps + warp) % vheads;
-  const int kvh = vh / p.chunks, head0 = vh % p.chunks * p.per_chunk;
-  const int heads = min(p.per_chunk, p.group - head0);       // of this warp
-  const long long line0 = static_cast<long long>(range) * range_len;
-  const int line1 = static_cast<int>(min(line0 + range_len, static_cast<long long>(total)));
-  constexpr int kRow = kFp8 ? kHD : 2 * kHD;                 // bytes of a head's row
-  const int64_t row_bytes = static_cast<int64_t>(p.num_kv_heads) * kRow;
-  const uint8_t *kbase = p.k_cache + kvh * kRow + k_dim<kFp8>(0, kp) * (kRow / kHD);
-  const uint8_t *vbase = p.v_cache + kvh * kRow + 16 * g;
-  // bytes between a lane's 16-byte loads of one K row / V row
-  constexpr int kStepK = 64, kStepV = 128;
-  constexpr int kKL = kFp8 ? 2 : 4, kVL = kFp8 ? 1 : 2;
-
-  int seq = s_seq[warp], pos = s_pos[warp];
-  for (; seq < p.num_seqs && pos < line1; ++seq) {
-    const Seen seen = seen_of(p, seq, false);
-    const int tiles = tiles_of(seen.n);
-    const int first_tile = pos + kSegTiles;                  // on the line
-    const int t0 = static_cast<int>(max(line0 - first_tile, 0ll)), t1 = min(line1 - first_tile, tiles);
-    pos += cost_of(seen.n);
-    if (t0 >= t1) continue;
-    const bool whole = t0 == 0 && t1 == tiles;
-
-    // the lane's token of a tile: its block and its row in the block
-    const int32_t *bt = p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq;
-    auto look_up = [&](int t, int &id, int &off) {
-      const int j = t * kTok + (lane & 15);
-      id = -1;
-      off = 0;
-      if (t < t1 && j < seen.n) {
-        const uint32_t at = j + (j >= p.sinks ? seen.shift : 0);
-        const uint32_t b = div_of(at, p.bs);
-        off = static_cast<int>(at - b * p.bs.d);
-        id = __ldg(bt + b);
-      }
-    };
-    // cache row of the lane's token (-1: none); its scale, of K in the lower half
-    // of the warp and of V in the upper
-    auto resolve = [&](int t, int id, int off, int &row, float &scale) {
-      const bool real = t < t1 && t * kTok + (lane & 15) < seen.n;
-      const bool good = real && id >= 0 && id < p.num_blocks;
-      if (real && !good && lane < 16) raise_error(p.err, PKV_DEVERR_BLOCK_ID);
-      row = good ? id * static_cast<int>(p.bs.d) + off : -1;
-      scale = 0.f;
-      if constexpr (kFp8)
-        if (good) scale = __ldg((lane < 16 ? p.k_scales : p.v_scales) + static_cast<int64_t>(id) * p.num_kv_heads + kvh);
-    };
-    uint4 kr[2][kKL], vr[4][kVL];
-    auto load_k = [&](int row) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int r = __shfl_sync(0xffffffffu, row, g + 8 * x);
-        const uint8_t *src = kbase + r * row_bytes;
-#pragma unroll
-        for (int d = 0; d < kKL; ++d) kr[x][d] = r >= 0 ? ld_once(src + d * kStepK) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto load_v = [&](int row) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int r = __shfl_sync(0xffffffffu, row, 2 * kp + (x & 1) + 8 * (x >> 1));
-        const uint8_t *src = vbase + r * row_bytes;
-#pragma unroll
-        for (int d = 0; d < kVL; ++d) vr[x][d] = r >= 0 ? ld_once(src + d * kStepV) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    int id, off, row;
-    float scale;
-    look_up(t0, id, off);
-    resolve(t0, id, off, row, scale);
-    look_up(t0 + 1, id, off);
-    load_k(row);
-    load_v(row);
-
-    // ---- Q: B fragments, element (k, head g); qmul of the lane's heads 2 kp, 2 kp + 1
-    uint32_t qf[NT][8][2];
-    float qmul[NT][2];
+  // q: the first of `heads` rows.
+  __device__ __forceinline__ void start(const __nv_bfloat16 *q, int heads, float scale_log2) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, kp = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int h = nt * 8 + g;
-      uint4 x[4];
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        // fp8: a lane's 16 dims are two loads
-        const int dim = kFp8 ? k_dim<kFp8>(d >> 1, kp) + 8 * (d & 1) : k_dim<kFp8>(d, kp);
-        x[d] = make_uint4(0, 0, 0, 0);
-        if (h < heads)
-          x[d] = __ldg(reinterpret_cast<const uint4 *>(
-              p.q + (static_cast<int64_t>(seq) * p.num_q_heads + kvh * p.group + head0 + h) * kHD + dim));
-      }
       uint32_t w[16];
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        w[4 * d] = x[d].x;
-        w[4 * d + 1] = x[d].y;
-        w[4 * d + 2] = x[d].z;
-        w[4 * d + 3] = x[d].w;
+      for (int i = 0; i < 4; ++i) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (h < heads) x = __ldg(reinterpret_cast<const uint4 *>(q + h * kHD + q_dim(i, kp)));
+        w[4 * i] = x.x;
+        w[4 * i + 1] = x.y;
+        w[4 * i + 2] = x.z;
+        w[4 * i + 3] = x.w;
       }
       if constexpr (kFp8) {
         // f16 has three bits more than bf16 but a small range: the head's row is
@@ -333,21 +214,16 @@ decode_warp_kernel(const WarpParams p) {
           w[i] = *reinterpret_cast<const uint32_t *>(&hh);
         }
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        qmul[nt][0] = p.scale_log2 * __shfl_sync(0xffffffffu, down, 8 * kp);
-        qmul[nt][1] = p.scale_log2 * __shfl_sync(0xffffffffu, down, 8 * kp + 4);
+        qmul[nt][0] = scale_log2 * __shfl_sync(0xffffffffu, down, 8 * kp);
+        qmul[nt][1] = scale_log2 * __shfl_sync(0xffffffffu, down, 8 * kp + 4);
       } else {
-        qmul[nt][0] = qmul[nt][1] = p.scale_log2;
+        qmul[nt][0] = qmul[nt][1] = scale_log2;
       }
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         qf[nt][s][0] = w[2 * s];
         qf[nt][s][1] = w[2 * s + 1];
       }
-    }
-
-    float o[NT][8][4], m[NT][2], mw[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -358,162 +234,154 @@ decode_warp_kernel(const WarpParams p) {
         l[nt][e] = 0.f;
       }
     }
+  }
 
-#pragma unroll 1
-    for (int t = t0; t < t1; ++t) {
-      // ---- S^T = K Q^T
-      float s[NT][4];
+  // S^T = K Q^T from the lane's parts of the K rows of tokens g and g + 8: s[0, 1] are
+  // token g's scores of heads 2 kp, 2 kp + 1, s[2, 3] token g + 8's. Two chains of four
+  // MMAs instead of one of eight.
+  __device__ __forceinline__ void scores(const uint4 (&k)[2][kKL], float (&s)[NT][4]) const {
+    float odd[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[nt][e] = odd[nt][e] = 0.f;
 #pragma unroll
-      for (int st = 0; st < 8; ++st) {
-        uint32_t a[4];
-        if constexpr (kFp8) {
-          const uint32_t *x0 = &kr[0][st >> 2].x, *x1 = &kr[1][st >> 2].x;
-          const uint32_t w0 = x0[st & 3], w1 = x1[st & 3];
-          a[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(w0));
-          a[1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w1));
-          a[2] = e4m3x2_to_f16x2(static_cast<uint16_t>(w0 >> 16));
-          a[3] = e4m3x2_to_f16x2(static_cast<uint16_t>(w1 >> 16));
-        } else {
-          const uint32_t *x0 = &kr[0][st >> 1].x, *x1 = &kr[1][st >> 1].x;
-          a[0] = x0[2 * (st & 1)];
-          a[1] = x1[2 * (st & 1)];
-          a[2] = x0[2 * (st & 1) + 1];
-          a[3] = x1[2 * (st & 1) + 1];
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16<kFp8>(s[nt], a[0], a[1], a[2], a[3], qf[nt][st][0], qf[nt][st][1]);
-      }
-      // the lane's two tokens, g and g + 8, and their scales
-      const bool real0 = __shfl_sync(0xffffffffu, row, g) >= 0, real1 = __shfl_sync(0xffffffffu, row, g + 8) >= 0;
-      float ks0 = 1.f, ks1 = 1.f, vs0 = 0.f, vs1 = 0.f;
+    for (int st = 0; st < 8; ++st) {
+      uint32_t a[4];
       if constexpr (kFp8) {
-        ks0 = __shfl_sync(0xffffffffu, scale, g);
-        ks1 = __shfl_sync(0xffffffffu, scale, g + 8);
-        const float ls = lg2(scale);
-        vs0 = __shfl_sync(0xffffffffu, ls, g + 16);
-        vs1 = __shfl_sync(0xffffffffu, ls, g + 24);
+        const uint32_t w0 = (&k[0][st >> 2].x)[st & 3], w1 = (&k[1][st >> 2].x)[st & 3];
+        a[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(w0));
+        a[1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w1));
+        a[2] = e4m3x2_to_f16x2(static_cast<uint16_t>(w0 >> 16));
+        a[3] = e4m3x2_to_f16x2(static_cast<uint16_t>(w1 >> 16));
+      } else {
+        a[0] = (&k[0][st >> 1].x)[2 * (st & 1)];
+        a[1] = (&k[1][st >> 1].x)[2 * (st & 1)];
+        a[2] = (&k[0][st >> 1].x)[2 * (st & 1) + 1];
+        a[3] = (&k[1][st >> 1].x)[2 * (st & 1) + 1];
       }
-      // next tile's K while the softmax runs
-      int next_row = -1;
-      float next_scale = 0.f;
-      if (t + 1 < t1) {
-        resolve(t + 1, id, off, next_row, next_scale);
-        look_up(t + 2, id, off);
-        load_k(next_row);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        mma16<kFp8>(st & 1 ? odd[nt] : s[nt], a[0], a[1], a[2], a[3], qf[nt][st][0], qf[nt][st][1]);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] += odd[nt][e];
+  }
+
+  // The weights of the tile as B fragments of P^T. real, ks, vs: whether tokens g and
+  // g + 8 count, their keys' scale and the log2 of their values' scale (fp8).
+  __device__ __forceinline__ void weights(float (&s)[NT][4], bool real0, bool real1, float ks0, float ks1,
+                                          float vs0, float vs1, uint32_t (&pb)[NT][2]) {
+    bool grow = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x = s[nt][e] * qmul[nt][e & 1];
+        if constexpr (kFp8) x *= e < 2 ? ks0 : ks1;
+        x = (e < 2 ? real0 : real1) ? x : -INFINITY;
+        s[nt][e] = x;
+        grow |= x > m[nt][e & 1] + kGrow;
+        if constexpr (kFp8) grow |= x + (e < 2 ? vs0 : vs1) > mw[nt][e & 1] + kGrow;
       }
-      // ---- softmax against the kept maxima
-      bool grow = false;
+    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = s[nt][e] * qmul[nt][e & 1];
-          if constexpr (kFp8) x *= e < 2 ? ks0 : ks1;
-          x = (e < 2 ? real0 : real1) ? x : -INFINITY;
-          s[nt][e] = x;
-          grow |= x > m[nt][e & 1] + kGrow;
-          if constexpr (kFp8) grow |= x + (e < 2 ? vs0 : vs1) > mw[nt][e & 1] + kGrow;
-        }
-      if (__any_sync(0xffffffffu, grow)) {
+        for (int e = 0; e < 2; ++e) {
+          float top = fmaxf(s[nt][e], s[nt][e + 2]);
+          float topw = kFp8 ? fmaxf(s[nt][e] + vs0, s[nt][e + 2] + vs1) : 0.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(s[nt][e], s[nt][e + 2]);
-            float topw = kFp8 ? fmaxf(s[nt][e] + vs0, s[nt][e + 2] + vs1) : 0.f;
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) {
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-              if constexpr (kFp8) topw = fmaxf(topw, __shfl_xor_sync(0xffffffffu, topw, x));
-            }
-            top = fmaxf(top, m[nt][e]);
-            const float f = top == -INFINITY ? 1.f : ex2(m[nt][e] - top);
-            m[nt][e] = top;
-            l[nt][e] *= f;
-            float fo = f;
-            if constexpr (kFp8) {
-              topw = fmaxf(topw, mw[nt][e]);
-              fo = topw == -INFINITY ? 1.f : ex2(mw[nt][e] - topw);
-              mw[nt][e] = topw;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              o[nt][i][e] *= fo;
-              o[nt][i][e + 2] *= fo;
-            }
+          for (int x = 4; x < 32; x <<= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            if constexpr (kFp8) topw = fmaxf(topw, __shfl_xor_sync(0xffffffffu, topw, x));
           }
-      }
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-          w[e] = ex2(s[nt][e] - ref);
+          top = fmaxf(top, m[nt][e]);
+          const float f = top == -INFINITY ? 1.f : ex2(m[nt][e] - top);
+          m[nt][e] = top;
+          l[nt][e] *= f;
+          float fo = f;
           if constexpr (kFp8) {
-            l[nt][e & 1] += w[e];
-            const float refw = mw[nt][e & 1] == -INFINITY ? 0.f : mw[nt][e & 1];
-            w[e] = ex2(s[nt][e] + (e < 2 ? vs0 : vs1) - (refw - kLift));
+            topw = fmaxf(topw, mw[nt][e]);
+            fo = topw == -INFINITY ? 1.f : ex2(mw[nt][e] - topw);
+            mw[nt][e] = topw;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            o[nt][i][e] *= fo;
+            o[nt][i][e + 2] *= fo;
           }
         }
-        if constexpr (kFp8) {
-          const __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
-          pb[nt][0] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h0));
-          pb[nt][1] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h1));
-        } else {
-          // the sum is of the rounded weights, so that the output stays a mean of V
-          const uint32_t h0 = float2_to_bf16x2(w[0], w[1]), h1 = float2_to_bf16x2(w[2], w[3]);
-          const float2 r0 = bf16x2_to_float2(h0), r1 = bf16x2_to_float2(h1);
-          l[nt][0] += r0.x + r1.x;
-          l[nt][1] += r0.y + r1.y;
-          pb[nt][0] = transpose8x8(h0);
-          pb[nt][1] = transpose8x8(h1);
-        }
-      }
-      // ---- O^T += V^T P^T: tile i has the dims 2 i, 2 i + 1 of each lane's 16
-#pragma unroll
-      for (int w = 0; w < (kFp8 ? 4 : 8); ++w) {
-        uint32_t a[8];
-        if constexpr (kFp8) {
-          // words of four dims: (token, next token) codes of a dim side by side
-          const uint32_t x0 = (&vr[0][0].x)[w], x1 = (&vr[1][0].x)[w], x2 = (&vr[2][0].x)[w], x3 = (&vr[3][0].x)[w];
-          const uint32_t p0 = __byte_perm(x0, x1, 0x5140), p1 = __byte_perm(x0, x1, 0x7362);
-          const uint32_t p2 = __byte_perm(x2, x3, 0x5140), p3 = __byte_perm(x2, x3, 0x7362);
-          a[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(p0));
-          a[1] = e4m3x2_to_f16x2(static_cast<uint16_t>(p0 >> 16));
-          a[2] = e4m3x2_to_f16x2(static_cast<uint16_t>(p2));
-          a[3] = e4m3x2_to_f16x2(static_cast<uint16_t>(p2 >> 16));
-          a[4] = e4m3x2_to_f16x2(static_cast<uint16_t>(p1));
-          a[5] = e4m3x2_to_f16x2(static_cast<uint16_t>(p1 >> 16));
-          a[6] = e4m3x2_to_f16x2(static_cast<uint16_t>(p3));
-          a[7] = e4m3x2_to_f16x2(static_cast<uint16_t>(p3 >> 16));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16<kFp8>(o[nt][2 * w], a[0], a[1], a[2], a[3], pb[nt][0], pb[nt][1]);
-            mma16<kFp8>(o[nt][2 * w + 1], a[4], a[5], a[6], a[7], pb[nt][0], pb[nt][1]);
-          }
-        } else {
-          const uint32_t x0 = (&vr[0][w >> 2].x)[w & 3], x1 = (&vr[1][w >> 2].x)[w & 3];
-          const uint32_t x2 = (&vr[2][w >> 2].x)[w & 3], x3 = (&vr[3][w >> 2].x)[w & 3];
-          a[0] = __byte_perm(x0, x1, 0x5410);
-          a[1] = __byte_perm(x0, x1, 0x7632);
-          a[2] = __byte_perm(x2, x3, 0x5410);
-          a[3] = __byte_perm(x2, x3, 0x7632);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16<kFp8>(o[nt][w], a[0], a[1], a[2], a[3], pb[nt][0], pb[nt][1]);
-        }
-      }
-      if (t + 1 < t1) load_v(next_row);
-      row = next_row;
-      scale = next_scale;
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
+        w[e] = ex2(s[nt][e] - ref);
+        if constexpr (kFp8) {
+          l[nt][e & 1] += w[e];
+          const float refw = mw[nt][e & 1] == -INFINITY ? 0.f : mw[nt][e & 1];
+          w[e] = ex2(s[nt][e] + (e < 2 ? vs0 : vs1) - (refw - kLift));
+        }
+      }
+      uint32_t h0, h1;
+      if constexpr (kFp8) {
+        const __half2 x0 = __floats2half2_rn(w[0], w[1]), x1 = __floats2half2_rn(w[2], w[3]);
+        h0 = *reinterpret_cast<const uint32_t *>(&x0);
+        h1 = *reinterpret_cast<const uint32_t *>(&x1);
+      } else {
+        // the sum is of the rounded weights, so that the output stays a mean of V
+        h0 = float2_to_bf16x2(w[0], w[1]);
+        h1 = float2_to_bf16x2(w[2], w[3]);
+        const float2 r0 = bf16x2_to_float2(h0), r1 = bf16x2_to_float2(h1);
+        l[nt][0] += r0.x + r1.x;
+        l[nt][1] += r0.y + r1.y;
+      }
+      pb[nt][0] = transpose8x8(h0);
+      pb[nt][1] = transpose8x8(h1);
+    }
+  }
 
-    // ---- the sequence's rows, or a record of this range's part
+  // O^T += V^T P^T from the lane's parts of the V rows of tokens 2 kp, 2 kp + 1,
+  // 2 kp + 8, 2 kp + 9. MMA i has the dims 2 i, 2 i + 1 of each lane's 16.
+  __device__ __forceinline__ void accumulate(const uint4 (&v)[4][kVL], const uint32_t (&pb)[NT][2]) {
+#pragma unroll
+    for (int w = 0; w < (kFp8 ? 4 : 8); ++w) {
+      const uint32_t x0 = (&v[0][w >> 2].x)[w & 3], x1 = (&v[1][w >> 2].x)[w & 3];
+      const uint32_t x2 = (&v[2][w >> 2].x)[w & 3], x3 = (&v[3][w >> 2].x)[w & 3];
+      if constexpr (kFp8) {
+        // words of four dims: (token, next token) codes of a dim side by side
+        const uint32_t p0 = __byte_perm(x0, x1, 0x5140), p1 = __byte_perm(x0, x1, 0x7362);
+        const uint32_t p2 = __byte_perm(x2, x3, 0x5140), p3 = __byte_perm(x2, x3, 0x7362);
+        const uint32_t a0 = e4m3x2_to_f16x2(static_cast<uint16_t>(p0));
+        const uint32_t a1 = e4m3x2_to_f16x2(static_cast<uint16_t>(p0 >> 16));
+        const uint32_t a2 = e4m3x2_to_f16x2(static_cast<uint16_t>(p2));
+        const uint32_t a3 = e4m3x2_to_f16x2(static_cast<uint16_t>(p2 >> 16));
+        const uint32_t b0 = e4m3x2_to_f16x2(static_cast<uint16_t>(p1));
+        const uint32_t b1 = e4m3x2_to_f16x2(static_cast<uint16_t>(p1 >> 16));
+        const uint32_t b2 = e4m3x2_to_f16x2(static_cast<uint16_t>(p3));
+        const uint32_t b3 = e4m3x2_to_f16x2(static_cast<uint16_t>(p3 >> 16));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16<kFp8>(o[nt][2 * w], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          mma16<kFp8>(o[nt][2 * w + 1], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
+        }
+      } else {
+        const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
+        const uint32_t a2 = __byte_perm(x2, x3, 0x5410), a3 = __byte_perm(x2, x3, 0x7632);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16<kFp8>(o[nt][w], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+      }
+    }
+  }
+
+  // The sequence's output rows (whole), or records of this range's part of it.
+  __device__ __forceinline__ void finish(bool whole, int heads, __nv_bfloat16 *out, float4 *ml, float *po) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, kp = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -523,7 +391,6 @@ decode_warp_kernel(const WarpParams p) {
         for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         const int h = nt * 8 + 2 * kp + e;
         if (h >= heads) continue;
-        // lane's dims: fp8 16 g + 0 .. 15; bf16 8 g + 0 .. 7 and 64 + 8 g + 0 .. 7
         float v[16];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -537,21 +404,451 @@ decode_warp_kernel(const WarpParams p) {
           uint32_t w[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) w[i] = float2_to_bf16x2(v[2 * i] * f * fw, v[2 * i + 1] * f * fw);
-          __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(seq) * p.num_q_heads + kvh * p.group + head0 + h) * kHD;
+          __nv_bfloat16 *dst = out + h * kHD;
           *reinterpret_cast<uint4 *>(dst + dim0) = make_uint4(w[0], w[1], w[2], w[3]);
           *reinterpret_cast<uint4 *>(dst + dim1) = make_uint4(w[4], w[5], w[6], w[7]);
         } else {
-          const int64_t rec = (static_cast<int64_t>(range * 2 + (t0 == 0 ? 1 : 0)) * vheads + vh) * p.per_chunk + h;
-          float *dst = p.po + rec * kHD;
+          float *dst = po + h * kHD;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             *reinterpret_cast<float4 *>(dst + dim0 + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             *reinterpret_cast<float4 *>(dst + dim1 + 4 * i) =
                 make_float4(v[8 + 4 * i], v[9 + 4 * i], v[10 + 4 * i], v[11 + 4 * i]);
           }
-          if (g == 0) p.ml[rec] = make_float4(m[nt][e], sum, kFp8 ? mw[nt][e] : m[nt][e], 0.f);
+          if (g == 0) ml[h] = make_float4(m[nt][e], sum, kFp8 ? mw[nt][e] : m[nt][e], 0.f);
         }
       }
+  }
+};
+
+// What a sequence's query sees, as a walk of units of `unit` tokens (boxes; 1 for
+// direct loads): the first `front` units and, `gap` units further on, the others.
+// A unit may hold tokens that are not seen: p counts if p < ctx and (p < sinks or
+// p >= first).
+struct Seen {
+  int ctx, first, units, front, gap;
+};
+
+__device__ __forceinline__ Seen seen_of(const WarpParams &p, int i, int unit, bool report) {
+  int ctx = __ldg(p.context_lens + i);
+  if (ctx < 0 || ctx > p.max_context_len) {
+    if (report) raise_error(p.err, PKV_DEVERR_LENGTH);
+    ctx = min(max(ctx, 0), p.max_context_len);
+  }
+  Seen s{ctx, 0, 0, 0, 0};
+  if (p.window > 0) s.first = max(ctx - p.window, 0);
+  const int shift = unit == 16 ? 4 : unit == 8 ? 3 : 0;
+  const int lo = s.first >> shift;
+  const int front = (min(p.sinks, ctx) + unit - 1) >> shift;
+  if (lo > front) {
+    s.front = front;
+    s.gap = lo - front;
+  }
+  s.units = ((ctx + unit - 1) >> shift) - s.gap;
+  return s;
+}
+
+__device__ __forceinline__ int tiles_of(const Seen &s, int unit) { return (s.units * unit + kTok - 1) / kTok; }
+__device__ __forceinline__ int cost_of(const Seen &s, int unit) { return s.units > 0 ? tiles_of(s, unit) + kSegTiles : 0; }
+
+// Where the CTA's ranges start on the line of all sequences. Walker w of the CTA
+// (w < walkers) takes range first_range(w).
+struct Plan {
+  int range_len, total;
+};
+
+template <int kMaxWalkers, typename F>
+__device__ __forceinline__ Plan plan_ranges(const WarpParams &p, int unit, int walkers, int *part, int *seq_of,
+                                            int *pos_of, F range_of) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int threads = blockDim.x, warps = threads >> 5;
+  const int per = (p.num_seqs + threads - 1) / threads;
+  const int lo = min(tid * per, p.num_seqs), hi = min(lo + per, p.num_seqs);
+  int mine = 0;
+  for (int i = lo; i < hi; ++i) mine += cost_of(seen_of(p, i, unit, blockIdx.x == 0), unit);
+  int inc = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += o;
+  }
+  if (lane == 31) part[warp] = inc;
+  if (tid < walkers) seq_of[tid] = p.num_seqs;
+  __syncthreads();
+  int before = inc - mine, total = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) before += part[w];
+    total += part[w];
+  }
+  const int range_len = max((total + p.ranges - 1) / p.ranges, kMinTiles);
+  int at = before;
+  for (int i = lo; i < hi; ++i) {
+    const int end = at + cost_of(seen_of(p, i, unit, false), unit);
+    for (int w = 0; w < walkers; ++w) {
+      const long long first = static_cast<long long>(range_of(w)) * range_len;
+      if (first >= at && first < end) {
+        seq_of[w] = i;
+        pos_of[w] = at;
+      }
+    }
+    if (blockIdx.x == 0) p.plan[1 + i] = at;
+    at = end;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    p.plan[0] = range_len;
+    p.plan[1 + p.num_seqs] = total;
+  }
+  __syncthreads();
+  return Plan{range_len, total};
+}
+
+// The parts of sequences in one range of the line, one after the other.
+struct Walk {
+  int seq, pos;
+  long long line0;
+  int line1;
+  // the current part: tiles [t0, t1) of all `tiles` of sequence `seq`
+  Seen seen;
+  int t0, t1, tiles;
+
+  __device__ __forceinline__ Walk(const Plan &plan, int range, int seq_at, int pos_at) : seq(seq_at - 1), pos(pos_at) {
+    line0 = static_cast<long long>(range) * plan.range_len;
+    line1 = static_cast<int>(min(line0 + plan.range_len, static_cast<long long>(plan.total)));
+    seq = seq_at - 1;
+  }
+  __device__ __forceinline__ bool next(const WarpParams &p, int unit) {
+    while (++seq < p.num_seqs && pos < line1) {
+      seen = seen_of(p, seq, unit, false);
+      tiles = tiles_of(seen, unit);
+      const int first = pos + kSegTiles;
+      t0 = static_cast<int>(max(line0 - first, 0ll));
+      t1 = min(line1 - first, tiles);
+      pos += cost_of(seen, unit);
+      if (t0 < t1) return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+
+// ----------------------------------------------------------- direct loads --
+
+// Every warp loads its tiles itself, whatever the block size. NT: tiles of 8 query
+// heads a warp computes for its KV head.
+template <bool kFp8, int NT>
+__global__ void __launch_bounds__(kDirectWarps * 32, kFp8 && NT == 1 ? 2 : 1)
+decode_direct_kernel(const WarpParams p) {
+  using H = Heads<kFp8, NT>;
+  __shared__ int s_part[kDirectWarps], s_seq[kDirectWarps], s_pos[kDirectWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, kp = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int vheads = p.num_kv_heads * p.chunks;
+  auto range_of = [&](int w) { return (static_cast<int>(blockIdx.x) * kDirectWarps + w) / vheads; };
+  const Plan plan = plan_ranges<kDirectWarps>(p, 1, kDirectWarps, s_part, s_seq, s_pos, range_of);
+  const int range = range_of(warp), vh = (blockIdx.x * kDirectWarps + warp) % vheads;
+  const int kvh = vh / p.chunks, head0 = vh % p.chunks * p.per_chunk;
+  const int heads = min(p.per_chunk, p.group - head0);       // of this warp
+  constexpr int kRow = kFp8 ? kHD : 2 * kHD;                 // bytes of a head's row
+  const int64_t row_bytes = static_cast<int64_t>(p.num_kv_heads) * kRow;
+  const uint8_t *kbase = p.k_cache + kvh * kRow + 32 * kp;
+  const uint8_t *vbase = p.v_cache + kvh * kRow + 16 * g;
+  H x;
+  Walk walk(plan, range, s_seq[warp], s_pos[warp]);
+  while (walk.next(p, 1)) {
+    const Seen &seen = walk.seen;
+    const int t1 = walk.t1;
+    // the lane's token of a tile: its block and its row in the block
+    const int32_t *bt = p.block_tables + static_cast<int64_t>(walk.seq) * p.max_blocks_per_seq;
+    auto look_up = [&](int t, int &id, int &off) {
+      const int j = t * kTok + (lane & 15);
+      id = -1;
+      off = 0;
+      if (t < t1 && j < seen.units) {
+        const uint32_t at = j + (j >= seen.front ? seen.gap : 0);
+        const uint32_t b = div_of(at, p.bs);
+        off = static_cast<int>(at - b * p.bs.d);
+        id = __ldg(bt + b);
+      }
+    };
+    // cache row of the lane's token (-1: none, or one between the sinks and the
+    // window); its scale, of K in the lower half of the warp and of V in the upper
+    auto resolve = [&](int t, int id, int off, int &row, float &scale) {
+      const int j = t * kTok + (lane & 15);
+      const int at = j + (j >= seen.front ? seen.gap : 0);
+      const bool real = t < t1 && j < seen.units && (at < p.sinks || at >= seen.first);
+      const bool good = real && id >= 0 && id < p.num_blocks;
+      if (real && !good && lane < 16) raise_error(p.err, PKV_DEVERR_BLOCK_ID);
+      row = good ? id * static_cast<int>(p.bs.d) + off : -1;
+      scale = 0.f;
+      if constexpr (kFp8)
+        if (good) scale = __ldg((lane < 16 ? p.k_scales : p.v_scales) + static_cast<int64_t>(id) * p.num_kv_heads + kvh);
+    };
+    uint4 kr[2][H::kKL], vr[4][H::kVL];
+    auto load_k = [&](int row) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = __shfl_sync(0xffffffffu, row, g + 8 * i);
+        const uint8_t *src = kbase + r * row_bytes;
+#pragma unroll
+        for (int d = 0; d < H::kKL; ++d)
+          kr[i][d] = r >= 0 ? ld_once(src + (d >> 1) * 128 + (d & 1) * 16) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto load_v = [&](int row) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = __shfl_sync(0xffffffffu, row, 2 * kp + (i & 1) + 8 * (i >> 1));
+        const uint8_t *src = vbase + r * row_bytes;
+#pragma unroll
+        for (int d = 0; d < H::kVL; ++d) vr[i][d] = r >= 0 ? ld_once(src + d * 128) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    int id, off, row;
+    float scale;
+    look_up(walk.t0, id, off);
+    resolve(walk.t0, id, off, row, scale);
+    look_up(walk.t0 + 1, id, off);
+    load_k(row);
+    load_v(row);
+    const int64_t out_row = static_cast<int64_t>(walk.seq) * p.num_q_heads + kvh * p.group + head0;
+    x.start(p.q + out_row * kHD, heads, p.scale_log2);
+#pragma unroll 1
+    for (int t = walk.t0; t < t1; ++t) {
+      float s[NT][4];
+      x.scores(kr, s);
+      const bool real0 = __shfl_sync(0xffffffffu, row, g) >= 0, real1 = __shfl_sync(0xffffffffu, row, g + 8) >= 0;
+      float ks0 = 1.f, ks1 = 1.f, vs0 = 0.f, vs1 = 0.f;
+      if constexpr (kFp8) {
+        ks0 = __shfl_sync(0xffffffffu, scale, g);
+        ks1 = __shfl_sync(0xffffffffu, scale, g + 8);
+        const float ls = lg2(scale);
+        vs0 = __shfl_sync(0xffffffffu, ls, g + 16);
+        vs1 = __shfl_sync(0xffffffffu, ls, g + 24);
+      }
+      // the next tile's K is on its way while the softmax runs, its V after the PV
+      int next_row = -1;
+      float next_scale = 0.f;
+      if (t + 1 < t1) {
+        resolve(t + 1, id, off, next_row, next_scale);
+        look_up(t + 2, id, off);
+        load_k(next_row);
+      }
+      uint32_t pb[NT][2];
+      x.weights(s, real0, real1, ks0, ks1, vs0, vs1, pb);
+      x.accumulate(vr, pb);
+      if (t + 1 < t1) load_v(next_row);
+      row = next_row;
+      scale = next_scale;
+    }
+    const int64_t rec = (static_cast<int64_t>(range * 2 + (walk.t0 == 0 ? 1 : 0)) * vheads + vh) * p.per_chunk;
+    x.finish(walk.whole(), heads, p.out + out_row * kHD, p.ml + rec, p.po + rec * kHD);
+  }
+}
+
+// --------------------------------------------------- shared-memory rings --
+
+// Bytes of one stage: K and V of a tile, all heads of the CTA.
+__host__ __device__ constexpr int stage_bytes(bool fp8, int heads) { return 2 * kTok * heads * (fp8 ? kHD : 2 * kHD); }
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int *abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
+// A producer warp per ring loads tiles of 16 tokens, all KV heads of the CTA at once,
+// as one or two boxes (units) of K and of V; vheads warps per ring take one KV head's
+// rows each out of shared memory. A box lands as [head][token][128 bytes] (bf16: two
+// such halves of 64 dims), swizzled by the token, which makes every 16-byte load
+// below free of bank conflicts.
+template <bool kFp8, int NT, int kMaxWarps>
+__global__ void __launch_bounds__(kMaxWarps * 32, 1)
+decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const WarpParams p) {
+  using H = Heads<kFp8, NT>;
+  constexpr int kHalves = kFp8 ? 1 : 2;       // 128-byte pieces of a head's row
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_part[kMaxWarps], s_seq[kMaxWarps], s_pos[kMaxWarps];
+  __shared__ uint64_t s_bar[2 * kMaxStages * kMaxWarps / 2];
+  __shared__ int s_abort;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, kp = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int hc = p.heads_per_cta, stages = p.stages;
+  const int ring_warps = hc * p.chunks;                       // consumers of a ring
+  const int consumers = ring_warps * p.rings;
+  const int ring = warp < consumers ? warp / ring_warps : warp - consumers;
+  auto full = [&](int s) { return smem_addr(&s_bar[2 * (ring * stages + s)]); };
+  auto empty = [&](int s) { return smem_addr(&s_bar[2 * (ring * stages + s) + 1]); };
+  volatile int *abort = &s_abort;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.rings * stages; ++i) {
+      mbar_init(smem_addr(&s_bar[2 * i]), 1);
+      mbar_init(smem_addr(&s_bar[2 * i + 1]), ring_warps);
+    }
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  // ring r of CTA b: range (b / groups) * rings + r of head group b % groups
+  const int hg = blockIdx.x % p.head_groups;
+  auto range_of = [&](int r) { return static_cast<int>(blockIdx.x) / p.head_groups * p.rings + r; };
+  const Plan plan = plan_ranges<kMaxWarps>(p, p.unit, p.rings, s_part, s_seq, s_pos, range_of);
+  const int range = range_of(ring);
+  const int bytes = stage_bytes(kFp8, hc);
+  const uint32_t ring_base = base + ring * stages * bytes;
+  // strides of a stage in bytes: V behind K; dims halves; heads; tokens 8 .. 15
+  const uint32_t v_off = bytes / 2, half_dims = kTok * hc * 128;
+  const uint32_t head_step = p.unit * 128;
+  const uint32_t upper = p.unit == 16 ? 1024u : v_off / 2;
+  const uint32_t upper_dims = p.unit == 16 ? half_dims : half_dims / 2;   // dims halves of one box
+  Walk walk(plan, range, s_seq[ring], s_pos[ring]);
+  int it = 0;                                                 // tiles through the ring so far
+  bool ok = true;
+
+  if (warp >= consumers) {
+    // ------------------------------------------------------------- producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    const int per_tile = kTok / p.unit, batch = 32 / per_tile;  // units of a tile, tiles of a batch
+    const int oob_row = p.num_blocks * static_cast<int>(p.bs.d);
+    while (ok && walk.next(p, p.unit)) {
+      const int32_t *bt = p.block_tables + static_cast<int64_t>(walk.seq) * p.max_blocks_per_seq;
+      for (int tb = walk.t0; ok && tb < walk.t1; tb += batch) {
+        // the lane's unit of the batch: its first cache row; behind the last one, and
+        // for a bad block id, rows behind the pool, which read as zero
+        const int u = tb * per_tile + lane;
+        int row = oob_row;
+        if (u < walk.seen.units && u < walk.t1 * per_tile) {
+          const uint32_t at = static_cast<uint32_t>(u + (u >= walk.seen.front ? walk.seen.gap : 0)) * p.unit;
+          const uint32_t b = div_of(at, p.bs);
+          const int id = __ldg(bt + b);
+          if (id >= 0 && id < p.num_blocks) row = id * static_cast<int>(p.bs.d) + static_cast<int>(at - b * p.bs.d);
+          else raise_error(p.err, PKV_DEVERR_BLOCK_ID);
+        }
+        const int n = min(batch, walk.t1 - tb);
+        for (int j = 0; j < n; ++j, ++it) {
+          const int s = it % stages, round = it / stages;
+          int good = 1;
+          if (lane == 0) {
+            if (round > 0 && !mbar_wait(empty(s), (round - 1) & 1, abort)) {
+              good = 0;
+              *abort = 1;
+              raise_error(p.err, PKV_DEVERR_TIMEOUT);
+            } else {
+              mbar_arrive_expect_tx(full(s), bytes);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, good, 0);
+          if (!ok) break;
+          // lane: which of K and V, of the dims halves and of the tile's units it loads
+          const int unit = lane % per_tile, half = lane / per_tile % kHalves, is_v = lane / (per_tile * kHalves);
+          const int r = __shfl_sync(0xffffffffu, row, j * per_tile + unit);
+          if (is_v < 2) {
+            const uint32_t dst = ring_base + s * bytes + is_v * v_off + unit * (v_off / per_tile) + half * upper_dims;
+            tma_load_3d(dst, is_v ? &tm_v : &tm_k, half * 64, r, hg * hc, full(s));
+          }
+        }
+      }
+    }
+    // every copy lands before the CTA may exit
+    if (lane == 0)
+      for (int j = max(0, it - stages); j < it; ++j) mbar_wait(full(j % stages), (j / stages) & 1, nullptr);
+  } else {
+    // ------------------------------------------------------------ consumers
+    const int in_ring = warp % ring_warps;
+    const int kvh = hg * hc + in_ring / p.chunks, head0 = in_ring % p.chunks * p.per_chunk;
+    const bool real_head = kvh < p.num_kv_heads;              // a group may hang over the last head
+    const int heads = real_head ? min(p.per_chunk, p.group - head0) : 0;
+    const int vheads = p.num_kv_heads * p.chunks, vh = kvh * p.chunks + in_ring % p.chunks;
+    const uint32_t head_base = ring_base + in_ring / p.chunks * head_step;
+    // 16-byte pieces of the lane: K row g: pieces 2 kp, 2 kp + 1; V rows 2 kp, 2 kp + 1: piece g
+    const uint32_t k0 = g * 128 + (((2 * kp) ^ g) << 4), k1 = g * 128 + (((2 * kp + 1) ^ g) << 4);
+    const uint32_t v0 = 2 * kp * 128 + ((g ^ (2 * kp)) << 4), v1 = (2 * kp + 1) * 128 + ((g ^ (2 * kp + 1)) << 4);
+    H x;
+    while (ok && walk.next(p, p.unit)) {
+      const Seen seen = walk.seen;
+      const int64_t out_row = static_cast<int64_t>(walk.seq) * p.num_q_heads + kvh * p.group + head0;
+      x.start(p.q + (real_head ? out_row * kHD : 0), heads, p.scale_log2);
+      const int32_t *bt = p.block_tables + static_cast<int64_t>(walk.seq) * p.max_blocks_per_seq;
+      // fp8: scales of 8 tiles at a time, lane = (8 tokens, K or V): ids a batch ahead
+      float sc = 0.f, next_sc = 0.f;
+      auto scale_of = [&](int tb) {
+        const int j = tb * kTok + (lane >> 1) * 8;            // first of the 8 tokens on the walk
+        const int u = j / p.unit;
+        float v = 0.f;
+        if (real_head && u < seen.units) {
+          const uint32_t at = static_cast<uint32_t>(u + (u >= seen.front ? seen.gap : 0)) * p.unit;
+          const int id = __ldg(bt + div_of(at, p.bs));
+          if (id >= 0 && id < p.num_blocks)
+            v = __ldg((lane & 1 ? p.v_scales : p.k_scales) + static_cast<int64_t>(id) * p.num_kv_heads + kvh);
+        }
+        return v;
+      };
+      if constexpr (kFp8) {
+        sc = scale_of(walk.t0);
+        if (walk.t0 + 8 < walk.t1) next_sc = scale_of(walk.t0 + 8);
+        if (lane & 1) sc = lg2(sc);
+      }
+#pragma unroll 1
+      for (int t = walk.t0; t < walk.t1; ++t, ++it) {
+        const int s = it % stages;
+        if (!warp_wait(full(s), (it / stages) & 1, abort)) {
+          ok = false;
+          *abort = 1;
+          raise_error(p.err, PKV_DEVERR_TIMEOUT);
+          break;
+        }
+        const uint32_t kt = head_base + s * bytes, vt = kt + v_off;
+        uint4 k[2][H::kKL], v[4][H::kVL];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int d = 0; d < H::kKL; ++d)
+            k[i][d] = lds128(kt + i * upper + (d >> 1) * upper_dims + (d & 1 ? k1 : k0));
+        float sv[NT][4];
+        x.scores(k, sv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int d = 0; d < H::kVL; ++d) v[i][d] = lds128(vt + (i >> 1) * upper + d * upper_dims + (i & 1 ? v1 : v0));
+        // first positions of the tile's two eights
+        const int j0 = t * kTok, j1 = j0 + 8;
+        const int front = seen.front * p.unit, gap = seen.gap * p.unit;
+        const int a0 = j0 + (j0 >= front ? gap : 0), a1 = j1 + (j1 >= front ? gap : 0);
+        auto counts = [&](int at) { return at < seen.ctx && (at < p.sinks || at >= seen.first); };
+        const bool real0 = counts(a0 + g), real1 = counts(a1 + g);
+        float ks0 = 1.f, ks1 = 1.f, vs0 = 0.f, vs1 = 0.f;
+        if constexpr (kFp8) {
+          const int b = (t - walk.t0) & 7;
+          ks0 = __shfl_sync(0xffffffffu, sc, 4 * b);
+          vs0 = __shfl_sync(0xffffffffu, sc, 4 * b + 1);
+          ks1 = __shfl_sync(0xffffffffu, sc, 4 * b + 2);
+          vs1 = __shfl_sync(0xffffffffu, sc, 4 * b + 3);
+          if (b == 7) {
+            sc = lane & 1 ? lg2(next_sc) : next_sc;
+            if (t + 9 < walk.t1) next_sc = scale_of(t + 9);
+          }
+        }
+        uint32_t pb[NT][2];
+        x.weights(sv, real0, real1, ks0, ks1, vs0, vs1, pb);
+        // what a row that does not count holds is not known: 0 times NaN is NaN
+        if (!__all_sync(0xffffffffu, real0 && real1)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!counts((i >> 1 ? a1 : a0) + 2 * kp + (i & 1)))
+#pragma unroll
+              for (int d = 0; d < H::kVL; ++d) v[i][d] = make_uint4(0, 0, 0, 0);
+        }
+        x.accumulate(v, pb);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(s));
+      }
+      if (!ok) break;
+      const int64_t rec = (static_cast<int64_t>(range * 2 + (walk.t0 == 0 ? 1 : 0)) * vheads + vh) * p.per_chunk;
+      x.finish(walk.whole(), heads, p.out + out_row * kHD, p.ml + rec, p.po + rec * kHD);
+    }
   }
 }
 
@@ -560,10 +857,10 @@ decode_warp_kernel(const WarpParams p) {
 // One warp per (sequence, query head) merges the records of a cut sequence:
 // out = sum O_i 2^(M_i - M*) / sum l_i 2^(m_i - m*) * 2^(M* - m* - lift); a
 // sequence that sees nothing gets zeros.
-__global__ void __launch_bounds__(kThreads) decode_warp_combine_kernel(const WarpParams p, float lift) {
+__global__ void __launch_bounds__(kCombineWarps * 32) decode_warp_combine_kernel(const WarpParams p, float lift) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const long long w = static_cast<long long>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
   const int seq = static_cast<int>(w / p.num_q_heads), qh = static_cast<int>(w % p.num_q_heads);
   if (seq >= p.num_seqs) return;
   const int range_len = __ldg(p.plan), a = __ldg(p.plan + 1 + seq), b = __ldg(p.plan + 2 + seq);
@@ -626,11 +923,13 @@ __global__ void __launch_bounds__(kThreads) decode_warp_combine_kernel(const War
 
 struct Shape {
   int chunks, per_chunk, ranges, grid;
-  bool wide;   // two tiles of 8 query heads a warp
+  bool wide;           // two tiles of 8 query heads a warp
+  bool ring;
+  int unit, heads_per_cta, head_groups, rings, stages, warps;
 };
 
-// Ranges: as many as resident warps, over the (KV head, chunk) pairs.
-bool shape_of(int num_q_heads, int num_kv_heads, bool fp8, Shape *s) {
+// Ranges: as many as resident walkers of one (KV head, chunk) pair.
+bool shape_of(int num_q_heads, int num_kv_heads, int block_size, bool fp8, Shape *s) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const int sms = sm_count(dev);
@@ -641,10 +940,30 @@ bool shape_of(int num_q_heads, int num_kv_heads, bool fp8, Shape *s) {
   s->chunks = (group + most - 1) / most;
   s->per_chunk = (group + s->chunks - 1) / s->chunks;
   const int vheads = num_kv_heads * s->chunks;
+  const int most_warps = s->wide ? kWideWarps : kNarrowWarps;
+  s->ring = block_size % 8 == 0 && s->chunks < most_warps;
+  if (s->ring) {
+    s->unit = block_size % 16 == 0 ? 16 : 8;
+    s->heads_per_cta = (most_warps - 1) / s->chunks;           // a warp per (head, chunk) and a producer
+    if (s->heads_per_cta > 8) s->heads_per_cta = 8;
+    if (s->heads_per_cta > num_kv_heads) s->heads_per_cta = num_kv_heads;
+    s->head_groups = (num_kv_heads + s->heads_per_cta - 1) / s->heads_per_cta;
+    const int bytes = stage_bytes(fp8, s->heads_per_cta), ring_warps = s->heads_per_cta * s->chunks;
+    s->rings = most_warps / (ring_warps + 1);
+    while (s->rings > 1 && kRingBytes / (s->rings * bytes) < 3) --s->rings;
+    s->stages = kRingBytes / (s->rings * bytes);
+    if (s->stages > kMaxStages) s->stages = kMaxStages;
+    s->warps = s->rings * (ring_warps + 1);
+    s->grid = sms / s->head_groups;                            // per head group
+    if (s->grid < 1) s->grid = 1;
+    s->ranges = s->grid * s->rings;
+    s->grid *= s->head_groups;
+    return true;
+  }
   const int ctas = sms * (fp8 && !s->wide ? 2 : 1);
-  s->ranges = ctas * kWarps / vheads;
+  s->ranges = ctas * kDirectWarps / vheads;
   if (s->ranges < 1) s->ranges = 1;
-  s->grid = (s->ranges * vheads + kWarps - 1) / kWarps;
+  s->grid = (s->ranges * vheads + kDirectWarps - 1) / kDirectWarps;
   return true;
 }
 
@@ -658,16 +977,58 @@ size_t bytes_of(int num_seqs, const Shape &s, int num_kv_heads) {
   return plan_bytes(num_seqs) + records_of(s, num_kv_heads) * (sizeof(float4) + kHD * sizeof(float));
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// Boxes of 128 bytes of `unit` tokens of `heads` KV heads.
+bool cache_map(CUtensorMap *map, const void *base, uint64_t rows, uint64_t hkv, bool fp8, int unit, int heads) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = fp8 ? kHD : 2 * kHD;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHD), rows, hkv};
+  cuuint64_t strides[2] = {hkv * row, row};
+  cuuint32_t box[3] = {fp8 ? 128u : 64u, static_cast<cuuint32_t>(unit), static_cast<cuuint32_t>(heads)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+using RingKernel = void (*)(CUtensorMap, CUtensorMap, WarpParams);
+
+// Largest dynamic shared memory of kernel `which`, set once a device.
+cudaError_t allow_smem(const void *kern, int which, int bytes) {
+  static std::atomic<uint64_t> done[4];
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev <= 63 && (done[which].load() & bit)) return cudaSuccess;
+  if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) return e;
+  done[which].fetch_or(bit);
+  return cudaSuccess;
+}
+
 }  // namespace
 
 size_t decode_warp_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads) {
   size_t need = 0;
-  for (bool fp8 : {false, true}) {
-    Shape s;
-    if (!shape_of(num_q_heads, num_kv_heads, fp8, &s)) return 0;
-    const size_t b = bytes_of(num_seqs, s, num_kv_heads);
-    if (b > need) need = b;
-  }
+  for (bool fp8 : {false, true})
+    for (int block_size : {1, 8}) {        // every path
+      Shape s;
+      if (!shape_of(num_q_heads, num_kv_heads, block_size, fp8, &s)) return 0;
+      const size_t b = bytes_of(num_seqs, s, num_kv_heads);
+      if (b > need) need = b;
+    }
   return need;
 }
 
@@ -679,7 +1040,7 @@ bool decode_warp_fits(int num_seqs, int max_context_len, int num_q_heads) {
 cudaError_t launch_decode_warp(const DecodeWarpArgs &a, cudaStream_t stream) {
   const bool fp8 = a.k_scales != nullptr;
   Shape s;
-  if (!shape_of(a.num_q_heads, a.num_kv_heads, fp8, &s)) return cudaErrorInvalidValue;
+  if (!shape_of(a.num_q_heads, a.num_kv_heads, a.block_size, fp8, &s)) return cudaErrorInvalidValue;
   WarpParams p;
   p.out = static_cast<__nv_bfloat16 *>(a.out);
   p.q = static_cast<const __nv_bfloat16 *>(a.q);
@@ -716,13 +1077,32 @@ cudaError_t launch_decode_warp(const DecodeWarpArgs &a, cudaStream_t stream) {
   p.ml = reinterpret_cast<float4 *>(static_cast<uint8_t *>(a.workspace) + plan_bytes(a.num_seqs));
   p.po = reinterpret_cast<float *>(p.ml + records_of(s, a.num_kv_heads));
   p.err = a.err;
-  auto kern = fp8 ? (s.wide ? decode_warp_kernel<true, 2> : decode_warp_kernel<true, 1>)
-                  : (s.wide ? decode_warp_kernel<false, 2> : decode_warp_kernel<false, 1>);
-  kern<<<s.grid, kThreads, 0, stream>>>(p);
+  if (s.ring) {
+    p.unit = s.unit;
+    p.heads_per_cta = s.heads_per_cta;
+    p.head_groups = s.head_groups;
+    p.rings = s.rings;
+    p.stages = s.stages;
+    const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.block_size;
+    CUtensorMap tk, tv;
+    if (!cache_map(&tk, a.k_cache, rows, a.num_kv_heads, fp8, s.unit, s.heads_per_cta) ||
+        !cache_map(&tv, a.v_cache, rows, a.num_kv_heads, fp8, s.unit, s.heads_per_cta))
+      return cudaErrorInvalidValue;
+    RingKernel kern = fp8 ? (s.wide ? decode_ring_kernel<true, 2, kWideWarps> : decode_ring_kernel<true, 1, kNarrowWarps>)
+                          : (s.wide ? decode_ring_kernel<false, 2, kWideWarps> : decode_ring_kernel<false, 1, kNarrowWarps>);
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), (fp8 ? 1 : 0) + (s.wide ? 2 : 0), kRingBytes + 1024))
+      return e;
+    const int smem = s.rings * s.stages * stage_bytes(fp8, s.heads_per_cta) + 1024;
+    kern<<<s.grid, s.warps * 32, smem, stream>>>(tk, tv, p);
+  } else {
+    auto kern = fp8 ? (s.wide ? decode_direct_kernel<true, 2> : decode_direct_kernel<true, 1>)
+                    : (s.wide ? decode_direct_kernel<false, 2> : decode_direct_kernel<false, 1>);
+    kern<<<s.grid, kDirectWarps * 32, 0, stream>>>(p);
+  }
   if (cudaError_t e = cudaGetLastError()) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.num_seqs) * a.num_q_heads + kWarps - 1) / kWarps));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.num_seqs) * a.num_q_heads + kCombineWarps - 1) / kCombineWarps));
+  cfg.blockDim = dim3(kCombineWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
