@@ -956,7 +956,7 @@ size_t pkv_decode_window_workspace_size(int32_t num_seqs, int32_t num_q_heads,
   if (num_seqs < 0 || num_q_heads < 1 || num_kv_heads < 1 || head_dim != 128 ||
       num_q_heads % num_kv_heads != 0)
     return 0;
-  return pkv::decode_warp_workspace_bytes(num_seqs, num_q_heads, num_kv_heads);
+  return pkv::decode_warp_workspace_bytes(num_q_heads, num_kv_heads);
 }
 
 // Shared body of pkv_paged_decode_fp8_block (with scales) and pkv_paged_decode_window.
@@ -974,9 +974,10 @@ static pkv_status decode_warp_call(void *out, const void *q, const void *k_cache
       !(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f))
     return PKV_ERR_ARG;
   if (head_dim != 128 || num_q_heads % num_kv_heads != 0) return PKV_ERR_SHAPE;
-  if (int64_t(max_context_len) > int64_t(max_blocks_per_seq) * block_size ||
-      int64_t(num_blocks) * block_size > 0x7fffffffll ||   // cache rows are numbered in int32
-      !pkv::decode_warp_fits(num_seqs, max_context_len, num_q_heads))
+  if (int64_t(max_context_len) > int64_t(max_blocks_per_seq) * block_size || num_q_heads > 65535 ||
+      // cache rows, a box past the last one included, are numbered in int32
+      int64_t(num_blocks) * block_size > 0x7fffffffll - 512 ||
+      !pkv::decode_warp_fits(num_seqs, max_context_len))
     return PKV_ERR_ARG;
   if (num_seqs == 0) return PKV_OK;
   if (!out || !q || !k_cache || !v_cache || !context_lens ||
@@ -985,7 +986,7 @@ static pkv_status decode_warp_call(void *out, const void *q, const void *k_cache
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
       overlap(out, q, int64_t(num_seqs) * num_q_heads * head_dim * 2))
     return PKV_ERR_ARG;
-  const size_t need = pkv::decode_warp_workspace_bytes(num_seqs, num_q_heads, num_kv_heads);
+  const size_t need = pkv::decode_warp_workspace_bytes(num_q_heads, num_kv_heads);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
       workspace_bytes < need || workspace_bytes < 256)
     return PKV_ERR_WORKSPACE;

@@ -101,7 +101,12 @@ struct WarpParams {
   int head_groups;     // boxes over all KV heads
   int rings;           // of a CTA
   int stages;          // of a ring
-  int *plan;           // [0] tiles of a range, [1 ..] starts of the sequences on the line
+  // What the second launch merges, an entry (sequence, its first and its last range;
+  // sequence -1 or one range: nothing) for each of whichever are fewer: the sequences,
+  // or the ranges, which have the sequence that they begin inside of if they are the
+  // second of its ranges.
+  int4 *cuts;
+  bool cuts_by_seq;
   float4 *ml;          // records: (m, l, M)
   float *po;           // and O
   uint32_t *err;
@@ -491,30 +496,52 @@ __device__ __forceinline__ Plan plan_ranges(const WarpParams &p, int unit, int w
         pos_of[w] = at;
       }
     }
-    if (blockIdx.x == 0) p.plan[1 + i] = at;
     at = end;
-  }
-  if (blockIdx.x == 0 && tid == 0) {
-    p.plan[0] = range_len;
-    p.plan[1 + p.num_seqs] = total;
   }
   __syncthreads();
   return Plan{range_len, total};
+}
+
+// Zeros for the sequences that see nothing, spread over the CTAs; `threads` threads of
+// this one call it.
+__device__ __forceinline__ void zero_rows(const WarpParams &p, int threads) {
+  for (int i = blockIdx.x; i < p.num_seqs; i += gridDim.x) {
+    if (__ldg(p.context_lens + i) > 0 && p.max_context_len > 0) continue;
+    if (p.cuts_by_seq && threadIdx.x == 0) p.cuts[i] = make_int4(-1, 0, 0, 0);
+    uint4 *dst = reinterpret_cast<uint4 *>(p.out + static_cast<int64_t>(i) * p.num_q_heads * kHD);
+    for (int x = threadIdx.x; x < p.num_q_heads * (kHD / 8); x += threads) dst[x] = make_uint4(0, 0, 0, 0);
+  }
 }
 
 // The parts of sequences in one range of the line, one after the other.
 struct Walk {
   int seq, pos;
   long long line0;
-  int line1;
+  int line1, range_len;
   // the current part: tiles [t0, t1) of all `tiles` of sequence `seq`
   Seen seen;
   int t0, t1, tiles;
 
-  __device__ __forceinline__ Walk(const Plan &plan, int range, int seq_at, int pos_at) : seq(seq_at - 1), pos(pos_at) {
+  __device__ __forceinline__ Walk(const Plan &plan, int range, int seq_at, int pos_at)
+      : seq(seq_at - 1), pos(pos_at), range_len(plan.range_len) {
     line0 = static_cast<long long>(range) * plan.range_len;
     line1 = static_cast<int>(min(line0 + plan.range_len, static_cast<long long>(plan.total)));
-    seq = seq_at - 1;
+  }
+  // The entry of WarpParams::cuts that this range stands for; before the first next().
+  __device__ __forceinline__ void begin(const WarpParams &p, int range, int unit) const {
+    if (p.cuts_by_seq) return;
+    int4 cut = make_int4(-1, 0, 0, 0);
+    if (seq + 1 < p.num_seqs && pos + kSegTiles < line0) {
+      const int r0 = (pos + kSegTiles) / range_len;
+      const int r1 = (pos + cost_of(seen_of(p, seq + 1, unit, false), unit) - 1) / range_len;
+      if (range == r0 + 1) cut = make_int4(seq + 1, r0, r1, 0);
+    }
+    p.cuts[range] = cut;
+  }
+  // The entry of the sequence that begins with the current part.
+  __device__ __forceinline__ void entry(const WarpParams &p, int range) const {
+    if (p.cuts_by_seq && t0 == 0)
+      p.cuts[seq] = make_int4(seq, range, static_cast<int>((pos - 1) / range_len), 0);
   }
   __device__ __forceinline__ bool next(const WarpParams &p, int unit) {
     while (++seq < p.num_seqs && pos < line1) {
@@ -542,6 +569,7 @@ decode_direct_kernel(const WarpParams p) {
   __shared__ int s_part[kDirectWarps], s_seq[kDirectWarps], s_pos[kDirectWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, kp = lane & 3;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int vheads = p.num_kv_heads * p.chunks;
   auto range_of = [&](int w) { return (static_cast<int>(blockIdx.x) * kDirectWarps + w) / vheads; };
@@ -555,7 +583,11 @@ decode_direct_kernel(const WarpParams p) {
   const uint8_t *vbase = p.v_cache + kvh * kRow + 16 * g;
   H x;
   Walk walk(plan, range, s_seq[warp], s_pos[warp]);
+  const bool tells = vh == 0 && lane == 0 && range < p.ranges;
+  if (tells) walk.begin(p, range, 1);
+  zero_rows(p, blockDim.x);
   while (walk.next(p, 1)) {
+    if (tells) walk.entry(p, range);
     const Seen &seen = walk.seen;
     const int t1 = walk.t1;
     // the lane's token of a tile: its block and its row in the block
@@ -673,7 +705,6 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, kp = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int hc = p.heads_per_cta, stages = p.stages;
   const int ring_warps = hc * p.chunks;                       // consumers of a ring
   const int consumers = ring_warps * p.rings;
@@ -688,7 +719,12 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     }
     s_abort = 0;
     fence_barrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
+  // launched while the kernel before this one drains: nothing of its is read before here
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // ring r of CTA b: range (b / groups) * rings + r of head group b % groups
   const int hg = blockIdx.x % p.head_groups;
   auto range_of = [&](int r) { return static_cast<int>(blockIdx.x) / p.head_groups * p.rings + r; };
@@ -707,13 +743,12 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 
   if (warp >= consumers) {
     // ------------------------------------------------------------- producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
+    const bool tells = lane == 0 && hg == 0;
+    if (tells) walk.begin(p, range, p.unit);
     const int per_tile = kTok / p.unit, batch = 32 / per_tile;  // units of a tile, tiles of a batch
     const int oob_row = p.num_blocks * static_cast<int>(p.bs.d);
     while (ok && walk.next(p, p.unit)) {
+      if (tells) walk.entry(p, range);
       const int32_t *bt = p.block_tables + static_cast<int64_t>(walk.seq) * p.max_blocks_per_seq;
       for (int tb = walk.t0; ok && tb < walk.t1; tb += batch) {
         // the lane's unit of the batch: its first cache row; behind the last one, and
@@ -757,6 +792,7 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
       for (int j = max(0, it - stages); j < it; ++j) mbar_wait(full(j % stages), (j / stages) & 1, nullptr);
   } else {
     // ------------------------------------------------------------ consumers
+    zero_rows(p, consumers * 32);
     const int in_ring = warp % ring_warps;
     const int kvh = hg * hc + in_ring / p.chunks, head0 = in_ring % p.chunks * p.per_chunk;
     const bool real_head = kvh < p.num_kv_heads;              // a group may hang over the last head
@@ -854,30 +890,27 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 
 // --------------------------------------------------------------- combine --
 
-// One warp per (sequence, query head) merges the records of a cut sequence:
-// out = sum O_i 2^(M_i - M*) / sum l_i 2^(m_i - m*) * 2^(M* - m* - lift); a
-// sequence that sees nothing gets zeros.
-__global__ void __launch_bounds__(kCombineWarps * 32) decode_warp_combine_kernel(const WarpParams p, float lift) {
+// `share` warps per (entry of cuts, query head) merge the records of a cut sequence:
+// out = sum O_i 2^(M_i - M*) / sum l_i 2^(m_i - m*) * 2^(M* - m* - lift)
+__global__ void __launch_bounds__(kCombineWarps * 32) decode_warp_combine_kernel(const WarpParams p, int share, float lift) {
+  __shared__ float4 s_acc[kCombineWarps][32];
+  __shared__ float s_sum[kCombineWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
-  const int seq = static_cast<int>(w / p.num_q_heads), qh = static_cast<int>(w % p.num_q_heads);
-  if (seq >= p.num_seqs) return;
-  const int range_len = __ldg(p.plan), a = __ldg(p.plan + 1 + seq), b = __ldg(p.plan + 2 + seq);
-  uint2 *dst = reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(seq) * p.num_q_heads + qh) * kHD) + lane;
-  if (a == b) {
-    *dst = make_uint2(0, 0);
-    return;
-  }
-  const int r0 = (a + kSegTiles) / range_len, r1 = (b - 1) / range_len;
-  if (r0 == r1) return;
+  const int4 cut = p.cuts[blockIdx.x];
+  const int seq = cut.x, r0 = cut.y, r1 = cut.z;
+  if (seq < 0 || r0 == r1) return;   // the whole CTA
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = warp % share;
+  const int qh = blockIdx.y * (kCombineWarps / share) + warp / share;
+  const bool row = qh < p.num_q_heads;
   const int in_group = qh % p.group;
   const int vheads = p.num_kv_heads * p.chunks;
   const int vh = qh / p.group * p.chunks + in_group / p.per_chunk, h = in_group % p.per_chunk;
   auto record = [&](int r) { return (static_cast<int64_t>(2 * r + (r == r0 ? 1 : 0)) * vheads + vh) * p.per_chunk + h; };
-  float top = -INFINITY, topw = -INFINITY;
-  for (int r = r0 + lane; r <= r1; r += 32) {
-    const float4 v = p.ml[record(r)];
+  const int n = row ? r1 - r0 + 1 : 0;
+  float top = -INFINITY, topw = -INFINITY, sum = 0.f;
+  for (int i = lane; i < n; i += 32) {
+    const float4 v = p.ml[record(r0 + i)];
     top = fmaxf(top, v.x);
     topw = fmaxf(topw, v.z);
   }
@@ -887,26 +920,28 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode_warp_combine_kernel
     topw = fmaxf(topw, __shfl_xor_sync(0xffffffffu, topw, x));
   }
   const float ref = top == -INFINITY ? 0.f : top, refw = topw == -INFINITY ? 0.f : topw;
-  float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int base = r0; base <= r1; base += 32) {
+  // records part, part + share, ...: 32 at a time, a lane each for their factors
+  for (int base = part; base < n; base += 32 * share) {
     float f = 0.f;
-    if (base + lane <= r1) {
-      const float4 v = p.ml[record(base + lane)];
+    const int own = base + lane * share;
+    if (own < n) {
+      const float4 v = p.ml[record(r0 + own)];
       sum += v.y * ex2(v.x - ref);
       f = ex2(v.z - refw);
     }
-    const int n = min(32, r1 - base + 1);
-    for (int k = 0; k < n; k += 8) {
+    const int left = min(32, (n - base + share - 1) / share);
+    for (int k = 0; k < left; k += 8) {
       float4 x[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        x[u] = k + u < n ? *(reinterpret_cast<const float4 *>(p.po + record(base + k + u) * kHD) + lane)
-                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[u] = k + u < left
+                   ? *(reinterpret_cast<const float4 *>(p.po + record(r0 + base + (k + u) * share) * kHD) + lane)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const float y = __shfl_sync(0xffffffffu, f, (k + u) & 31);
-        if (k + u < n) {
+        const float y = __shfl_sync(0xffffffffu, f, k + u);
+        if (k + u < left) {
           acc.x += x[u].x * y;
           acc.y += x[u].y * y;
           acc.z += x[u].z * y;
@@ -917,8 +952,21 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode_warp_combine_kernel
   }
 #pragma unroll
   for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  if (share > 1) {
+    s_acc[warp][lane] = acc;
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (part > 0) return;
+    for (int w = 1; w < share; ++w) {
+      const float4 x = s_acc[warp + w][lane];
+      acc = make_float4(acc.x + x.x, acc.y + x.y, acc.z + x.z, acc.w + x.w);
+      sum += s_sum[warp + w];
+    }
+  }
+  if (!row) return;
   const float f = 1.f / sum, fw = ex2(refw - ref - lift);
-  *dst = make_uint2(float2_to_bf16x2(acc.x * f * fw, acc.y * f * fw), float2_to_bf16x2(acc.z * f * fw, acc.w * f * fw));
+  reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(seq) * p.num_q_heads + qh) * kHD)[lane] =
+      make_uint2(float2_to_bf16x2(acc.x * f * fw, acc.y * f * fw), float2_to_bf16x2(acc.z * f * fw, acc.w * f * fw));
 }
 
 struct Shape {
@@ -967,14 +1015,14 @@ bool shape_of(int num_q_heads, int num_kv_heads, int block_size, bool fp8, Shape
   return true;
 }
 
-size_t plan_bytes(int num_seqs) { return (sizeof(int) * (static_cast<size_t>(num_seqs) + 2) + 255) & ~size_t(255); }
+size_t cuts_bytes(const Shape &s) { return (sizeof(int4) * s.ranges + 255) & ~size_t(255); }
 
 size_t records_of(const Shape &s, int num_kv_heads) {
   return static_cast<size_t>(s.ranges) * 2 * num_kv_heads * s.chunks * s.per_chunk;
 }
 
-size_t bytes_of(int num_seqs, const Shape &s, int num_kv_heads) {
-  return plan_bytes(num_seqs) + records_of(s, num_kv_heads) * (sizeof(float4) + kHD * sizeof(float));
+size_t bytes_of(const Shape &s, int num_kv_heads) {
+  return cuts_bytes(s) + records_of(s, num_kv_heads) * (sizeof(float4) + kHD * sizeof(float));
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -1018,23 +1066,40 @@ cudaError_t allow_smem(const void *kern, int which, int bytes) {
   return cudaSuccess;
 }
 
+// A launch that may begin while the kernel before it on the stream ends; the kernels
+// here wait for that one before they read anything.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(cudaStream_t stream, dim3 grid, int threads, int smem, void (*kern)(P...), const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace
 
-size_t decode_warp_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads) {
+size_t decode_warp_workspace_bytes(int num_q_heads, int num_kv_heads) {
   size_t need = 0;
   for (bool fp8 : {false, true})
     for (int block_size : {1, 8}) {        // every path
       Shape s;
       if (!shape_of(num_q_heads, num_kv_heads, block_size, fp8, &s)) return 0;
-      const size_t b = bytes_of(num_seqs, s, num_kv_heads);
+      const size_t b = bytes_of(s, num_kv_heads);
       if (b > need) need = b;
     }
   return need;
 }
 
-bool decode_warp_fits(int num_seqs, int max_context_len, int num_q_heads) {
+bool decode_warp_fits(int num_seqs, int max_context_len) {
   const int64_t tiles = (static_cast<int64_t>(max_context_len) + kTok - 1) / kTok + kSegTiles;
-  return num_seqs * tiles < (int64_t(1) << 31) && static_cast<int64_t>(num_seqs) * num_q_heads < (int64_t(1) << 31);
+  return num_seqs * tiles < (int64_t(1) << 31);
 }
 
 cudaError_t launch_decode_warp(const DecodeWarpArgs &a, cudaStream_t stream) {
@@ -1073,8 +1138,9 @@ cudaError_t launch_decode_warp(const DecodeWarpArgs &a, cudaStream_t stream) {
   p.sinks = a.sinks < a.max_context_len ? a.sinks : a.max_context_len;
   p.scale_log2 = a.scale * kLog2e;
   p.ranges = s.ranges;
-  p.plan = static_cast<int *>(a.workspace);
-  p.ml = reinterpret_cast<float4 *>(static_cast<uint8_t *>(a.workspace) + plan_bytes(a.num_seqs));
+  p.cuts = static_cast<int4 *>(a.workspace);
+  p.cuts_by_seq = a.num_seqs <= s.ranges;
+  p.ml = reinterpret_cast<float4 *>(static_cast<uint8_t *>(a.workspace) + cuts_bytes(s));
   p.po = reinterpret_cast<float *>(p.ml + records_of(s, a.num_kv_heads));
   p.err = a.err;
   if (s.ring) {
@@ -1093,23 +1159,18 @@ cudaError_t launch_decode_warp(const DecodeWarpArgs &a, cudaStream_t stream) {
     if (cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), (fp8 ? 1 : 0) + (s.wide ? 2 : 0), kRingBytes + 1024))
       return e;
     const int smem = s.rings * s.stages * stage_bytes(fp8, s.heads_per_cta) + 1024;
-    kern<<<s.grid, s.warps * 32, smem, stream>>>(tk, tv, p);
+    if (cudaError_t e = launch_dependent(stream, dim3(s.grid), s.warps * 32, smem, kern, tk, tv, p)) return e;
   } else {
     auto kern = fp8 ? (s.wide ? decode_direct_kernel<true, 2> : decode_direct_kernel<true, 1>)
                     : (s.wide ? decode_direct_kernel<false, 2> : decode_direct_kernel<false, 1>);
-    kern<<<s.grid, kDirectWarps * 32, 0, stream>>>(p);
+    if (cudaError_t e = launch_dependent(stream, dim3(s.grid), kDirectWarps * 32, 0, kern, p)) return e;
   }
-  if (cudaError_t e = cudaGetLastError()) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.num_seqs) * a.num_q_heads + kCombineWarps - 1) / kCombineWarps));
-  cfg.blockDim = dim3(kCombineWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_warp_combine_kernel, p, fp8 ? kLift : 0.f);
+  // warps a merge: one for every 8 records that a sequence has on average
+  int share = 1;
+  while (share < kCombineWarps && share * 8 * static_cast<int64_t>(a.num_seqs) < s.ranges) share *= 2;
+  const int rows = kCombineWarps / share;
+  return launch_dependent(stream, dim3(p.cuts_by_seq ? a.num_seqs : s.ranges, (a.num_q_heads + rows - 1) / rows), kCombineWarps * 32, 0,
+                          decode_warp_combine_kernel, p, share, fp8 ? kLift : 0.f);
 }
 
 }  // namespace pkv

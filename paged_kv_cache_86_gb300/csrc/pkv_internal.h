@@ -350,9 +350,9 @@ struct DecodeWarpArgs {
   uint32_t *err;
 };
 // 0 without a device.
-size_t decode_warp_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads);
-// Tiles of all sequences and output rows are numbered in 32 bits: whether the bounds allow it.
-bool decode_warp_fits(int num_seqs, int max_context_len, int num_q_heads);
+size_t decode_warp_workspace_bytes(int num_q_heads, int num_kv_heads);
+// Tiles of all sequences are numbered in 32 bits: whether the bounds allow it.
+bool decode_warp_fits(int num_seqs, int max_context_len);
 cudaError_t launch_decode_warp(const DecodeWarpArgs &a, cudaStream_t stream);
 
 }  // namespace pkv

@@ -81,7 +81,7 @@ def cases():
     yield "paged_decode_fp8_block", dict(k_scales=NULL), ARG
     yield "paged_decode_fp8_block", dict(v_scales=NULL), ARG
     yield "paged_decode_fp8_block", dict(s=1 << 30, most=64), ARG          # tiles past 32 bits
-    yield "paged_decode_window", dict(s=1 << 27), ARG                      # output rows past 32 bits
+    yield "paged_decode_window", dict(s=1 << 29), ARG
     yield "paged_prefill_window", dict(cu=NULL), ARG
     yield "paged_prefill_window", dict(cuk=NULL), ARG
     yield "paged_prefill_window", dict(total=-1), ARG
