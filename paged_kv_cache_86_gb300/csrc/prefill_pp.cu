@@ -69,7 +69,7 @@ constexpr int kItemRing = 4;         // work items handed from the Q/K loader to
 constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 9 + 2 * kItemRing;
 constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16 + 4 * kItemRing + 1024;
 // with a window, tiles start at a box: smaller boxes leave fewer keys that no row sees
-constexpr int kWinBoxRows = 32;
+constexpr int kWinBoxRows = 64;
 constexpr int kItemReaders = 1 + 1 + 8;   // V loader, MMA issuer, eight softmax warps
 
 struct PPParams {
@@ -103,12 +103,22 @@ struct PPParams {
   int window;
   int sinks;
   const __nv_bfloat16 *q;
+  int wide_out;      // out is 32-byte aligned
 };
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 __device__ __forceinline__ uint64_t desc_kmajor(uint32_t tile_base, int kk) {
@@ -673,14 +683,14 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
         const int key0 = j * kTile;
         if constexpr (kWin) {
-          if (key0 + kTile > see_hi) {
+          if (key0 + kTile > see_hi || max(key0, see_front) < min(see_lo, key0 + kTile)) {
 #pragma unroll
-            for (int e = 0; e < kTile; ++e) s[e] = (key0 + e < see_hi) ? s[e] : -INFINITY;
-          }
-          if (max(key0, see_front) < min(see_lo, key0 + kTile)) {
+            for (int cc = 0; cc < kTile; cc += 32) {
+              const uint32_t below = low_bits(see_hi - key0 - cc);
+              const uint32_t sees = below & (~low_bits(see_lo - key0 - cc) | low_bits(see_front - key0 - cc));
 #pragma unroll
-            for (int e = 0; e < kTile; ++e)
-              s[e] = (key0 + e < see_front || key0 + e >= see_lo) ? s[e] : -INFINITY;
+              for (int e = 0; e < 32; ++e) s[cc + e] = (sees >> e & 1u) ? s[cc + e] : -INFINITY;
+            }
           }
           // rows of a box behind the sequence's last key hold whatever the pool does:
           // zero their values (weight 0 times NaN is NaN); the keys' scores are masked
@@ -776,6 +786,21 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         if (store) {
           uint4 *dst = reinterpret_cast<uint4 *>(orow + cc * 32);
+          if constexpr (kWin) {
+#pragma unroll
+            for (int q8 = 0; q8 < 2; ++q8) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                w[e] = float2_to_bf16x2(o[q8 * 16 + 2 * e] * inv, o[q8 * 16 + 2 * e + 1] * inv);
+              if (p.wide_out) {
+                st_global_32(dst + 2 * q8, w);
+              } else {
+                dst[2 * q8] = make_uint4(w[0], w[1], w[2], w[3]);
+                dst[2 * q8 + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
+          } else
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
             uint4 v;
@@ -917,6 +942,7 @@ cudaError_t launch_prefill_pp(const PrefillArgs &a, cudaStream_t stream) {
   p.window = a.window;
   p.sinks = a.sinks < a.max_seqlen_k ? a.sinks : a.max_seqlen_k;
   p.q = static_cast<const __nv_bfloat16 *>(a.q);
+  p.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
   p.ticket = static_cast<uint32_t *>(a.workspace);
   if (p.ticket == nullptr) return cudaErrorInvalidValue;
   if (!a.ticket_zeroed)
