@@ -938,57 +938,15 @@ def tree_decode(q, key, value, k_cache, v_cache, block_tables, context_lens, cu_
     return out
 
 
-def _row_stride_of(t) -> int:
-    """_row_stride, and -1 for what is no tensor."""
-    try:
-        return _row_stride(t)
-    except AttributeError:
-        return -1
-
-
-def _fp8_block_pool(k_cache, v_cache, k_scales, v_scales):
-    """Sizes of an fp8 pool [NB, bs, Hkv, 128] with scales [NB, Hkv], checked."""
-    try:
-        fine = (k_cache.dtype is _U8 and k_cache.dim() == 4 and k_cache.is_contiguous()
-                and v_cache.dtype is _U8 and v_cache.dim() == 4 and v_cache.is_contiguous()
-                and k_scales.dtype is _F32 and k_scales.dim() == 2 and k_scales.is_contiguous()
-                and v_scales.dtype is _F32 and v_scales.dim() == 2 and v_scales.is_contiguous())
-    except AttributeError:
-        fine = False
-    if not fine:
-        _dense(_U8, 4, k_cache=k_cache, v_cache=v_cache)
-        _dense(_F32, 2, k_scales=k_scales, v_scales=v_scales)
-    shape = k_cache.shape
-    scales = (shape[0], shape[2])
-    if v_cache.shape != shape or k_scales.shape != scales or v_scales.shape != scales:
-        raise ValueError("caches must be [NB, bs, Hkv, D] and their scales [NB, Hkv]")
-    return shape
-
-
-def _tables_and_lens(block_tables, **lens):
-    """block_tables [S, MB] and the named one-dimensional int32 arrays, checked; their layout only."""
-    try:
-        fine = (block_tables.dtype is _I32 and block_tables.dim() == 2
-                and block_tables.is_contiguous()
-                and all(t.dtype is _I32 and t.dim() == 1 and t.is_contiguous()
-                        for t in lens.values()))
-    except AttributeError:
-        fine = False
-    if not fine:
-        _dense(_I32, 2, block_tables=block_tables)
-        _dense(_I32, 1, **lens)
-    return block_tables.shape
-
-
-def _one_device(**tensors) -> int:
-    """The device index that all the named tensors share."""
-    index = -1
-    for t in tensors.values():
-        at = t.get_device()
-        if at < 0 or (index >= 0 and at != index):
-            _refuse_device(**tensors)
-        index = at
-    return index
+def _refuse_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables, rows=(), **lens):
+    """Raise for the first argument of a call over an fp8 pool with block scales whose type or
+    layout the call's one-expression check has refused."""
+    _rows(**dict(rows))
+    _dense(_U8, 4, k_cache=k_cache, v_cache=v_cache)
+    _dense(_F32, 2, k_scales=k_scales, v_scales=v_scales)
+    _dense(_I32, 2, block_tables=block_tables)
+    _dense(_I32, 1, **lens)
+    raise ValueError("caches must be [NB, bs, Hkv, D], their scales [NB, Hkv]")
 
 
 def store_kvcache_fp8_block(key, value, k_cache, v_cache, k_scales, v_scales, block_tables,
@@ -998,19 +956,40 @@ def store_kvcache_fp8_block(key, value, k_cache, v_cache, k_scales, v_scales, bl
     are one power of two per (block, KV head). Sequence i's rows cu_seqlens_q[i] ..
     cu_seqlens_q[i + 1] - 1 are its last tokens; context_lens[i] counts them. Where a block
     holds older tokens and its scale has to grow, their codes are re-expressed."""
-    ks, vs = _row_stride_of(key), _row_stride_of(value)
-    if ks < 0 or vs < 0:
-        _rows(key=key, value=value)
-    nb, bs, hkv, d = _fp8_block_pool(k_cache, v_cache, k_scales, v_scales)
-    s, mb = _tables_and_lens(block_tables, cu_seqlens_q=cu_seqlens_q, context_lens=context_lens)
-    total = key.shape[0]
-    if key.shape != (total, hkv, d) or value.shape != key.shape:
+    try:
+        ks, vs, shape = _row_stride(key), _row_stride(value), k_cache.shape
+        fine = (ks >= 0 and vs >= 0 and k_cache.dtype is _U8 and k_cache.is_contiguous()
+                and v_cache.dtype is _U8 and v_cache.is_contiguous() and k_scales.dtype is _F32
+                and k_scales.is_contiguous() and v_scales.dtype is _F32
+                and v_scales.is_contiguous() and block_tables.dtype is _I32
+                and block_tables.is_contiguous() and cu_seqlens_q.dtype is _I32
+                and cu_seqlens_q.is_contiguous() and context_lens.dtype is _I32
+                and context_lens.is_contiguous() and len(shape) == 4 and v_cache.shape == shape
+                and k_scales.shape == (shape[0], shape[2]) and v_scales.shape == k_scales.shape
+                and block_tables.dim() == 2 and cu_seqlens_q.dim() == 1
+                and context_lens.dim() == 1)
+    except AttributeError:
+        fine = False
+    if not fine:
+        _refuse_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables,
+                          dict(key=key, value=value), cu_seqlens_q=cu_seqlens_q,
+                          context_lens=context_lens)
+    nb, bs, hkv, d = shape
+    s, mb = block_tables.shape
+    rows = key.shape
+    total = rows[0]
+    if rows[1] != hkv or rows[2] != d or value.shape != rows:
         raise ValueError("key / value must be [total_q, Hkv, D]")
     if cu_seqlens_q.shape[0] != s + 1 or context_lens.shape[0] != s:
         raise ValueError("metadata shape mismatch")
-    index = _one_device(key=key, value=value, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
-                        v_scales=v_scales, block_tables=block_tables, cu_seqlens_q=cu_seqlens_q,
-                        context_lens=context_lens)
+    index = key.get_device()
+    if not (index >= 0 and value.get_device() == index and k_cache.get_device() == index
+            and v_cache.get_device() == index and k_scales.get_device() == index
+            and v_scales.get_device() == index and block_tables.get_device() == index
+            and cu_seqlens_q.get_device() == index and context_lens.get_device() == index):
+        _refuse_device(key=key, value=value, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
+                       v_scales=v_scales, block_tables=block_tables, cu_seqlens_q=cu_seqlens_q,
+                       context_lens=context_lens)
     lib = _lib or load()
     ctx, st = _enter(index, stream)
     try:
@@ -1033,26 +1012,47 @@ def load_kvcache_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables, c
     rows may be strided); a bf16 block pool [NB, bs, Hkv, 128] viewed as rows is one."""
     if (key_out is None) != (value_out is None):
         raise ValueError("key_out and value_out go together")
-    nb, bs, hkv, d = _fp8_block_pool(k_cache, v_cache, k_scales, v_scales)
-    s, mb = _tables_and_lens(block_tables, context_lens=context_lens, row_starts=row_starts)
+    try:
+        shape = k_cache.shape
+        fine = (k_cache.dtype is _U8 and k_cache.is_contiguous() and v_cache.dtype is _U8
+                and v_cache.is_contiguous() and k_scales.dtype is _F32
+                and k_scales.is_contiguous() and v_scales.dtype is _F32
+                and v_scales.is_contiguous() and block_tables.dtype is _I32
+                and block_tables.is_contiguous() and context_lens.dtype is _I32
+                and context_lens.is_contiguous() and row_starts.dtype is _I32
+                and row_starts.is_contiguous() and len(shape) == 4 and v_cache.shape == shape
+                and k_scales.shape == (shape[0], shape[2]) and v_scales.shape == k_scales.shape
+                and block_tables.dim() == 2 and context_lens.dim() == 1 and row_starts.dim() == 1)
+    except AttributeError:
+        fine = False
+    if not fine:
+        _refuse_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables,
+                          context_lens=context_lens, row_starts=row_starts)
+    nb, bs, hkv, d = shape
+    s, mb = block_tables.shape
     if context_lens.shape[0] != s or row_starts.shape[0] != s:
         raise ValueError("metadata shape mismatch")
-    named = dict(k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
-                 block_tables=block_tables, context_lens=context_lens, row_starts=row_starts)
     if key_out is None:
         if num_rows is None or num_rows < 0:
             raise ValueError("num_rows must be given, and not negative, without key_out / value_out")
         ks = vs = hkv * d
     else:
-        ks, vs = _row_stride_of(key_out), _row_stride_of(value_out)
-        if ks < 0 or vs < 0:
-            _rows(key_out=key_out, value_out=value_out)
+        _rows(key_out=key_out, value_out=value_out)
+        ks, vs = _row_stride(key_out), _row_stride(value_out)
         if num_rows is None:
             num_rows = key_out.shape[0]
         if key_out.shape != (num_rows, hkv, d) or value_out.shape != key_out.shape:
             raise ValueError("key_out / value_out must be [num_rows, Hkv, D]")
-        named.update(key_out=key_out, value_out=value_out)
-    index = _one_device(**named)
+    index = k_cache.get_device()
+    if not (index >= 0 and v_cache.get_device() == index and k_scales.get_device() == index
+            and v_scales.get_device() == index and block_tables.get_device() == index
+            and context_lens.get_device() == index and row_starts.get_device() == index):
+        _refuse_device(k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
+                       block_tables=block_tables, context_lens=context_lens,
+                       row_starts=row_starts)
+    if key_out is not None and not (key_out.get_device() == index
+                                    and value_out.get_device() == index):
+        _refuse_device(k_cache=k_cache, key_out=key_out, value_out=value_out)
     lib = _lib or load()
     ctx, st = _enter(index, stream)
     try:
@@ -1081,33 +1081,6 @@ def _decode_window_workspace(index: int, s: int, hq: int, hkv: int, d: int) -> i
     return max(load().pkv_decode_window_workspace_size(s, hq, hkv, d), 256)
 
 
-def _query(q, rows):
-    """q [rows, Hq, D] bf16, dense."""
-    try:
-        fine = q.dtype is _BF16 and q.dim() == 3 and q.is_contiguous()
-    except AttributeError:
-        fine = False
-    if not fine:
-        _dense(_BF16, 3, q=q)
-    if rows is not None and q.shape[0] != rows:
-        raise ValueError("metadata rows must equal the number of sequences")
-    return q.shape
-
-
-def _bf16_pool(k_cache, v_cache):
-    """Sizes of a bf16 pool [NB, bs, Hkv, D], checked."""
-    try:
-        fine = (k_cache.dtype is _BF16 and k_cache.dim() == 4 and k_cache.is_contiguous()
-                and v_cache.dtype is _BF16 and v_cache.dim() == 4 and v_cache.is_contiguous())
-    except AttributeError:
-        fine = False
-    if not fine:
-        _dense(_BF16, 4, k_cache=k_cache, v_cache=v_cache)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache / v_cache shape mismatch")
-    return k_cache.shape
-
-
 def _workspace_for(workspace, need: int, q):
     """The caller's workspace (checked) or a new one of `need` bytes."""
     if workspace is None:
@@ -1124,13 +1097,34 @@ def paged_decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables
     """Decode attention over fp8 E4M3 caches [NB, bs, Hkv, 128] with scales [NB, Hkv], one
     query row q [S, Hq, 128] per sequence. window 0: over the whole context; otherwise over
     the last `window` tokens and the first `sinks`. Returns out [S, Hq, 128] bf16."""
-    nb, bs, hkv, d = _fp8_block_pool(k_cache, v_cache, k_scales, v_scales)
-    s, mb = _tables_and_lens(block_tables, context_lens=context_lens)
-    _, hq, dq = _query(q, s)
-    if dq != d or context_lens.shape[0] != s:
+    try:
+        shape = k_cache.shape
+        fine = (q.dtype is _BF16 and q.is_contiguous() and k_cache.dtype is _U8
+                and k_cache.is_contiguous() and v_cache.dtype is _U8 and v_cache.is_contiguous()
+                and k_scales.dtype is _F32 and k_scales.is_contiguous()
+                and v_scales.dtype is _F32 and v_scales.is_contiguous()
+                and block_tables.dtype is _I32 and block_tables.is_contiguous()
+                and context_lens.dtype is _I32 and context_lens.is_contiguous()
+                and len(shape) == 4 and v_cache.shape == shape
+                and k_scales.shape == (shape[0], shape[2]) and v_scales.shape == k_scales.shape
+                and q.dim() == 3 and block_tables.dim() == 2 and context_lens.dim() == 1)
+    except AttributeError:
+        fine = False
+    if not fine:
+        _dense(_BF16, 3, q=q)
+        _refuse_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables,
+                          context_lens=context_lens)
+    nb, bs, hkv, d = shape
+    s, hq, dq = q.shape
+    tables, mb = block_tables.shape
+    if dq != d or tables != s or context_lens.shape[0] != s:
         raise ValueError("q / cache / metadata shape mismatch")
-    index = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
-                        v_scales=v_scales, block_tables=block_tables, context_lens=context_lens)
+    index = q.get_device()
+    if not (index >= 0 and k_cache.get_device() == index and v_cache.get_device() == index
+            and k_scales.get_device() == index and v_scales.get_device() == index
+            and block_tables.get_device() == index and context_lens.get_device() == index):
+        _refuse_device(q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
+                       v_scales=v_scales, block_tables=block_tables, context_lens=context_lens)
     lib = _lib or load()
     ctx, st = _enter(index, stream)
     try:
@@ -1153,13 +1147,31 @@ def paged_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale: 
     """Decode attention over the last `window` tokens and the first `sinks` of each sequence
     in bf16 caches [NB, bs, Hkv, 128], one query row q [S, Hq, 128] per sequence. Returns out
     [S, Hq, 128] bf16."""
-    nb, bs, hkv, d = _bf16_pool(k_cache, v_cache)
-    s, mb = _tables_and_lens(block_tables, context_lens=context_lens)
-    _, hq, dq = _query(q, s)
-    if dq != d or context_lens.shape[0] != s:
+    try:
+        shape = k_cache.shape
+        fine = (q.dtype is _BF16 and q.is_contiguous() and k_cache.dtype is _BF16
+                and k_cache.is_contiguous() and v_cache.dtype is _BF16
+                and v_cache.is_contiguous() and block_tables.dtype is _I32
+                and block_tables.is_contiguous() and context_lens.dtype is _I32
+                and context_lens.is_contiguous() and len(shape) == 4 and q.dim() == 3
+                and v_cache.dim() == 4 and block_tables.dim() == 2 and context_lens.dim() == 1)
+    except AttributeError:
+        fine = False
+    if not fine:
+        _dense(_BF16, 3, q=q)
+        _dense(_BF16, 4, k_cache=k_cache, v_cache=v_cache)
+        _dense(_I32, 2, block_tables=block_tables)
+        _dense(_I32, 1, context_lens=context_lens)
+    nb, bs, hkv, d = shape
+    s, hq, dq = q.shape
+    tables, mb = block_tables.shape
+    if dq != d or v_cache.shape != shape or tables != s or context_lens.shape[0] != s:
         raise ValueError("q / cache / metadata shape mismatch")
-    index = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                        context_lens=context_lens)
+    index = q.get_device()
+    if not (index >= 0 and k_cache.get_device() == index and v_cache.get_device() == index
+            and block_tables.get_device() == index and context_lens.get_device() == index):
+        _refuse_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                       context_lens=context_lens)
     lib = _lib or load()
     ctx, st = _enter(index, stream)
     try:
@@ -1182,13 +1194,35 @@ def paged_prefill_window(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_
     """Causal chunked-prefill attention in which the row at position t sees the keys p <= t
     with p < sinks or p > t - window; otherwise as paged_prefill. Returns out
     [total_q, Hq, 128] bf16; rows behind cu_seqlens_q[-1] are not written."""
-    nb, bs, hkv, d = _bf16_pool(k_cache, v_cache)
-    s, mb = _tables_and_lens(block_tables, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
-    total, hq, dq = _query(q, None)
-    if dq != d or cu_seqlens_q.shape[0] != s + 1 or cu_seqlens_k.shape[0] != s + 1:
+    try:
+        shape = k_cache.shape
+        fine = (q.dtype is _BF16 and q.is_contiguous() and k_cache.dtype is _BF16
+                and k_cache.is_contiguous() and v_cache.dtype is _BF16
+                and v_cache.is_contiguous() and block_tables.dtype is _I32
+                and block_tables.is_contiguous() and cu_seqlens_q.dtype is _I32
+                and cu_seqlens_q.is_contiguous() and cu_seqlens_k.dtype is _I32
+                and cu_seqlens_k.is_contiguous() and len(shape) == 4 and q.dim() == 3
+                and v_cache.dim() == 4 and block_tables.dim() == 2 and cu_seqlens_q.dim() == 1
+                and cu_seqlens_k.dim() == 1)
+    except AttributeError:
+        fine = False
+    if not fine:
+        _dense(_BF16, 3, q=q)
+        _dense(_BF16, 4, k_cache=k_cache, v_cache=v_cache)
+        _dense(_I32, 2, block_tables=block_tables)
+        _dense(_I32, 1, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
+    nb, bs, hkv, d = shape
+    total, hq, dq = q.shape
+    s, mb = block_tables.shape
+    if (dq != d or v_cache.shape != shape or cu_seqlens_q.shape[0] != s + 1
+            or cu_seqlens_k.shape[0] != s + 1):
         raise ValueError("q / cache / metadata shape mismatch")
-    index = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                        cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
+    index = q.get_device()
+    if not (index >= 0 and k_cache.get_device() == index and v_cache.get_device() == index
+            and block_tables.get_device() == index and cu_seqlens_q.get_device() == index
+            and cu_seqlens_k.get_device() == index):
+        _refuse_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                       cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
     lib = _lib or load()
     ctx, st = _enter(index, stream)
     try:

@@ -32,7 +32,7 @@ constexpr int kRowBytes = 128;          // codes of one head's row
 
 // The largest i in [0, n) with a[i] <= t (0 if there is none), for non-decreasing
 // a: 32 probes at a time, one a lane. The whole warp calls it.
-__device__ __forceinline__ int last_at_or_before(const int32_t *a, int n, long long t) {
+__device__ __forceinline__ int last_at_or_before(const int32_t *a, int n, int t) {
   const int lane = threadIdx.x & 31;
   int lo = 0;
   while (n > 1) {
@@ -80,7 +80,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float by) {
 // CTA (x, y): the touched blocks whose first new row lies in rows
 // [x * chunk, (x + 1) * chunk), for the (K or V, head) pairs y * teams_at_once ...
 // 2 * Hkv - 1, kTeams / team of them, `team` half-warps each.
-__global__ void __launch_bounds__(kThreads) store_fp8_block_kernel(const Fp8BlockStoreArgs a, int chunk,
+__global__ void __launch_bounds__(kThreads, 4) store_fp8_block_kernel(const Fp8BlockStoreArgs a, int chunk,
                                                                    int team) {
   __shared__ uint32_t s_top[2][kTeams];
   const int lane = threadIdx.x & 31, sub = lane & 15;
@@ -98,44 +98,45 @@ __global__ void __launch_bounds__(kThreads) store_fp8_block_kernel(const Fp8Bloc
   const int bs = a.block_size;
   const int64_t cap = static_cast<int64_t>(a.max_blocks_per_seq) * bs;
 
-  int64_t t = static_cast<int64_t>(blockIdx.x) * chunk;
-  const int64_t t_end = min(t + chunk, static_cast<int64_t>(a.total_q));
+  int t = blockIdx.x * chunk;                     // the launcher keeps this below total_q
+  const int t_end = t + min(chunk, a.total_q - t);
   // a round of one token a sequence: row t is sequence t's
   int seq;
   if (t < a.num_seqs && __ldg(a.cu_seqlens_q + t) == t && __ldg(a.cu_seqlens_q + t + 1) == t + 1)
-    seq = static_cast<int>(t);
+    seq = t;
   else
     seq = last_at_or_before(a.cu_seqlens_q, a.num_seqs, t);
   int units = 0;                                  // every thread of the CTA counts the same
   for (; seq < a.num_seqs && t < t_end; ++seq) {
-    const int64_t q0 = __ldg(a.cu_seqlens_q + seq), q1 = __ldg(a.cu_seqlens_q + seq + 1);
-    const int64_t ctx = __ldg(a.context_lens + seq);
+    const int q0 = __ldg(a.cu_seqlens_q + seq), q1 = __ldg(a.cu_seqlens_q + seq + 1);
+    const int ctx = __ldg(a.context_lens + seq);
     if (q0 < 0 || q1 < q0 || q1 > a.total_q || ctx < q1 - q0 || ctx > cap) {
       if (reports) raise_error(a.err, PKV_DEVERR_LENGTH);
       continue;
     }
-    const int64_t start = ctx - (q1 - q0);        // position of the sequence's first new row
+    const int start = ctx - (q1 - q0);            // position of the sequence's first new row
     if (t < q0) t = q0;
-    if (t > q0) {                                 // behind the first row: at the next block's first
-      const int64_t off = (start + (t - q0)) % bs;
-      if (off > 0) t = min(t + bs - off, q1);
+    // row and block of the position of row t; behind the first row, on to the next block's first
+    int blk = (start + (t - q0)) / bs, off0 = (start + (t - q0)) - blk * bs;
+    if (t > q0 && off0 > 0) {
+      t = bs - off0 < q1 - t ? t + (bs - off0) : q1;
+      ++blk;
+      off0 = 0;
     }
-    for (; t < q1 && t < t_end; ++units) {
-      const int64_t pos = start + (t - q0);
-      const int blk = static_cast<int>(pos / bs), off0 = static_cast<int>(pos % bs);
-      const int n = static_cast<int>(min(static_cast<int64_t>(bs - off0), q1 - t));
+    for (; t < q1 && t < t_end; ++units, ++blk, off0 = 0) {
+      const int n = min(bs - off0, q1 - t);
       const int id = __ldg(a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq + blk);
-      const bool good = id >= 0 && id < a.num_blocks;
-      if (!good && reports) raise_error(a.err, PKV_DEVERR_BLOCK_ID);
-      const bool mine = active && good;
       // new row r of the unit: row t + r of the call, row off0 + r of the block
       const __nv_bfloat16 *row = src + t * stride;
       uint4 held[kHold];
 #pragma unroll
       for (int i = 0; i < kHold; ++i) {
         const int r = member + i * team;
-        held[i] = mine && r < n ? __ldg(reinterpret_cast<const uint4 *>(row + r * stride)) : make_uint4(0, 0, 0, 0);
+        held[i] = active && r < n ? __ldg(reinterpret_cast<const uint4 *>(row + r * stride)) : make_uint4(0, 0, 0, 0);
       }
+      const bool good = id >= 0 && id < a.num_blocks;
+      if (!good && reports) raise_error(a.err, PKV_DEVERR_BLOCK_ID);
+      const bool mine = active && good;
       float *scale_at = scales + static_cast<int64_t>(good ? id : 0) * a.num_kv_heads + head;
       float old = 0.f;
       if (off0 > 0 && mine && sub == 0) old = *scale_at;
@@ -189,9 +190,17 @@ __global__ void __launch_bounds__(kThreads) store_fp8_block_kernel(const Fp8Bloc
         }
         if (off0 > 0 && now != old) {
           const float by = old * inv;
-          for (int r = member; r < off0; r += team) {
-            uint2 *p = reinterpret_cast<uint2 *>(dst - (off0 - r) * step);
-            *p = make_uint2(rescale4(p->x, by), rescale4(p->y, by));
+          uint8_t *older = dst - off0 * step;
+          for (int r = member; r < off0; r += 4 * team) {
+            uint2 c[4];                           // on their way together
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (r + i * team < off0) c[i] = *reinterpret_cast<const uint2 *>(older + (r + i * team) * step);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (r + i * team < off0)
+                *reinterpret_cast<uint2 *>(older + (r + i * team) * step) =
+                    make_uint2(rescale4(c[i].x, by), rescale4(c[i].y, by));
           }
         }
         if (member == 0 && sub == 0) *scale_at = now;
@@ -289,12 +298,12 @@ cudaError_t launch_store_fp8_block(const Fp8BlockStoreArgs &a, cudaStream_t stre
   // From the average of new tokens a sequence: rows a CTA looks for first rows in,
   // and half-warps a (block, head) is spread over, so that a full block's rows stay
   // in registers between the maximum and the codes.
-  const int avg = (a.total_q + a.num_seqs - 1) / a.num_seqs;
+  const int avg = (a.total_q - 1) / a.num_seqs + 1;
   const int rows = avg < a.block_size ? avg : a.block_size;
   int team = 1;
   while (team < kTeams && team * kHold < rows) team *= 2;
   const int at_once = kTeams / team;
-  const dim3 grid(static_cast<unsigned>((a.total_q + rows - 1) / rows),
+  const dim3 grid(static_cast<unsigned>((a.total_q - 1) / rows + 1),
                   static_cast<unsigned>((2 * a.num_kv_heads + at_once - 1) / at_once));
   store_fp8_block_kernel<<<grid, kThreads, 0, stream>>>(a, rows, team);
   return cudaGetLastError();
