@@ -636,13 +636,23 @@ decode_direct_kernel(const WarpParams p) {
         for (int d = 0; d < H::kVL; ++d) vr[i][d] = r >= 0 ? ld_once(src + d * 128) : make_uint4(0, 0, 0, 0);
       }
     };
-    int id, off, row;
-    float scale;
+    // A token's heads lie side by side, but the warps that take them come by at eight
+    // different times: a tile ahead of its loads one of them asks L2 for all of them.
+    auto ask = [&](int r) {
+      if (r >= 0 && (lane & 15) % vheads == vh)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                     :: "l"((lane < 16 ? p.k_cache : p.v_cache) + r * row_bytes), "r"(static_cast<uint32_t>(row_bytes)));
+    };
+    int id, off, row, next_row;
+    float scale, next_scale;
     look_up(walk.t0, id, off);
     resolve(walk.t0, id, off, row, scale);
-    look_up(walk.t0 + 1, id, off);
     load_k(row);
     load_v(row);
+    look_up(walk.t0 + 1, id, off);
+    resolve(walk.t0 + 1, id, off, next_row, next_scale);
+    ask(next_row);
+    look_up(walk.t0 + 2, id, off);
     const int64_t out_row = static_cast<int64_t>(walk.seq) * p.num_q_heads + kvh * p.group + head0;
     x.start(p.q + out_row * kHD, heads, p.scale_log2);
 #pragma unroll 1
@@ -659,19 +669,20 @@ decode_direct_kernel(const WarpParams p) {
         vs1 = __shfl_sync(0xffffffffu, ls, g + 24);
       }
       // the next tile's K is on its way while the softmax runs, its V after the PV
-      int next_row = -1;
-      float next_scale = 0.f;
-      if (t + 1 < t1) {
-        resolve(t + 1, id, off, next_row, next_scale);
-        look_up(t + 2, id, off);
-        load_k(next_row);
-      }
+      int row2;
+      float scale2;
+      resolve(t + 2, id, off, row2, scale2);
+      ask(row2);
+      look_up(t + 3, id, off);
+      if (t + 1 < t1) load_k(next_row);
       uint32_t pb[NT][2];
       x.weights(s, real0, real1, ks0, ks1, vs0, vs1, pb);
       x.accumulate(vr, pb);
       if (t + 1 < t1) load_v(next_row);
       row = next_row;
       scale = next_scale;
+      next_row = row2;
+      next_scale = scale2;
     }
     const int64_t rec = (static_cast<int64_t>(range * 2 + (walk.t0 == 0 ? 1 : 0)) * vheads + vh) * p.per_chunk;
     x.finish(walk.whole(), heads, p.out + out_row * kHD, p.ml + rec, p.po + rec * kHD);
