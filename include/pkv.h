@@ -489,7 +489,8 @@ pkv_status pkv_load_kvcache_fp8_block(void *key_out, void *value_out,
  * window 0 is the whole context.
  *   Arguments, graphs and errors as for pkv_paged_decode, except: any
  *   num_q_heads that is a multiple of num_kv_heads, any block_size >= 1; scale
- *   > 0; num_blocks * block_size at most 2^31 - 512; out and q must not overlap;
+ *   > 0; max_context_len and num_blocks * block_size at most 2^31 - 512; out
+ *   and q must not overlap;
  *   workspace of pkv_decode_window_workspace_size bytes.
  *   A token that is not seen, and a row behind the last token, is never touched,
  *   whatever it holds. A seen key or value that is not finite counts as it does

@@ -525,6 +525,7 @@ def paged_prefill(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_tables,
 # fails does it look for the tensor at fault and name it.
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+_MAX_I32 = 0x7fffffff   # windows and sinks beyond it see the same: no context is longer
 # the current stream's handle without building a Stream object (2 us of a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -1134,8 +1135,9 @@ def paged_decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), mb,
             context_lens.data_ptr(), s, mb * bs if max_context_len is None else max_context_len,
-            window, sinks, hq, hkv, d, bs, nb, scale, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), st), "pkv_paged_decode_fp8_block")
+            min(window, _MAX_I32), min(sinks, _MAX_I32), hq, hkv, d, bs, nb, scale,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), st),
+            "pkv_paged_decode_fp8_block")
     finally:
         _leave(ctx)
     return out
@@ -1180,9 +1182,10 @@ def paged_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale: 
         _check(lib.pkv_paged_decode_window(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_tables.data_ptr(), mb, context_lens.data_ptr(), s,
-            mb * bs if max_context_len is None else max_context_len, window, sinks, hq, hkv, d,
-            bs, nb, scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            PKV_BF16, st), "pkv_paged_decode_window")
+            mb * bs if max_context_len is None else max_context_len, min(window, _MAX_I32),
+            min(sinks, _MAX_I32), hq, hkv, d, bs, nb, scale, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), PKV_BF16, st),
+            "pkv_paged_decode_window")
     finally:
         _leave(ctx)
     return out
@@ -1231,7 +1234,8 @@ def paged_prefill_window(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_
         _check(lib.pkv_paged_prefill_window(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), max_seqlen_q, max_seqlen_k,
-            block_tables.data_ptr(), mb, s, total, window, sinks, hq, hkv, d, bs, nb, scale,
+            block_tables.data_ptr(), mb, s, total, min(window, _MAX_I32), min(sinks, _MAX_I32),
+            hq, hkv, d, bs, nb, scale,
             workspace.data_ptr(), workspace.numel() * workspace.element_size(), PKV_BF16, st),
             "pkv_paged_prefill_window")
     finally:

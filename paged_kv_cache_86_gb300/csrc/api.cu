@@ -975,6 +975,7 @@ static pkv_status decode_warp_call(void *out, const void *q, const void *k_cache
     return PKV_ERR_ARG;
   if (head_dim != 128 || num_q_heads % num_kv_heads != 0) return PKV_ERR_SHAPE;
   if (int64_t(max_context_len) > int64_t(max_blocks_per_seq) * block_size || num_q_heads > 65535 ||
+      max_context_len > 0x7fffffff - 512 ||
       // cache rows, a box past the last one included, are numbered in int32
       int64_t(num_blocks) * block_size > 0x7fffffffll - 512 ||
       !pkv::decode_warp_fits(num_seqs, max_context_len))

@@ -1003,10 +1003,10 @@ bool shape_of(int num_q_heads, int num_kv_heads, int block_size, bool fp8, Shape
   s->ring = block_size % 8 == 0 && s->chunks < most_warps;
   if (s->ring) {
     s->unit = block_size % 16 == 0 ? 16 : 8;
-    s->heads_per_cta = (most_warps - 1) / s->chunks;           // a warp per (head, chunk) and a producer
-    if (s->heads_per_cta > 8) s->heads_per_cta = 8;
-    if (s->heads_per_cta > num_kv_heads) s->heads_per_cta = num_kv_heads;
-    s->head_groups = (num_kv_heads + s->heads_per_cta - 1) / s->heads_per_cta;
+    int heads = (most_warps - 1) / s->chunks;                  // a warp per (head, chunk) and a producer
+    if (heads > 8) heads = 8;
+    s->head_groups = (num_kv_heads + heads - 1) / heads;
+    s->heads_per_cta = (num_kv_heads + s->head_groups - 1) / s->head_groups;
     const int bytes = stage_bytes(fp8, s->heads_per_cta), ring_warps = s->heads_per_cta * s->chunks;
     s->rings = most_warps / (ring_warps + 1);
     while (s->rings > 1 && kRingBytes / (s->rings * bytes) < 3) --s->rings;

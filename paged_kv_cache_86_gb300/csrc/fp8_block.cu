@@ -310,7 +310,7 @@ cudaError_t launch_store_fp8_block(const Fp8BlockStoreArgs &a, cudaStream_t stre
 }
 
 cudaError_t launch_load_fp8_block(const Fp8BlockLoadArgs &a, cudaStream_t stream) {
-  load_fp8_block_kernel<<<static_cast<unsigned>((a.num_rows + kLoadRows - 1) / kLoadRows), kThreads, 0, stream>>>(a);
+  load_fp8_block_kernel<<<static_cast<unsigned>((a.num_rows - 1) / kLoadRows + 1), kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

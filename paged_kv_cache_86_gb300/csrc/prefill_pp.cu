@@ -33,6 +33,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "pkv_device.cuh"
@@ -95,7 +96,9 @@ struct PPParams {
   int num_kv_heads;
   int q_tiles;       // 128-row query tiles of the longest chunk
   int pair_tiles;    // odd GQA group: A and B are two consecutive query tiles of one head
-  uint32_t *ticket;  // next unclaimed work item (zeroed before the launch)
+  // next unclaimed work item (zeroed before the launch); with a window nullptr if
+  // every item has a CTA of its own
+  uint32_t *ticket;
   float scale_log2;
   uint32_t *err;
   // sliding-window instances: a row at position t sees the keys <= t that are
@@ -286,7 +289,7 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const int q_end = p.cu_q[it.seq + 1];
     it.k_len = p.cu_k[it.seq + 1] - p.cu_k[it.seq];
     it.q_len = q_end - it.q_begin;
-    if (it.q_len < 0 || it.q_len > p.max_seqlen_q || q_end > p.total_q || it.k_len < 0 ||
+    if (it.q_begin < 0 || it.q_len < 0 || it.q_len > p.max_seqlen_q || q_end > p.total_q || it.k_len < 0 ||
         it.k_len > p.max_seqlen_k || (p.causal && it.q_len > it.k_len)) {
       if (threadIdx.x == 0 && it.qh_a == 0 && it.r0 == 0) raise_error(p.err, PKV_DEVERR_LENGTH);
       return false;
@@ -419,7 +422,8 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 !mbar_wait(item_empty(slot), ((n / kItemRing) - 1) & 1, abort_flag)) {
               fail();
             } else {
-              w = static_cast<int>(atomicAdd(p.ticket, 1u));
+              if (kWin && p.ticket == nullptr) w = n == 0 ? static_cast<int>(blockIdx.x) : n_items;
+              else w = static_cast<int>(atomicAdd(p.ticket, 1u));
               item_ring[slot] = w;
               mbar_arrive(item_full(slot));
             }
@@ -688,8 +692,10 @@ prefill_pp_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             for (int cc = 0; cc < kTile; cc += 32) {
               const uint32_t below = low_bits(see_hi - key0 - cc);
               const uint32_t sees = below & (~low_bits(see_lo - key0 - cc) | low_bits(see_front - key0 - cc));
+              if (sees != 0xffffffffu) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) s[cc + e] = (sees >> e & 1u) ? s[cc + e] : -INFINITY;
+                for (int e = 0; e < 32; ++e) s[cc + e] = (sees >> e & 1u) ? s[cc + e] : -INFINITY;
+              }
             }
           }
           // rows of a box behind the sequence's last key hold whatever the pool does:
@@ -887,9 +893,14 @@ bool prefill_pp_supported(int num_q_heads, int num_kv_heads, int block_size) {
 }
 
 cudaError_t launch_prefill_pp(const PrefillArgs &a, cudaStream_t stream) {
-  static std::once_flag attr_once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(attr_once, [] {
+  // once a device: the attribute belongs to the device's copy of the kernel
+  static std::atomic<uint64_t> attr_set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t dev_bit = uint64_t(1) << (dev & 63);
+  if (dev > 63 || !(attr_set.load() & dev_bit)) {
+    cudaError_t attr_err = cudaSuccess;
     for (auto kern : {prefill_pp_kernel<false, false>, prefill_pp_kernel<true, false>,
                       prefill_pp_kernel<false, true>, prefill_pp_kernel<true, true>}) {
       if (attr_err == cudaSuccess)
@@ -901,8 +912,9 @@ cudaError_t launch_prefill_pp(const PrefillArgs &a, cudaStream_t stream) {
       if (attr_err == cudaSuccess) attr_err = cudaFuncGetAttributes(&fa, kern);
       if (attr_err == cudaSuccess && fa.numRegs != kRegsLaunch) attr_err = cudaErrorInvalidConfiguration;
     }
-  });
-  if (attr_err != cudaSuccess) return attr_err;
+    if (attr_err != cudaSuccess) return attr_err;
+    attr_set.fetch_or(dev_bit);
+  }
   const bool gather = a.block_size % 8 != 0, windowed = a.window > 0;
   auto kern = gather ? (windowed ? prefill_pp_kernel<true, true> : prefill_pp_kernel<true, false>)
                      : (windowed ? prefill_pp_kernel<false, true> : prefill_pp_kernel<false, false>);
@@ -945,18 +957,17 @@ cudaError_t launch_prefill_pp(const PrefillArgs &a, cudaStream_t stream) {
   p.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 ? 1 : 0;
   p.ticket = static_cast<uint32_t *>(a.workspace);
   if (p.ticket == nullptr) return cudaErrorInvalidValue;
-  if (!a.ticket_zeroed)
-    if (cudaError_t me = cudaMemsetAsync(p.ticket, 0, sizeof(uint32_t), stream)) return me;
   const long long n_items =
       p.pair_tiles ? static_cast<long long>((p.q_tiles + 1) / 2) * a.num_q_heads * a.num_seqs
                    : static_cast<long long>(p.q_tiles) * (a.num_q_heads / 2) * a.num_seqs;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
   const int sms = sm_count(dev);
   if (sms <= 0) return cudaErrorInvalidValue;
   long long ctas = n_items < sms ? n_items : sms;
   if (a.max_ctas > 0 && a.max_ctas < ctas) ctas = a.max_ctas;
+  // (a clearing node in front of the kernel costs a small call 2 us)
+  if (windowed && n_items <= ctas) p.ticket = nullptr;
+  else if (!a.ticket_zeroed)
+    if (cudaError_t me = cudaMemsetAsync(p.ticket, 0, sizeof(uint32_t), stream)) return me;
   const dim3 grid(static_cast<unsigned>(ctas));
   if (!a.overlap_previous) {
     kern<<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, p);

@@ -214,3 +214,95 @@ def test_results_do_not_depend_on_the_workspace():
     n = pkv.decode_window_workspace_size(2, 16, 4)
     outs = [w.call(pkv, d, workspace=torch.full((n,), b, dtype=torch.uint8, device="cuda")) for b in (0, 255)]
     assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("hq,hkv,bs,ctx,window,sinks", [
+    (12, 12, 16, [70, 33], 40, 2),                   # heads in two groups of six
+    (18, 9, 8, [70, 33], 40, 2),                     # nine heads: groups of five with one to spare, boxes of 8 tokens
+    (64, 16, 8, [90, 5, 0], 33, 9),
+    (48, 3, 8, [200, 21], 100, 12),
+    (33, 1, 8, [300, 9], 77, 8),                     # three chunks of eleven heads
+    (130, 1, 16, [40, 100], 64, 3),                  # nine chunks
+    (400, 1, 16, [20], 9, 3),                        # more chunks than a CTA has warps
+], ids=str)
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_head_layouts(hq, hkv, bs, ctx, window, sinks, fp8):
+    for win in (window, 0) if fp8 else (window,):
+        w = Window(hq, hkv, bs, ctx, win, sinks, fp8=fp8, seed=hq).poison_unseen()
+        assert_window_close(w.call(pkv, w.device()), w)
+    assert pkv.get_device_errors() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_more_sequences_than_ranges(fp8):
+    """Cut sequences are found by range where there are fewer ranges than sequences; empty ones among
+    them, and at both ends."""
+    rng = np.random.default_rng(3)
+    ctx = [0, 0] + [int(c) for c in rng.integers(0, 90, 900)] + [700, 0]
+    w = Window(16, 8, 16, ctx, 60, 5, fp8=fp8).poison_unseen()
+    out = torch.full((len(ctx), 16, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    w.call(pkv, w.device(), out=out)
+    assert_window_close(out, w)
+    assert pkv.get_device_errors() == 0
+
+
+@pytest.mark.parametrize("hkv,bs", [(8, 16), (1, 8), (2, 6)])
+def test_one_long_sequence(hkv, bs):
+    """One request over every range: many records merged by several warps."""
+    w = Window(2 * hkv, hkv, bs, [40000], 0, 0, fp8=True, seed=2)
+    assert_window_close(w.call(pkv, w.device()), w)
+
+
+def test_no_sequences_and_no_context():
+    w = Window(8, 2, 16, [0, 0], 5, 1)
+    out = torch.full((2, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    w.call(pkv, w.device(), out=out)
+    assert torch.equal(out, torch.zeros_like(out))
+    d = w.device()
+    pkv.paged_decode_window(d["q"][:0], d["k_cache"], d["v_cache"], d["block_tables"][:0], d["context_lens"][:0],
+                            w.scale, 5)
+    assert pkv.get_device_errors() == 0
+
+
+def test_windows_past_32_bits_see_everything():
+    w = Window(8, 2, 16, [50, 3], 1 << 20, 0)
+    d = w.device()
+    a = w.call(pkv, d)
+    w.window, w.sinks = (1 << 32) + 5, 1 << 33
+    assert torch.equal(a, w.call(pkv, d))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("bs", [16, 6])
+def test_pools_past_32_bit_offsets(fp8, bs):
+    """The request's blocks lie behind the first 4 GB of the caches."""
+    w = Window(16, 8, bs, [300, 40], 200, 4, fp8=fp8)
+    d = w.device()
+    far = (1 << 32) // (bs * 8 * 128 * (1 if fp8 else 2)) + 7
+    for n in ("k_cache", "v_cache"):
+        pool = torch.empty((far + w.num_blocks,) + tuple(d[n].shape[1:]), dtype=d[n].dtype, device="cuda")
+        pool[far:] = d[n]
+        d[n] = pool
+    for n in ("k_scales", "v_scales") if fp8 else ():
+        pool = torch.ones((far + w.num_blocks, 8), device="cuda")
+        pool[far:] = d[n]
+        d[n] = pool
+    d["block_tables"] = torch.where(d["block_tables"] >= 0, d["block_tables"] + far, -1).to(torch.int32)
+    assert_window_close(w.call(pkv, d), w)
+    assert pkv.get_device_errors() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_two_calls_at_once(fp8):
+    """Calls on two streams, each with its own workspace, over and over."""
+    ws = [Window(32, 8, 16, ctx, 300, 4, fp8=fp8, seed=i) for i, ctx in enumerate(([900, 50, 3], [20, 1500]))]
+    ds = [w.device() for w in ws]
+    streams = [torch.cuda.Stream() for _ in ws]
+    torch.cuda.synchronize()
+    outs = [[w.call(pkv, d, stream=s) for w, d, s in zip(ws, ds, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in outs:
+        for o, first in zip(pair, outs[0]):
+            assert torch.equal(o, first)
+    for o, w in zip(outs[0], ws):
+        assert_window_close(o, w)

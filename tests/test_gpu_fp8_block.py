@@ -246,3 +246,70 @@ def test_load_bad_blocks_and_lengths():
     a[5] = i32([-3, 9])
     pkv.load_kvcache_fp8_block(*a, i32([0, 40]), num_rows=49)
     assert pkv.get_device_errors() == 4
+
+
+def test_pools_past_32_bit_offsets():
+    """Blocks behind the first 4 GB of the caches, written and read back."""
+    s = Store(8, 16, [5, 0], [30, 20])
+    far = (1 << 32) // (16 * 8 * 128) + 3
+    caches, scales = [], []
+    for c, sc in s.pools:
+        cache = torch.empty((far + s.num_blocks, 16, 8, 128), dtype=torch.uint8, device="cuda")
+        cache[far:] = torch.from_numpy(c).cuda()
+        scale = torch.ones((far + s.num_blocks, 8), device="cuda")
+        scale[far:] = torch.from_numpy(sc).float().cuda()
+        caches.append(cache)
+        scales.append(scale)
+    tables = i32(np.where(s.tables >= 0, s.tables + far, -1))
+    pkv.store_kvcache_fp8_block(s.x[0].cuda(), s.x[1].cuda(), *caches, *scales, tables, i32(s.cu), i32(s.after))
+    got = pkv.load_kvcache_fp8_block(*caches, *scales, tables, i32(s.after), i32([0, s.after[0]]), sum(s.after))
+    for i in range(2):
+        want = store_reference(s.x[i], *s.pools[i], s.tables, s.cu, s.after)
+        assert np.array_equal(caches[i][far:].cpu().numpy(), want[0])
+        rows = []
+        for r, a in enumerate(s.after):
+            p = np.arange(a)
+            b = s.tables[r, p // 16]
+            rows.append(torch.from_numpy(TABLE[want[0][b, p % 16]] * want[1][b][..., None]).to(torch.bfloat16))
+        assert torch.equal(got[i].cpu(), torch.cat(rows))
+    assert pkv.get_device_errors() == 0
+
+
+def test_captured_store_replays_with_new_rows():
+    s = Store(4, 16, [3, 20], [1, 1])
+    caches = [torch.from_numpy(c).cuda() for c, _ in s.pools]
+    scales = [torch.from_numpy(c).float().cuda() for _, c in s.pools]
+    x, tables, cu = [t.cuda() for t in s.x], i32(s.tables), i32(s.cu)
+    lens = i32(s.after)
+    held = [tuple(p) for p in s.pools]
+    args = (*x, *caches, *scales, tables, cu, lens)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        pkv.store_kvcache_fp8_block(*args)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkv.store_kvcache_fp8_block(*args)
+    after = list(s.after)
+    held = [store_reference(t, *h, s.tables, s.cu, after) for t, h in zip(s.x, held)]
+    for step in range(8):
+        new = [(normal((2, 4, 128), 50 + 2 * step + i).float() * (1 + step)).to(torch.bfloat16) for i in range(2)]
+        after = [after[0] + 1, after[1] + (1 if after[1] < 32 else 0)]
+        for dst, src in zip(x, new):
+            dst.copy_(src)
+        lens.copy_(i32(after))
+        g.replay()
+        held = [store_reference(t, *h, s.tables, s.cu, after) for t, h in zip(new, held)]
+        for i in range(2):
+            assert np.array_equal(caches[i].cpu().numpy(), held[i][0])
+            assert np.array_equal(scales[i].double().cpu().numpy(), held[i][1])
+    assert pkv.get_device_errors() == 0
+
+
+def test_store_of_many_short_sequences_and_empty_ones():
+    rng = np.random.default_rng(4)
+    new = [int(n) for n in rng.integers(0, 4, 700)]
+    before = [int(n) for n in rng.integers(0, 20, 700)]
+    Store(2, 8, before, new).check()
+    Store(1, 16, [0] * 40 + [7], [0] * 40 + [33]).check()

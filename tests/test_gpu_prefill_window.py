@@ -117,3 +117,42 @@ def test_captured_call_replays_with_other_lengths():
         torch.cuda.synchronize()
         assert_window_close(out, w)
     assert pkv.get_device_errors() == 0
+
+
+def test_pools_past_32_bit_offsets():
+    w = Window(4, 2, 16, [200, 40], 50, 4, q_lens=[140, 40])
+    d = w.device()
+    far = (1 << 32) // (16 * 2 * 128 * 2) + 7
+    for n in ("k_cache", "v_cache"):
+        pool = torch.empty((far + w.num_blocks,) + tuple(d[n].shape[1:]), dtype=d[n].dtype, device="cuda")
+        pool[far:] = d[n]
+        d[n] = pool
+    d["block_tables"] = torch.where(d["block_tables"] >= 0, d["block_tables"] + far, -1).to(torch.int32)
+    assert_window_close(w.call(pkv, d), w)
+
+
+def test_output_at_any_16_byte_boundary():
+    w = Window(4, 2, 16, [150], 40, 2, q_lens=[150])
+    room = torch.zeros(w.q.numel() + 8, dtype=torch.bfloat16, device="cuda")
+    d = w.device()
+    for at in (0, 8):
+        out = room[at:at + w.q.numel()].view(w.q.shape)
+        w.call(pkv, d, out=out)
+        assert_window_close(out, w)
+
+
+def test_more_items_than_sms_and_calls_at_once():
+    """Items claimed from the ticket, on two streams with workspaces of their own."""
+    ws = [Window(16, 2, 16, [260] * 12, 70, 3, q_lens=[256] * 12, seed=i) for i in range(2)]
+    ds = [w.device() for w in ws]
+    streams = [torch.cuda.Stream() for _ in ws]
+    torch.cuda.synchronize()
+    outs = [[w.call(pkv, d, stream=s) for w, d, s in zip(ws, ds, streams)] for _ in range(6)]
+    torch.cuda.synchronize()
+    for pair in outs:
+        for o, first in zip(pair, outs[0]):
+            assert torch.equal(o, first)
+    for o, w, d in zip(outs[0], ws, ds):
+        one = Window(16, 2, 16, [260], 70, 3, q_lens=[256])
+        one.tables, one.k_cache, one.v_cache, one.q = w.tables[5:6], w.k_cache, w.v_cache, w.q[5 * 256:6 * 256]
+        assert_window_close(o[5 * 256:6 * 256], one)
