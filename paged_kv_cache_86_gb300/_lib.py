@@ -939,15 +939,27 @@ def tree_decode(q, key, value, k_cache, v_cache, block_tables, context_lens, cu_
     return out
 
 
-def _refuse_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables, rows=(), **lens):
-    """Raise for the first argument of a call over an fp8 pool with block scales whose type or
-    layout the call's one-expression check has refused."""
-    _rows(**dict(rows))
-    _dense(_U8, 4, k_cache=k_cache, v_cache=v_cache)
-    _dense(_F32, 2, k_scales=k_scales, v_scales=v_scales)
+# The calls below check everything in one expression; where it does not hold, their
+# _refuse says what is wrong. Where the tensors' GPU is current and no stream is named, they
+# launch without _enter: a call on a few sequences is bound by the host.
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _refuse(queries, rows, fp8, k_cache, v_cache, k_scales, v_scales, block_tables, **lens):
+    """Raise for the first argument with a wrong type, layout or pool shape; return if their
+    other shapes or their devices are what was refused."""
+    _dense(_BF16, 3, **queries)
+    _rows(**rows)
+    _dense(_U8 if fp8 else _BF16, 4, k_cache=k_cache, v_cache=v_cache)
+    if fp8:
+        _dense(_F32, 2, k_scales=k_scales, v_scales=v_scales)
     _dense(_I32, 2, block_tables=block_tables)
     _dense(_I32, 1, **lens)
-    raise ValueError("caches must be [NB, bs, Hkv, D], their scales [NB, Hkv]")
+    nb, _, hkv, _ = k_cache.shape
+    if v_cache.shape != k_cache.shape or fp8 and not (k_scales.shape == v_scales.shape
+                                                      == (nb, hkv)):
+        raise ValueError("caches must be [NB, bs, Hkv, D], their scales [NB, Hkv]")
 
 
 def store_kvcache_fp8_block(key, value, k_cache, v_cache, k_scales, v_scales, block_tables,
@@ -958,49 +970,49 @@ def store_kvcache_fp8_block(key, value, k_cache, v_cache, k_scales, v_scales, bl
     cu_seqlens_q[i + 1] - 1 are its last tokens; context_lens[i] counts them. Where a block
     holds older tokens and its scale has to grow, their codes are re-expressed."""
     try:
-        ks, vs, shape = _row_stride(key), _row_stride(value), k_cache.shape
-        fine = (ks >= 0 and vs >= 0 and k_cache.dtype is _U8 and k_cache.is_contiguous()
-                and v_cache.dtype is _U8 and v_cache.is_contiguous() and k_scales.dtype is _F32
-                and k_scales.is_contiguous() and v_scales.dtype is _F32
-                and v_scales.is_contiguous() and block_tables.dtype is _I32
-                and block_tables.is_contiguous() and cu_seqlens_q.dtype is _I32
-                and cu_seqlens_q.is_contiguous() and context_lens.dtype is _I32
-                and context_lens.is_contiguous() and len(shape) == 4 and v_cache.shape == shape
-                and k_scales.shape == (shape[0], shape[2]) and v_scales.shape == k_scales.shape
-                and block_tables.dim() == 2 and cu_seqlens_q.dim() == 1
-                and context_lens.dim() == 1)
-    except AttributeError:
+        nb, bs, hkv, d = k_cache.shape
+        total, heads, dim = key.shape
+        s, mb = block_tables.shape
+        n, = context_lens.shape
+        ends, = cu_seqlens_q.shape
+        ks, vs, index = _row_stride(key), _row_stride(value), key.get_device()
+        fine = (ks >= 0 and vs >= 0 and k_cache.dtype is _U8 and v_cache.dtype is _U8
+                and k_scales.dtype is _F32 and v_scales.dtype is _F32
+                and block_tables.dtype is _I32 and cu_seqlens_q.dtype is _I32
+                and context_lens.dtype is _I32 and k_cache.is_contiguous()
+                and v_cache.is_contiguous() and k_scales.is_contiguous()
+                and v_scales.is_contiguous() and block_tables.is_contiguous()
+                and cu_seqlens_q.is_contiguous() and context_lens.is_contiguous()
+                and v_cache.shape == k_cache.shape and k_scales.shape == v_scales.shape
+                == (nb, hkv) and heads == hkv and dim == d and value.shape == key.shape
+                and n == s and ends == s + 1 and index >= 0 and value.get_device() == index
+                and k_cache.get_device() == index and v_cache.get_device() == index
+                and k_scales.get_device() == index and v_scales.get_device() == index
+                and block_tables.get_device() == index and cu_seqlens_q.get_device() == index
+                and context_lens.get_device() == index)
+    except (AttributeError, ValueError):
         fine = False
     if not fine:
-        _refuse_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables,
-                          dict(key=key, value=value), cu_seqlens_q=cu_seqlens_q,
-                          context_lens=context_lens)
-    nb, bs, hkv, d = shape
-    s, mb = block_tables.shape
-    rows = key.shape
-    total = rows[0]
-    if rows[1] != hkv or rows[2] != d or value.shape != rows:
-        raise ValueError("key / value must be [total_q, Hkv, D]")
-    if cu_seqlens_q.shape[0] != s + 1 or context_lens.shape[0] != s:
-        raise ValueError("metadata shape mismatch")
-    index = key.get_device()
-    if not (index >= 0 and value.get_device() == index and k_cache.get_device() == index
-            and v_cache.get_device() == index and k_scales.get_device() == index
-            and v_scales.get_device() == index and block_tables.get_device() == index
-            and cu_seqlens_q.get_device() == index and context_lens.get_device() == index):
+        _refuse({}, dict(key=key, value=value), True, k_cache, v_cache, k_scales, v_scales,
+                block_tables, cu_seqlens_q=cu_seqlens_q, context_lens=context_lens)
+        if key.shape != (key.shape[0],) + k_cache.shape[2:] or value.shape != key.shape:
+            raise ValueError("key / value must be [total_q, Hkv, D]")
+        if context_lens.shape[0] != s or cu_seqlens_q.shape[0] != s + 1:
+            raise ValueError("metadata shape mismatch")
         _refuse_device(key=key, value=value, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
                        v_scales=v_scales, block_tables=block_tables, cu_seqlens_q=cu_seqlens_q,
                        context_lens=context_lens)
     lib = _lib or load()
-    ctx, st = _enter(index, stream)
-    try:
-        _check(lib.pkv_store_kvcache_fp8_block(
-            key.data_ptr(), value.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(),
-            k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), mb,
-            cu_seqlens_q.data_ptr(), context_lens.data_ptr(), s, total, hkv, d, bs, nb, st),
-            "pkv_store_kvcache_fp8_block")
-    finally:
+    here = stream is None and index == _current_device()
+    ctx, st = (None, _raw_stream(index)) if here else _enter(index, stream)
+    status = lib.pkv_store_kvcache_fp8_block(
+        key.data_ptr(), value.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), mb,
+        cu_seqlens_q.data_ptr(), context_lens.data_ptr(), s, total, hkv, d, bs, nb, st)
+    if ctx is not None:
         _leave(ctx)
+    if status != 0:
+        raise PkvError(status, "pkv_store_kvcache_fp8_block")
 
 
 def load_kvcache_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
@@ -1013,60 +1025,62 @@ def load_kvcache_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables, c
     rows may be strided); a bf16 block pool [NB, bs, Hkv, 128] viewed as rows is one."""
     if (key_out is None) != (value_out is None):
         raise ValueError("key_out and value_out go together")
+    if key_out is None and (num_rows is None or num_rows < 0):
+        raise ValueError("num_rows must be given, and not negative, without key_out / value_out")
     try:
-        shape = k_cache.shape
-        fine = (k_cache.dtype is _U8 and k_cache.is_contiguous() and v_cache.dtype is _U8
-                and v_cache.is_contiguous() and k_scales.dtype is _F32
-                and k_scales.is_contiguous() and v_scales.dtype is _F32
-                and v_scales.is_contiguous() and block_tables.dtype is _I32
-                and block_tables.is_contiguous() and context_lens.dtype is _I32
-                and context_lens.is_contiguous() and row_starts.dtype is _I32
-                and row_starts.is_contiguous() and len(shape) == 4 and v_cache.shape == shape
-                and k_scales.shape == (shape[0], shape[2]) and v_scales.shape == k_scales.shape
-                and block_tables.dim() == 2 and context_lens.dim() == 1 and row_starts.dim() == 1)
-    except AttributeError:
+        nb, bs, hkv, d = k_cache.shape
+        s, mb = block_tables.shape
+        n, = context_lens.shape
+        starts, = row_starts.shape
+        index = k_cache.get_device()
+        fine = (k_cache.dtype is _U8 and v_cache.dtype is _U8 and k_scales.dtype is _F32
+                and v_scales.dtype is _F32 and block_tables.dtype is _I32
+                and context_lens.dtype is _I32 and row_starts.dtype is _I32
+                and k_cache.is_contiguous() and v_cache.is_contiguous()
+                and k_scales.is_contiguous() and v_scales.is_contiguous()
+                and block_tables.is_contiguous() and context_lens.is_contiguous()
+                and row_starts.is_contiguous() and v_cache.shape == k_cache.shape
+                and k_scales.shape == v_scales.shape == (nb, hkv) and n == s and starts == s
+                and key_out is None and index >= 0 and v_cache.get_device() == index
+                and k_scales.get_device() == index and v_scales.get_device() == index
+                and block_tables.get_device() == index and context_lens.get_device() == index
+                and row_starts.get_device() == index)
+    except (AttributeError, ValueError):
         fine = False
     if not fine:
-        _refuse_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables,
-                          context_lens=context_lens, row_starts=row_starts)
-    nb, bs, hkv, d = shape
-    s, mb = block_tables.shape
-    if context_lens.shape[0] != s or row_starts.shape[0] != s:
-        raise ValueError("metadata shape mismatch")
-    if key_out is None:
-        if num_rows is None or num_rows < 0:
-            raise ValueError("num_rows must be given, and not negative, without key_out / value_out")
-        ks = vs = hkv * d
-    else:
-        _rows(key_out=key_out, value_out=value_out)
-        ks, vs = _row_stride(key_out), _row_stride(value_out)
-        if num_rows is None:
-            num_rows = key_out.shape[0]
-        if key_out.shape != (num_rows, hkv, d) or value_out.shape != key_out.shape:
-            raise ValueError("key_out / value_out must be [num_rows, Hkv, D]")
-    index = k_cache.get_device()
-    if not (index >= 0 and v_cache.get_device() == index and k_scales.get_device() == index
-            and v_scales.get_device() == index and block_tables.get_device() == index
-            and context_lens.get_device() == index and row_starts.get_device() == index):
-        _refuse_device(k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
-                       block_tables=block_tables, context_lens=context_lens,
-                       row_starts=row_starts)
-    if key_out is not None and not (key_out.get_device() == index
-                                    and value_out.get_device() == index):
-        _refuse_device(k_cache=k_cache, key_out=key_out, value_out=value_out)
+        _refuse({}, {}, True, k_cache, v_cache, k_scales, v_scales, block_tables,
+                context_lens=context_lens, row_starts=row_starts)
+        if context_lens.shape[0] != s or row_starts.shape[0] != s:
+            raise ValueError("metadata shape mismatch")
+        named = dict(k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
+                     block_tables=block_tables, context_lens=context_lens, row_starts=row_starts)
+        if key_out is not None:
+            named.update(key_out=key_out, value_out=value_out)
+            _rows(key_out=key_out, value_out=value_out)
+            if num_rows is None:
+                num_rows = key_out.shape[0]
+            if key_out.shape != (num_rows, hkv, d) or value_out.shape != key_out.shape:
+                raise ValueError("key_out / value_out must be [num_rows, Hkv, D]")
+        if any(t.get_device() != index or index < 0 for t in named.values()):
+            _refuse_device(**named)
     lib = _lib or load()
-    ctx, st = _enter(index, stream)
+    here = stream is None and index == _current_device()
+    ctx, st = (None, _raw_stream(index)) if here else _enter(index, stream)
     try:
         if key_out is None:
+            ks = vs = hkv * d
             key_out = torch.empty((num_rows, hkv, d), dtype=_BF16, device=k_cache.device)
-            value_out = torch.empty((num_rows, hkv, d), dtype=_BF16, device=k_cache.device)
+            value_out = torch.empty_like(key_out)
+        else:
+            ks, vs = _row_stride(key_out), _row_stride(value_out)
         _check(lib.pkv_load_kvcache_fp8_block(
             key_out.data_ptr(), value_out.data_ptr(), ks, vs, k_cache.data_ptr(),
             v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
             mb, context_lens.data_ptr(), row_starts.data_ptr(), s, num_rows, hkv, d, bs, nb, st),
             "pkv_load_kvcache_fp8_block")
     finally:
-        _leave(ctx)
+        if ctx is not None:
+            _leave(ctx)
     return key_out, value_out
 
 
@@ -1077,9 +1091,9 @@ def decode_window_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: 
 
 
 @functools.lru_cache(maxsize=256)
-def _decode_window_workspace(index: int, s: int, hq: int, hkv: int, d: int) -> int:
-    """The size on device `index`, the current one; at least 256."""
-    return max(load().pkv_decode_window_workspace_size(s, hq, hkv, d), 256)
+def _decode_window_workspace(index: int, hq: int, hkv: int, d: int) -> int:
+    """The size on device `index`, the current one, for any number of sequences; at least 256."""
+    return max(load().pkv_decode_window_workspace_size(0, hq, hkv, d), 256)
 
 
 def _workspace_for(workspace, need: int, q):
@@ -1099,38 +1113,37 @@ def paged_decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables
     query row q [S, Hq, 128] per sequence. window 0: over the whole context; otherwise over
     the last `window` tokens and the first `sinks`. Returns out [S, Hq, 128] bf16."""
     try:
-        shape = k_cache.shape
-        fine = (q.dtype is _BF16 and q.is_contiguous() and k_cache.dtype is _U8
-                and k_cache.is_contiguous() and v_cache.dtype is _U8 and v_cache.is_contiguous()
-                and k_scales.dtype is _F32 and k_scales.is_contiguous()
-                and v_scales.dtype is _F32 and v_scales.is_contiguous()
-                and block_tables.dtype is _I32 and block_tables.is_contiguous()
-                and context_lens.dtype is _I32 and context_lens.is_contiguous()
-                and len(shape) == 4 and v_cache.shape == shape
-                and k_scales.shape == (shape[0], shape[2]) and v_scales.shape == k_scales.shape
-                and q.dim() == 3 and block_tables.dim() == 2 and context_lens.dim() == 1)
-    except AttributeError:
+        nb, bs, hkv, d = k_cache.shape
+        s, hq, dim = q.shape
+        tables, mb = block_tables.shape
+        n, = context_lens.shape
+        index = q.get_device()
+        fine = (q.dtype is _BF16 and k_cache.dtype is _U8 and v_cache.dtype is _U8
+                and k_scales.dtype is _F32 and v_scales.dtype is _F32
+                and block_tables.dtype is _I32 and context_lens.dtype is _I32
+                and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+                and k_scales.is_contiguous() and v_scales.is_contiguous()
+                and block_tables.is_contiguous() and context_lens.is_contiguous()
+                and v_cache.shape == k_cache.shape and k_scales.shape == v_scales.shape
+                == (nb, hkv) and dim == d and tables == s and n == s and index >= 0
+                and k_cache.get_device() == index and v_cache.get_device() == index
+                and k_scales.get_device() == index and v_scales.get_device() == index
+                and block_tables.get_device() == index and context_lens.get_device() == index)
+    except (AttributeError, ValueError):
         fine = False
     if not fine:
-        _dense(_BF16, 3, q=q)
-        _refuse_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables,
-                          context_lens=context_lens)
-    nb, bs, hkv, d = shape
-    s, hq, dq = q.shape
-    tables, mb = block_tables.shape
-    if dq != d or tables != s or context_lens.shape[0] != s:
-        raise ValueError("q / cache / metadata shape mismatch")
-    index = q.get_device()
-    if not (index >= 0 and k_cache.get_device() == index and v_cache.get_device() == index
-            and k_scales.get_device() == index and v_scales.get_device() == index
-            and block_tables.get_device() == index and context_lens.get_device() == index):
+        _refuse(dict(q=q), {}, True, k_cache, v_cache, k_scales, v_scales, block_tables,
+                context_lens=context_lens)
+        if dim != d or tables != s or n != s:
+            raise ValueError("q / cache / metadata shape mismatch")
         _refuse_device(q=q, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
                        v_scales=v_scales, block_tables=block_tables, context_lens=context_lens)
     lib = _lib or load()
-    ctx, st = _enter(index, stream)
+    here = stream is None and index == _current_device()
+    ctx, st = (None, _raw_stream(index)) if here else _enter(index, stream)
     try:
-        out = _out_like(out, q) if out is not None else torch.empty_like(q)
-        workspace = _workspace_for(workspace, _decode_window_workspace(index, s, hq, hkv, d), q)
+        out = torch.empty_like(q) if out is None else _out_like(out, q)
+        workspace = _workspace_for(workspace, _decode_window_workspace(index, hq, hkv, d), q)
         _check(lib.pkv_paged_decode_fp8_block(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), mb,
@@ -1139,7 +1152,8 @@ def paged_decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables
             workspace.data_ptr(), workspace.numel() * workspace.element_size(), st),
             "pkv_paged_decode_fp8_block")
     finally:
-        _leave(ctx)
+        if ctx is not None:
+            _leave(ctx)
     return out
 
 
@@ -1150,35 +1164,33 @@ def paged_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale: 
     in bf16 caches [NB, bs, Hkv, 128], one query row q [S, Hq, 128] per sequence. Returns out
     [S, Hq, 128] bf16."""
     try:
-        shape = k_cache.shape
-        fine = (q.dtype is _BF16 and q.is_contiguous() and k_cache.dtype is _BF16
-                and k_cache.is_contiguous() and v_cache.dtype is _BF16
-                and v_cache.is_contiguous() and block_tables.dtype is _I32
-                and block_tables.is_contiguous() and context_lens.dtype is _I32
-                and context_lens.is_contiguous() and len(shape) == 4 and q.dim() == 3
-                and v_cache.dim() == 4 and block_tables.dim() == 2 and context_lens.dim() == 1)
-    except AttributeError:
+        nb, bs, hkv, d = k_cache.shape
+        s, hq, dim = q.shape
+        tables, mb = block_tables.shape
+        n, = context_lens.shape
+        index = q.get_device()
+        fine = (q.dtype is _BF16 and k_cache.dtype is _BF16 and v_cache.dtype is _BF16
+                and block_tables.dtype is _I32 and context_lens.dtype is _I32
+                and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+                and block_tables.is_contiguous() and context_lens.is_contiguous()
+                and v_cache.shape == k_cache.shape and dim == d and tables == s and n == s
+                and index >= 0 and k_cache.get_device() == index and v_cache.get_device() == index
+                and block_tables.get_device() == index and context_lens.get_device() == index)
+    except (AttributeError, ValueError):
         fine = False
     if not fine:
-        _dense(_BF16, 3, q=q)
-        _dense(_BF16, 4, k_cache=k_cache, v_cache=v_cache)
-        _dense(_I32, 2, block_tables=block_tables)
-        _dense(_I32, 1, context_lens=context_lens)
-    nb, bs, hkv, d = shape
-    s, hq, dq = q.shape
-    tables, mb = block_tables.shape
-    if dq != d or v_cache.shape != shape or tables != s or context_lens.shape[0] != s:
-        raise ValueError("q / cache / metadata shape mismatch")
-    index = q.get_device()
-    if not (index >= 0 and k_cache.get_device() == index and v_cache.get_device() == index
-            and block_tables.get_device() == index and context_lens.get_device() == index):
+        _refuse(dict(q=q), {}, False, k_cache, v_cache, None, None, block_tables,
+                context_lens=context_lens)
+        if dim != d or tables != s or n != s:
+            raise ValueError("q / cache / metadata shape mismatch")
         _refuse_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
                        context_lens=context_lens)
     lib = _lib or load()
-    ctx, st = _enter(index, stream)
+    here = stream is None and index == _current_device()
+    ctx, st = (None, _raw_stream(index)) if here else _enter(index, stream)
     try:
-        out = _out_like(out, q) if out is not None else torch.empty_like(q)
-        workspace = _workspace_for(workspace, _decode_window_workspace(index, s, hq, hkv, d), q)
+        out = torch.empty_like(q) if out is None else _out_like(out, q)
+        workspace = _workspace_for(workspace, _decode_window_workspace(index, hq, hkv, d), q)
         _check(lib.pkv_paged_decode_window(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_tables.data_ptr(), mb, context_lens.data_ptr(), s,
@@ -1187,7 +1199,8 @@ def paged_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale: 
             workspace.numel() * workspace.element_size(), PKV_BF16, st),
             "pkv_paged_decode_window")
     finally:
-        _leave(ctx)
+        if ctx is not None:
+            _leave(ctx)
     return out
 
 
@@ -1198,48 +1211,46 @@ def paged_prefill_window(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_
     with p < sinks or p > t - window; otherwise as paged_prefill. Returns out
     [total_q, Hq, 128] bf16; rows behind cu_seqlens_q[-1] are not written."""
     try:
-        shape = k_cache.shape
-        fine = (q.dtype is _BF16 and q.is_contiguous() and k_cache.dtype is _BF16
-                and k_cache.is_contiguous() and v_cache.dtype is _BF16
-                and v_cache.is_contiguous() and block_tables.dtype is _I32
-                and block_tables.is_contiguous() and cu_seqlens_q.dtype is _I32
-                and cu_seqlens_q.is_contiguous() and cu_seqlens_k.dtype is _I32
-                and cu_seqlens_k.is_contiguous() and len(shape) == 4 and q.dim() == 3
-                and v_cache.dim() == 4 and block_tables.dim() == 2 and cu_seqlens_q.dim() == 1
-                and cu_seqlens_k.dim() == 1)
-    except AttributeError:
+        nb, bs, hkv, d = k_cache.shape
+        total, hq, dim = q.shape
+        s, mb = block_tables.shape
+        ends, = cu_seqlens_q.shape
+        k_ends, = cu_seqlens_k.shape
+        index = q.get_device()
+        fine = (q.dtype is _BF16 and k_cache.dtype is _BF16 and v_cache.dtype is _BF16
+                and block_tables.dtype is _I32 and cu_seqlens_q.dtype is _I32
+                and cu_seqlens_k.dtype is _I32 and q.is_contiguous() and k_cache.is_contiguous()
+                and v_cache.is_contiguous() and block_tables.is_contiguous()
+                and cu_seqlens_q.is_contiguous() and cu_seqlens_k.is_contiguous()
+                and v_cache.shape == k_cache.shape and dim == d and ends == s + 1
+                and k_ends == s + 1 and index >= 0 and k_cache.get_device() == index
+                and v_cache.get_device() == index and block_tables.get_device() == index
+                and cu_seqlens_q.get_device() == index and cu_seqlens_k.get_device() == index)
+    except (AttributeError, ValueError):
         fine = False
     if not fine:
-        _dense(_BF16, 3, q=q)
-        _dense(_BF16, 4, k_cache=k_cache, v_cache=v_cache)
-        _dense(_I32, 2, block_tables=block_tables)
-        _dense(_I32, 1, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
-    nb, bs, hkv, d = shape
-    total, hq, dq = q.shape
-    s, mb = block_tables.shape
-    if (dq != d or v_cache.shape != shape or cu_seqlens_q.shape[0] != s + 1
-            or cu_seqlens_k.shape[0] != s + 1):
-        raise ValueError("q / cache / metadata shape mismatch")
-    index = q.get_device()
-    if not (index >= 0 and k_cache.get_device() == index and v_cache.get_device() == index
-            and block_tables.get_device() == index and cu_seqlens_q.get_device() == index
-            and cu_seqlens_k.get_device() == index):
+        _refuse(dict(q=q), {}, False, k_cache, v_cache, None, None, block_tables,
+                cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
+        if dim != d or ends != s + 1 or k_ends != s + 1:
+            raise ValueError("q / cache / metadata shape mismatch")
         _refuse_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
                        cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k)
     lib = _lib or load()
-    ctx, st = _enter(index, stream)
+    here = stream is None and index == _current_device()
+    ctx, st = (None, _raw_stream(index)) if here else _enter(index, stream)
     try:
-        out = _out_like(out, q) if out is not None else torch.empty_like(q)
+        out = torch.empty_like(q) if out is None else _out_like(out, q)
         workspace = _workspace_for(workspace, 256, q)
         _check(lib.pkv_paged_prefill_window(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), max_seqlen_q, max_seqlen_k,
             block_tables.data_ptr(), mb, s, total, min(window, _MAX_I32), min(sinks, _MAX_I32),
-            hq, hkv, d, bs, nb, scale,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), PKV_BF16, st),
+            hq, hkv, d, bs, nb, scale, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), PKV_BF16, st),
             "pkv_paged_prefill_window")
     finally:
-        _leave(ctx)
+        if ctx is not None:
+            _leave(ctx)
     return out
 
 
