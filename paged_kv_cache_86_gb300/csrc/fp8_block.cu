@@ -16,6 +16,15 @@
 // maximum of the new rows, the scale, the codes, and, where the block holds older
 // rows and the scale has to grow, those rows' codes in the new scale. No atomics,
 // and no order between teams matters.
+//
+// What bounds them: the store reads 2 and writes 1 byte a value. 16384 tokens of 32
+// prompts (8 KV heads, block 16) take 20.5 us, 4.9 TB/s, 0.72 of the measured copy
+// rate: a third of the time is the chain lengths -> table -> rows of each of its 3.4
+// waves of CTAs, the rest is shared by loads and the arithmetic of the codes (issue
+// slots 0.66 busy). 64 registers for four CTAs an SM; three took 22.0 us, five (with
+// spills) 25.8; 4 or 16 rows a half-warp instead of 8 26.0 and 28.0; one wave of CTAs
+// with several blocks each 22.7. 512 tokens of 512 sequences: 6 us, the chain alone.
+// The read-back: 0.44 M tokens (8 KV heads) 284 us, 6.35 TB/s, 0.93 of the copy rate.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
