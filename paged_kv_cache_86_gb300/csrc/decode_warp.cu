@@ -23,9 +23,12 @@
 // producer warp copies tiles of all KV heads, which are contiguous in the cache, by
 // TMA into a ring that fills the SM's shared memory (decode_ring_kernel). Others:
 // every warp loads its rows straight into the registers that the MMAs take them
-// from (decode_direct_kernel), whose 128- or 256-byte pieces, read at eight
-// different times, DRAM serves at half the rate: 512 sequences (fp8, 0.59 M tokens)
-// 413 us against 220, behind a window of 1024 (bf16) 422 against 268.
+// from (decode_direct_kernel). Its pieces of 128 or 256 bytes, read at eight different
+// times, DRAM served at 0.45 of its rate; asked for in L2 together, a tile ahead, at
+// 0.6 to 0.7. 512 sequences (fp8, 0.59 M tokens): 206 us at block 16, 315 at block 6;
+// behind a window of 1024 (bf16) 248 and 345. At 0.89 and 0.97 of the copy rate, merge
+// included, the rings are bound by HBM; 3 sequences take 13 us, two launches of
+// dependent loads, and 17 with direct loads.
 //
 // Split: the seen tokens of all sequences, in tiles of 16 with kSegTiles of
 // overhead in front of each sequence, are one line that is cut into equal ranges;

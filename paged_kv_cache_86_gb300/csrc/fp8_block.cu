@@ -24,7 +24,7 @@
 // slots 0.66 busy). 64 registers for four CTAs an SM; three took 22.0 us, five (with
 // spills) 25.8; 4 or 16 rows a half-warp instead of 8 26.0 and 28.0; one wave of CTAs
 // with several blocks each 22.7. 512 tokens of 512 sequences: 6 us, the chain alone.
-// The read-back: 0.44 M tokens (8 KV heads) 284 us, 6.35 TB/s, 0.93 of the copy rate.
+// The read-back: 0.29 M tokens (8 KV heads) 284 us, 6.35 TB/s, 0.93 of the copy rate.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
