@@ -55,11 +55,9 @@ constexpr int kSegTiles = 2;               // what starting a sequence costs, in
 constexpr int kMinTiles = 4;               // shortest range
 constexpr int kDirectWarps = 8;            // warps of a CTA, direct loads
 // Warps of a CTA with rings, producers included, and so the registers of a thread
-// (168, 204). With 18 (96 registers, spills; two rings for 8 KV heads instead of
-// one) 512 sequences took 263 us (fp8) and 274 us (bf16, window of 1024), with 12
-// 220 and 268.
-constexpr int kNarrowWarps = 12;           // one tile of 8 query heads a warp
-constexpr int kWideWarps = 10;             // two
+// (168). With 18 (96 registers, spills; two rings for 8 KV heads instead of one) 512
+// sequences took 263 us (fp8) and 274 us (bf16, window of 1024), with 12 220 and 268.
+constexpr int kRingWarps = 12;
 constexpr int kCombineWarps = 8;
 constexpr int kRingBytes = 220 * 1024;     // of all stages of a CTA
 constexpr int kMaxStages = 16;             // of one ring
@@ -70,7 +68,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;
 constexpr float kLift = 7.f;
 
-// n / d for 0 <= n < 2^31 by a multiplication
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, "Division by
+// Invariant Integers using Multiplication")
 struct FastDiv {
   uint32_t mul, shift, d;
 };
@@ -163,7 +162,6 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
 
 // The operands of the two products, as a lane of mma.m16n8k16 holds them: fragment
 // row (column of B) g = lane / 4, pair kp = lane % 4. The 128 dims of S's
@@ -459,13 +457,15 @@ __device__ __forceinline__ Seen seen_of(const WarpParams &p, int i, int unit, bo
 __device__ __forceinline__ int tiles_of(const Seen &s, int unit) { return (s.units * unit + kTok - 1) / kTok; }
 __device__ __forceinline__ int cost_of(const Seen &s, int unit) { return s.units > 0 ? tiles_of(s, unit) + kSegTiles : 0; }
 
-// Where the CTA's ranges start on the line of all sequences. Walker w of the CTA
-// (w < walkers) takes range first_range(w).
 struct Plan {
-  int range_len, total;
+  int range_len, total;   // tiles of a range, of the line
 };
 
-template <int kMaxWalkers, typename F>
+// Where the CTA's ranges start on the line of all sequences: walker w of the CTA
+// (w < walkers) takes range range_of(w); its first sequence goes to seq_of[w] (num_seqs:
+// none) and that one's start on the line to pos_of[w]. The whole CTA calls it.
+
+template <typename F>
 __device__ __forceinline__ Plan plan_ranges(const WarpParams &p, int unit, int walkers, int *part, int *seq_of,
                                             int *pos_of, F range_of) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -576,7 +576,7 @@ decode_direct_kernel(const WarpParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int vheads = p.num_kv_heads * p.chunks;
   auto range_of = [&](int w) { return (static_cast<int>(blockIdx.x) * kDirectWarps + w) / vheads; };
-  const Plan plan = plan_ranges<kDirectWarps>(p, 1, kDirectWarps, s_part, s_seq, s_pos, range_of);
+  const Plan plan = plan_ranges(p, 1, kDirectWarps, s_part, s_seq, s_pos, range_of);
   const int range = range_of(warp), vh = (blockIdx.x * kDirectWarps + warp) % vheads;
   const int kvh = vh / p.chunks, head0 = vh % p.chunks * p.per_chunk;
   const int heads = min(p.per_chunk, p.group - head0);       // of this warp
@@ -706,15 +706,15 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const v
 // rows each out of shared memory. A box lands as [head][token][128 bytes] (bf16: two
 // such halves of 64 dims), swizzled by the token, which makes every 16-byte load
 // below free of bank conflicts.
-template <bool kFp8, int NT, int kMaxWarps>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1)
+template <bool kFp8, int NT>
+__global__ void __launch_bounds__(kRingWarps * 32, 1)
 decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const WarpParams p) {
   using H = Heads<kFp8, NT>;
   constexpr int kHalves = kFp8 ? 1 : 2;       // 128-byte pieces of a head's row
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_part[kMaxWarps], s_seq[kMaxWarps], s_pos[kMaxWarps];
-  __shared__ uint64_t s_bar[2 * kMaxStages * kMaxWarps / 2];
+  __shared__ int s_part[kRingWarps], s_seq[kRingWarps], s_pos[kRingWarps];
+  __shared__ uint64_t s_bar[2 * kMaxStages * (kRingWarps / 2)];   // full, empty; a ring has two warps at least
   __shared__ int s_abort;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -742,7 +742,7 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   // ring r of CTA b: range (b / groups) * rings + r of head group b % groups
   const int hg = blockIdx.x % p.head_groups;
   auto range_of = [&](int r) { return static_cast<int>(blockIdx.x) / p.head_groups * p.rings + r; };
-  const Plan plan = plan_ranges<kMaxWarps>(p, p.unit, p.rings, s_part, s_seq, s_pos, range_of);
+  const Plan plan = plan_ranges(p, p.unit, p.rings, s_part, s_seq, s_pos, range_of);
   const int range = range_of(ring);
   const int bytes = stage_bytes(kFp8, hc);
   const uint32_t ring_base = base + ring * stages * bytes;
@@ -997,21 +997,23 @@ bool shape_of(int num_q_heads, int num_kv_heads, int block_size, bool fp8, Shape
   const int sms = sm_count(dev);
   if (sms <= 0) return false;
   const int group = num_q_heads / num_kv_heads;
-  s->wide = group > 8;
+  // fp8 with one or two KV heads: warps of 8 query heads each instead of 16 (512
+  // sequences, groups of 16: 62 us against 79 with one KV head, 106 against 122 with
+  // two, but 197 against 166 with four and 374 against 301 with eight)
+  s->wide = group > 8 && !(fp8 && num_kv_heads <= 2);
   const int most = s->wide ? 16 : 8;
   s->chunks = (group + most - 1) / most;
   s->per_chunk = (group + s->chunks - 1) / s->chunks;
   const int vheads = num_kv_heads * s->chunks;
-  const int most_warps = s->wide ? kWideWarps : kNarrowWarps;
-  s->ring = block_size % 8 == 0 && s->chunks < most_warps;
+  s->ring = block_size % 8 == 0 && s->chunks < kRingWarps;
   if (s->ring) {
     s->unit = block_size % 16 == 0 ? 16 : 8;
-    int heads = (most_warps - 1) / s->chunks;                  // a warp per (head, chunk) and a producer
+    int heads = (kRingWarps - 1) / s->chunks;                  // a warp per (head, chunk) and a producer
     if (heads > 8) heads = 8;
     s->head_groups = (num_kv_heads + heads - 1) / heads;
     s->heads_per_cta = (num_kv_heads + s->head_groups - 1) / s->head_groups;
     const int bytes = stage_bytes(fp8, s->heads_per_cta), ring_warps = s->heads_per_cta * s->chunks;
-    s->rings = most_warps / (ring_warps + 1);
+    s->rings = kRingWarps / (ring_warps + 1);
     while (s->rings > 1 && kRingBytes / (s->rings * bytes) < 3) --s->rings;
     s->stages = kRingBytes / (s->rings * bytes);
     if (s->stages > kMaxStages) s->stages = kMaxStages;
@@ -1168,8 +1170,8 @@ cudaError_t launch_decode_warp(const DecodeWarpArgs &a, cudaStream_t stream) {
     if (!cache_map(&tk, a.k_cache, rows, a.num_kv_heads, fp8, s.unit, s.heads_per_cta) ||
         !cache_map(&tv, a.v_cache, rows, a.num_kv_heads, fp8, s.unit, s.heads_per_cta))
       return cudaErrorInvalidValue;
-    RingKernel kern = fp8 ? (s.wide ? decode_ring_kernel<true, 2, kWideWarps> : decode_ring_kernel<true, 1, kNarrowWarps>)
-                          : (s.wide ? decode_ring_kernel<false, 2, kWideWarps> : decode_ring_kernel<false, 1, kNarrowWarps>);
+    RingKernel kern = fp8 ? (s.wide ? decode_ring_kernel<true, 2> : decode_ring_kernel<true, 1>)
+                          : (s.wide ? decode_ring_kernel<false, 2> : decode_ring_kernel<false, 1>);
     if (cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), (fp8 ? 1 : 0) + (s.wide ? 2 : 0), kRingBytes + 1024))
       return e;
     const int smem = s.rings * s.stages * stage_bytes(fp8, s.heads_per_cta) + 1024;
