@@ -503,7 +503,9 @@ pkv_status pkv_load_kvcache_fp8_block(void *key_out, void *value_out,
  * max_seqlen_k and num_blocks * block_size at most 2^31 - 512, and out and q
  * must not overlap. Keys and values that a row does not see never change it,
  * whatever they hold: rows whose sums come out not finite are computed a second
- * time from their seen keys alone (slower).
+ * time from their seen keys alone. That is slower (a warp takes 0.02 ms a row and
+ * thousand keys), and where such rows see millions of keys each, a wait on the chip
+ * can run out (PKV_DEVERR_TIMEOUT).
  */
 size_t pkv_decode_window_workspace_size(int32_t num_seqs, int32_t num_q_heads,
                                         int32_t num_kv_heads, int32_t head_dim);

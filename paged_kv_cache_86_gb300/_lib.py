@@ -1096,13 +1096,10 @@ def _decode_window_workspace(index: int, hq: int, hkv: int, d: int) -> int:
     return max(load().pkv_decode_window_workspace_size(0, hq, hkv, d), 256)
 
 
-def _workspace_for(workspace, need: int, q):
-    """The caller's workspace (checked) or a new one of `need` bytes."""
-    if workspace is None:
-        return torch.empty(need, dtype=_U8, device=q.device)
+def _need_workspace(workspace, q):
+    """The caller's workspace is dense and on q's device."""
     if workspace.get_device() != q.get_device() or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on q's device")
-    return workspace
 
 
 def paged_decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
@@ -1143,14 +1140,19 @@ def paged_decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables
     ctx, st = (None, _raw_stream(index)) if here else _enter(index, stream)
     try:
         out = torch.empty_like(q) if out is None else _out_like(out, q)
-        workspace = _workspace_for(workspace, _decode_window_workspace(index, hq, hkv, d), q)
-        _check(lib.pkv_paged_decode_fp8_block(
+        if workspace is None:
+            workspace = torch.empty(_decode_window_workspace(index, hq, hkv, d), dtype=_U8,
+                                    device=q.device)
+        else:
+            _need_workspace(workspace, q)
+        status = lib.pkv_paged_decode_fp8_block(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), mb,
             context_lens.data_ptr(), s, mb * bs if max_context_len is None else max_context_len,
-            min(window, _MAX_I32), min(sinks, _MAX_I32), hq, hkv, d, bs, nb, scale,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), st),
-            "pkv_paged_decode_fp8_block")
+            window if window < _MAX_I32 else _MAX_I32, sinks if sinks < _MAX_I32 else _MAX_I32,
+            hq, hkv, d, bs, nb, scale, workspace.data_ptr(), workspace.nbytes, st)
+        if status != 0:
+            raise PkvError(status, "pkv_paged_decode_fp8_block")
     finally:
         if ctx is not None:
             _leave(ctx)
@@ -1190,14 +1192,19 @@ def paged_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale: 
     ctx, st = (None, _raw_stream(index)) if here else _enter(index, stream)
     try:
         out = torch.empty_like(q) if out is None else _out_like(out, q)
-        workspace = _workspace_for(workspace, _decode_window_workspace(index, hq, hkv, d), q)
-        _check(lib.pkv_paged_decode_window(
+        if workspace is None:
+            workspace = torch.empty(_decode_window_workspace(index, hq, hkv, d), dtype=_U8,
+                                    device=q.device)
+        else:
+            _need_workspace(workspace, q)
+        status = lib.pkv_paged_decode_window(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_tables.data_ptr(), mb, context_lens.data_ptr(), s,
-            mb * bs if max_context_len is None else max_context_len, min(window, _MAX_I32),
-            min(sinks, _MAX_I32), hq, hkv, d, bs, nb, scale, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), PKV_BF16, st),
-            "pkv_paged_decode_window")
+            mb * bs if max_context_len is None else max_context_len,
+            window if window < _MAX_I32 else _MAX_I32, sinks if sinks < _MAX_I32 else _MAX_I32,
+            hq, hkv, d, bs, nb, scale, workspace.data_ptr(), workspace.nbytes, PKV_BF16, st)
+        if status != 0:
+            raise PkvError(status, "pkv_paged_decode_window")
     finally:
         if ctx is not None:
             _leave(ctx)
@@ -1240,14 +1247,18 @@ def paged_prefill_window(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_
     ctx, st = (None, _raw_stream(index)) if here else _enter(index, stream)
     try:
         out = torch.empty_like(q) if out is None else _out_like(out, q)
-        workspace = _workspace_for(workspace, 256, q)
-        _check(lib.pkv_paged_prefill_window(
+        if workspace is None:
+            workspace = torch.empty(256, dtype=_U8, device=q.device)
+        else:
+            _need_workspace(workspace, q)
+        status = lib.pkv_paged_prefill_window(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), max_seqlen_q, max_seqlen_k,
-            block_tables.data_ptr(), mb, s, total, min(window, _MAX_I32), min(sinks, _MAX_I32),
-            hq, hkv, d, bs, nb, scale, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), PKV_BF16, st),
-            "pkv_paged_prefill_window")
+            block_tables.data_ptr(), mb, s, total, window if window < _MAX_I32 else _MAX_I32,
+            sinks if sinks < _MAX_I32 else _MAX_I32, hq, hkv, d, bs, nb, scale,
+            workspace.data_ptr(), workspace.nbytes, PKV_BF16, st)
+        if status != 0:
+            raise PkvError(status, "pkv_paged_prefill_window")
     finally:
         if ctx is not None:
             _leave(ctx)
