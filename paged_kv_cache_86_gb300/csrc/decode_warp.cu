@@ -752,7 +752,14 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
   const uint32_t upper = p.unit == 16 ? 1024u : v_off / 2;
   const uint32_t upper_dims = p.unit == 16 ? half_dims : half_dims / 2;   // dims halves of one box
   Walk walk(plan, range, s_seq[ring], s_pos[ring]);
-  int it = 0;                                                 // tiles through the ring so far
+  int s = 0;                                                  // the ring's next stage,
+  uint32_t phase = 0;                                         // and the parity of its turn
+  auto advance = [&]() {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  };
   bool ok = true;
 
   if (warp >= consumers) {
@@ -760,6 +767,7 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const bool tells = lane == 0 && hg == 0;
     if (tells) walk.begin(p, range, p.unit);
     const int per_tile = kTok / p.unit, batch = 32 / per_tile;  // units of a tile, tiles of a batch
+    int issued = 0;
     const int oob_row = p.num_blocks * static_cast<int>(p.bs.d);
     while (ok && walk.next(p, p.unit)) {
       if (tells) walk.entry(p, range);
@@ -777,11 +785,11 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
           else raise_error(p.err, PKV_DEVERR_BLOCK_ID);
         }
         const int n = min(batch, walk.t1 - tb);
-        for (int j = 0; j < n; ++j, ++it) {
-          const int s = it % stages, round = it / stages;
+        for (int j = 0; j < n; ++j) {
           int good = 1;
           if (lane == 0) {
-            if (round > 0 && !mbar_wait(empty(s), (round - 1) & 1, abort)) {
+            // (the turn before an unused barrier's first one counts as done)
+            if (!mbar_wait(empty(s), phase ^ 1, abort)) {
               good = 0;
               *abort = 1;
               raise_error(p.err, PKV_DEVERR_TIMEOUT);
@@ -798,12 +806,14 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             const uint32_t dst = ring_base + s * bytes + is_v * v_off + unit * (v_off / per_tile) + half * upper_dims;
             tma_load_3d(dst, is_v ? &tm_v : &tm_k, half * 64, r, hg * hc, full(s));
           }
+          ++issued;
+          advance();
         }
       }
     }
     // every copy lands before the CTA may exit
     if (lane == 0)
-      for (int j = max(0, it - stages); j < it; ++j) mbar_wait(full(j % stages), (j / stages) & 1, nullptr);
+      for (int j = max(0, issued - stages); j < issued; ++j) mbar_wait(full(j % stages), (j / stages) & 1, nullptr);
   } else {
     // ------------------------------------------------------------ consumers
     zero_rows(p, consumers * 32);
@@ -842,9 +852,8 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if (lane & 1) sc = lg2(sc);
       }
 #pragma unroll 1
-      for (int t = walk.t0; t < walk.t1; ++t, ++it) {
-        const int s = it % stages;
-        if (!warp_wait(full(s), (it / stages) & 1, abort)) {
+      for (int t = walk.t0; t < walk.t1; ++t) {
+        if (!warp_wait(full(s), phase, abort)) {
           ok = false;
           *abort = 1;
           raise_error(p.err, PKV_DEVERR_TIMEOUT);
@@ -894,6 +903,7 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         x.accumulate(v, pb);
         __syncwarp();
         if (lane == 0) mbar_arrive(empty(s));
+        advance();
       }
       if (!ok) break;
       const int64_t rec = (static_cast<int64_t>(range * 2 + (walk.t0 == 0 ? 1 : 0)) * vheads + vh) * p.per_chunk;
