@@ -1041,7 +1041,7 @@ def load_kvcache_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables, c
                 and block_tables.is_contiguous() and context_lens.is_contiguous()
                 and row_starts.is_contiguous() and v_cache.shape == k_cache.shape
                 and k_scales.shape == v_scales.shape == (nb, hkv) and n == s and starts == s
-                and key_out is None and index >= 0 and v_cache.get_device() == index
+                and index >= 0 and v_cache.get_device() == index
                 and k_scales.get_device() == index and v_scales.get_device() == index
                 and block_tables.get_device() == index and context_lens.get_device() == index
                 and row_starts.get_device() == index)
@@ -1052,17 +1052,22 @@ def load_kvcache_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables, c
                 context_lens=context_lens, row_starts=row_starts)
         if context_lens.shape[0] != s or row_starts.shape[0] != s:
             raise ValueError("metadata shape mismatch")
-        named = dict(k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
-                     block_tables=block_tables, context_lens=context_lens, row_starts=row_starts)
-        if key_out is not None:
-            named.update(key_out=key_out, value_out=value_out)
+    if key_out is not None:
+        if not (isinstance(key_out, torch.Tensor) and isinstance(value_out, torch.Tensor)):
+            raise TypeError("key_out and value_out must be torch tensors")
+        ks, vs = _row_stride(key_out), _row_stride(value_out)
+        if ks < 0 or vs < 0:
             _rows(key_out=key_out, value_out=value_out)
-            if num_rows is None:
-                num_rows = key_out.shape[0]
-            if key_out.shape != (num_rows, hkv, d) or value_out.shape != key_out.shape:
-                raise ValueError("key_out / value_out must be [num_rows, Hkv, D]")
-        if any(t.get_device() != index or index < 0 for t in named.values()):
-            _refuse_device(**named)
+        if num_rows is None:
+            num_rows = key_out.shape[0]
+        if key_out.shape != (num_rows, hkv, d) or value_out.shape != key_out.shape:
+            raise ValueError("key_out / value_out must be [num_rows, Hkv, D]")
+    if not fine:
+        _refuse_device(k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
+                       block_tables=block_tables, context_lens=context_lens,
+                       row_starts=row_starts)
+    if key_out is not None and not key_out.get_device() == value_out.get_device() == index:
+        _refuse_device(k_cache=k_cache, key_out=key_out, value_out=value_out)
     lib = _lib or load()
     here = stream is None and index == _current_device()
     ctx, st = (None, _raw_stream(index)) if here else _enter(index, stream)
@@ -1070,9 +1075,7 @@ def load_kvcache_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables, c
         if key_out is None:
             ks = vs = hkv * d
             key_out = torch.empty((num_rows, hkv, d), dtype=_BF16, device=k_cache.device)
-            value_out = torch.empty_like(key_out)
-        else:
-            ks, vs = _row_stride(key_out), _row_stride(value_out)
+            value_out = torch.empty((num_rows, hkv, d), dtype=_BF16, device=k_cache.device)
         _check(lib.pkv_load_kvcache_fp8_block(
             key_out.data_ptr(), value_out.data_ptr(), ks, vs, k_cache.data_ptr(),
             v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
