@@ -25,8 +25,8 @@
 // every warp loads its rows straight into the registers that the MMAs take them
 // from (decode_direct_kernel). Its pieces of 128 or 256 bytes, read at eight different
 // times, DRAM served at 0.45 of its rate; asked for in L2 together, a tile ahead, at
-// 0.6 to 0.7. 512 sequences (fp8, 0.59 M tokens): 206 us at block 16, 315 at block 6;
-// behind a window of 1024 (bf16) 248 and 345. At 0.89 and 0.97 of the copy rate, merge
+// 0.6 to 0.7. 512 sequences (fp8, 0.59 M tokens): 201 us at block 16, 315 at block 6;
+// behind a window of 1024 (bf16) 242 and 345. At 0.91 and 0.99 of the copy rate, merge
 // included, the rings are bound by HBM; 3 sequences take 13 us, two launches of
 // dependent loads, and 17 with direct loads.
 //
@@ -932,6 +932,18 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode_warp_combine_kernel
   const int vh = qh / p.group * p.chunks + in_group / p.per_chunk, h = in_group % p.per_chunk;
   auto record = [&](int r) { return (static_cast<int64_t>(2 * r + (r == r0 ? 1 : 0)) * vheads + vh) * p.per_chunk + h; };
   const int n = row ? r1 - r0 + 1 : 0;
+  // records base + (k + 0 .. 7) * share; the first ones are on their way while their
+  // factors are worked out
+  float4 x[8];
+  auto fetch = [&](int base, int k) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = base + (k + u) * share;
+      x[u] = i < n ? *(reinterpret_cast<const float4 *>(p.po + record(r0 + i) * kHD) + lane)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  fetch(part, 0);
   float top = -INFINITY, topw = -INFINITY, sum = 0.f;
   for (int i = lane; i < n; i += 32) {
     const float4 v = p.ml[record(r0 + i)];
@@ -956,12 +968,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode_warp_combine_kernel
     }
     const int left = min(32, (n - base + share - 1) / share);
     for (int k = 0; k < left; k += 8) {
-      float4 x[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        x[u] = k + u < left
-                   ? *(reinterpret_cast<const float4 *>(p.po + record(r0 + base + (k + u) * share) * kHD) + lane)
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (base != part || k > 0) fetch(base, k);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const float y = __shfl_sync(0xffffffffu, f, k + u);
