@@ -186,21 +186,30 @@ struct Heads {
     return kFp8 ? 32 * kp + 8 * i : 64 * (i >> 1) + 16 * kp + 8 * (i & 1);
   }
 
-  // q: the first of `heads` rows.
-  __device__ __forceinline__ void start(const __nv_bfloat16 *q, int heads, float scale_log2) {
+  // The lane's parts of `heads` query rows, the first one at q.
+  static __device__ __forceinline__ void load_q(const __nv_bfloat16 *q, int heads, uint4 (&raw)[NT][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, kp = lane & 3;
 #pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int h = nt * 8 + g;
+        raw[nt][i] = h < heads ? __ldg(reinterpret_cast<const uint4 *>(q + h * kHD + q_dim(i, kp))) : make_uint4(0, 0, 0, 0);
+      }
+  }
+
+  // A sequence begins, with what load_q has read.
+  __device__ __forceinline__ void start(const uint4 (&raw)[NT][4], float scale_log2) {
+    const int kp = threadIdx.x & 3;
+#pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int h = nt * 8 + g;
       uint32_t w[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (h < heads) x = __ldg(reinterpret_cast<const uint4 *>(q + h * kHD + q_dim(i, kp)));
-        w[4 * i] = x.x;
-        w[4 * i + 1] = x.y;
-        w[4 * i + 2] = x.z;
-        w[4 * i + 3] = x.w;
+        w[4 * i] = raw[nt][i].x;
+        w[4 * i + 1] = raw[nt][i].y;
+        w[4 * i + 2] = raw[nt][i].z;
+        w[4 * i + 3] = raw[nt][i].w;
       }
       if constexpr (kFp8) {
         // f16 has three bits more than bf16 but a small range: the head's row is
@@ -657,7 +666,9 @@ decode_direct_kernel(const WarpParams p) {
     ask(next_row);
     look_up(walk.t0 + 2, id, off);
     const int64_t out_row = static_cast<int64_t>(walk.seq) * p.num_q_heads + kvh * p.group + head0;
-    x.start(p.q + out_row * kHD, heads, p.scale_log2);
+    uint4 raw[NT][4];
+    x.load_q(p.q + out_row * kHD, heads, raw);
+    x.start(raw, p.scale_log2);
 #pragma unroll 1
     for (int t = walk.t0; t < t1; ++t) {
       float s[NT][4];
@@ -830,7 +841,8 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     while (ok && walk.next(p, p.unit)) {
       const Seen seen = walk.seen;
       const int64_t out_row = static_cast<int64_t>(walk.seq) * p.num_q_heads + kvh * p.group + head0;
-      x.start(p.q + (real_head ? out_row * kHD : 0), heads, p.scale_log2);
+      uint4 raw[NT][4];
+      x.load_q(p.q + (real_head ? out_row * kHD : 0), heads, raw);
       const int32_t *bt = p.block_tables + static_cast<int64_t>(walk.seq) * p.max_blocks_per_seq;
       // fp8: scales of 8 tiles at a time, lane = (8 tokens, K or V): ids a batch ahead
       float sc = 0.f, next_sc = 0.f;
@@ -851,6 +863,7 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if (walk.t0 + 8 < walk.t1) next_sc = scale_of(walk.t0 + 8);
         if (lane & 1) sc = lg2(sc);
       }
+      x.start(raw, p.scale_log2);
 #pragma unroll 1
       for (int t = walk.t0; t < walk.t1; ++t) {
         if (!warp_wait(full(s), phase, abort)) {
