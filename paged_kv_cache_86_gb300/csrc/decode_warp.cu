@@ -42,6 +42,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "cut_entries.h"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_tc.cuh"
@@ -935,7 +936,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode_warp_combine_kernel
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 cut = p.cuts[blockIdx.x];
   const int seq = cut.x, r0 = cut.y, r1 = cut.z;
-  if (seq < 0 || r0 == r1) return;   // the whole CTA
+  if (!merges_entry(seq, r0, r1, blockIdx.x, p.cuts_by_seq, p.num_seqs, p.ranges)) return;   // the whole CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = warp % share;
   const int qh = blockIdx.y * (kCombineWarps / share) + warp / share;
