@@ -395,6 +395,12 @@ pkv_status pkv_paged_decode_static_ws(void *out, const void *q,
  *   loaded as TMA boxes, others are gathered row by row); num_seqs and
  *   ceil(max_seqlen_q / 128) at most 65535. Unsupported shapes return
  *   PKV_ERR_SHAPE.
+ *   Values have to be finite, also those that a row does not see: where 8 divides
+ *   block_size, the rows of v_cache behind a sequence's last key in its last block
+ *   are read and multiplied by 0 (of k_cache those rows may hold anything), and so are
+ *   a chunk's later rows for its earlier ones. Clear a new pool, or use
+ *   pkv_paged_prefill_window, which takes any values. The chunks of pkv_mixed_step
+ *   are the same in this.
  */
 size_t pkv_prefill_workspace_size(int32_t num_seqs, int32_t total_q,
                                   int32_t num_q_heads, int32_t head_dim);
@@ -457,7 +463,9 @@ pkv_status pkv_store_kvcache_fp8_block(const void *key, const void *value,
  * value_out (rounded to nearest even; exact for the scales that the store
  * writes, down to 2^-120). Other rows are left as they were. With row_starts
  * at multiples of a block size the outputs are a bf16 block pool in which
- * sequence i owns consecutive blocks, which pkv_paged_prefill reads.
+ * sequence i owns consecutive blocks, which pkv_paged_prefill_window reads as
+ * it is; pkv_paged_prefill and pkv_mixed_step want the rows behind each
+ * sequence's last one finite (see there), which this call does not write.
  *   key_out, value_out  num_rows rows of num_kv_heads * 128 values, token
  *                       strides in elements as for pkv_store_kvcache.
  *   row_starts          [num_seqs] int32, non-decreasing, each sequence's rows

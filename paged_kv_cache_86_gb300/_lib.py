@@ -487,7 +487,9 @@ def prefill_workspace_size(num_seqs: int, total_q: int, num_q_heads: int,
 def paged_prefill(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_tables, scale: float,
                   max_seqlen_q: int, max_seqlen_k: int, causal: bool = True, out=None,
                   workspace=None, stream=None) -> torch.Tensor:
-    """Varlen chunked-prefill attention; returns out [total_q, Hq, D] bf16."""
+    """Varlen chunked-prefill attention; returns out [total_q, Hq, D] bf16. Every value of the
+    blocks it reads has to be finite, rows behind a sequence's last key among them
+    (paged_prefill_window takes any)."""
     named = ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (cu_seqlens_q, "cu_seqlens_q"),
              (cu_seqlens_k, "cu_seqlens_k"), (block_tables, "block_tables"))
     _need(q, "q", torch.bfloat16, 3, contiguous=True, on_gpu=False)
@@ -1022,7 +1024,9 @@ def load_kvcache_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables, c
     of sequence i goes to row row_starts[i] + p (int32 [S], non-decreasing, rows of one
     sequence ending before the next one's start). Returns (key, value) [num_rows, Hkv, 128];
     rows that no sequence has are left as they were. key_out / value_out may be given (token
-    rows may be strided); a bf16 block pool [NB, bs, Hkv, 128] viewed as rows is one."""
+    rows may be strided); a bf16 block pool [NB, bs, Hkv, 128] viewed as rows is one.
+    paged_prefill_window reads such a pool as it is; for paged_prefill and mixed_step the rows
+    of value_out behind each sequence's last one have to be finite, so clear a new one first."""
     if (key_out is None) != (value_out is None):
         raise ValueError("key_out and value_out go together")
     if key_out is None and (num_rows is None or num_rows < 0):
