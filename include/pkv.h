@@ -471,8 +471,10 @@ pkv_status pkv_store_kvcache_fp8_block(const void *key, const void *value,
  *   row_starts          [num_seqs] int32, non-decreasing, each sequence's rows
  *                       ending at or before the next one's start; rows from
  *                       num_rows on are not written.
- * A bad block id (PKV_DEVERR_BLOCK_ID) or a length outside
- * [0, max_blocks_per_seq * block_size] (PKV_DEVERR_LENGTH) leaves its rows.
+ * A block id outside [0, num_blocks) leaves the rows of its block
+ * (PKV_DEVERR_BLOCK_ID, if the call has any); a length outside
+ * [0, max_blocks_per_seq * block_size] leaves all rows of its sequence
+ * (PKV_DEVERR_LENGTH, whichever of them the call has).
  */
 pkv_status pkv_load_kvcache_fp8_block(void *key_out, void *value_out,
                                       int64_t key_token_stride, int64_t value_token_stride,

@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(kThreads) load_fp8_block_kernel(const Fp8Block
   __shared__ int s_id[kLoadRows], s_off[kLoadRows];
   const int bs = a.block_size;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kLoadRows;
+  const int64_t cap = static_cast<int64_t>(a.max_blocks_per_seq) * bs;
   if (threadIdx.x < 32) {
     const int first = last_at_or_before(a.row_starts, a.num_seqs, row0);
     if (threadIdx.x < kLoadRows) {
@@ -237,22 +238,22 @@ __global__ void __launch_bounds__(kThreads) load_fp8_block_kernel(const Fp8Block
       int i = first;
       while (i + 1 < a.num_seqs && __ldg(a.row_starts + i + 1) <= row) ++i;
       const int64_t pos = row - __ldg(a.row_starts + i), ctx = __ldg(a.context_lens + i);
-      const int64_t cap = static_cast<int64_t>(a.max_blocks_per_seq) * bs;
       int id = -1;
-      if (ctx < 0) raise_error(a.err, PKV_DEVERR_LENGTH);
-      if (row < a.num_rows && pos >= 0 && pos < ctx) {
-        if (pos >= cap) {
-          raise_error(a.err, PKV_DEVERR_LENGTH);
-        } else {
-          id = __ldg(a.block_tables + static_cast<int64_t>(i) * a.max_blocks_per_seq + pos / bs);
-          if (id < 0 || id >= a.num_blocks) {
-            raise_error(a.err, PKV_DEVERR_BLOCK_ID);
-            id = -1;
-          }
+      if (row < a.num_rows && pos >= 0 && pos < ctx && ctx <= cap) {
+        id = __ldg(a.block_tables + static_cast<int64_t>(i) * a.max_blocks_per_seq + pos / bs);
+        if (id < 0 || id >= a.num_blocks) {
+          raise_error(a.err, PKV_DEVERR_BLOCK_ID);
+          id = -1;
         }
       }
       s_id[threadIdx.x] = id;
       s_off[threadIdx.x] = static_cast<int>(pos % bs);
+    }
+  } else if (blockIdx.x == 0) {
+    // every length once, whichever rows the call has of its sequence
+    for (int i = threadIdx.x - 32; i < a.num_seqs; i += kThreads - 32) {
+      const int ctx = __ldg(a.context_lens + i);
+      if (ctx < 0 || ctx > cap) raise_error(a.err, PKV_DEVERR_LENGTH);
     }
   }
   __syncthreads();
