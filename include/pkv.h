@@ -490,7 +490,9 @@ pkv_status pkv_load_kvcache_fp8_block(void *key_out, void *value_out,
  * Attention that leaves old tokens out: a query at position t sees the keys
  * p <= t with p < sinks (the first tokens stay visible) or p > t - window (so
  * window 1 is the token itself; sinks 0 a plain window). window >= 1, sinks >= 0,
- * both may pass the context. Blocks whose tokens are not seen are not read,
+ * both may pass the context. A seen token of a block with a bad id
+ * (PKV_DEVERR_BLOCK_ID) counts as a zero key and value, in the three calls below.
+ * Blocks whose tokens are not seen are not read,
  * except, in the prefill, the rest of a box of up to 32 rows at an edge.
  *
  * pkv_paged_decode_window: pkv_paged_decode over the seen tokens of sequence i,

@@ -617,14 +617,15 @@ decode_direct_kernel(const WarpParams p) {
       }
     };
     // cache row of the lane's token (-1: none, or one between the sinks and the
-    // window); its scale, of K in the lower half of the warp and of V in the upper
+    // window; -2: of a bad block, a zero key and value as in the rings); its scale, of K
+    // in the lower half of the warp and of V in the upper
     auto resolve = [&](int t, int id, int off, int &row, float &scale) {
       const int j = t * kTok + (lane & 15);
       const int at = j + (j >= seen.front ? seen.gap : 0);
       const bool real = t < t1 && j < seen.units && (at < p.sinks || at >= seen.first);
       const bool good = real && id >= 0 && id < p.num_blocks;
       if (real && !good && lane < 16) raise_error(p.err, PKV_DEVERR_BLOCK_ID);
-      row = good ? id * static_cast<int>(p.bs.d) + off : -1;
+      row = good ? id * static_cast<int>(p.bs.d) + off : real ? -2 : -1;
       scale = 0.f;
       if constexpr (kFp8)
         if (good) scale = __ldg((lane < 16 ? p.k_scales : p.v_scales) + static_cast<int64_t>(id) * p.num_kv_heads + kvh);
@@ -674,7 +675,7 @@ decode_direct_kernel(const WarpParams p) {
     for (int t = walk.t0; t < t1; ++t) {
       float s[NT][4];
       x.scores(kr, s);
-      const bool real0 = __shfl_sync(0xffffffffu, row, g) >= 0, real1 = __shfl_sync(0xffffffffu, row, g + 8) >= 0;
+      const bool real0 = __shfl_sync(0xffffffffu, row, g) != -1, real1 = __shfl_sync(0xffffffffu, row, g + 8) != -1;
       float ks0 = 1.f, ks1 = 1.f, vs0 = 0.f, vs1 = 0.f;
       if constexpr (kFp8) {
         ks0 = __shfl_sync(0xffffffffu, scale, g);

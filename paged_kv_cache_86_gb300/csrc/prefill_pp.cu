@@ -179,8 +179,9 @@ struct SeenKeys {
 
 // One row by plain arithmetic, for the rows whose sums came out not finite: in the
 // tiles a key that the row does not see has weight 0, and 0 times an infinite or
-// NaN value is NaN. Here such keys are never touched. The whole warp works on the
-// row: a lane a key for the scores, four dims a lane for the output.
+// NaN value is NaN. Here such keys are never touched. A key of a bad block is a zero key
+// and value, as in the tiles. The whole warp works on the row: a lane a key for the
+// scores, four dims a lane for the output.
 __device__ __noinline__ void recompute_row(const PPParams &p, int seq, int qh, int64_t row, SeenKeys seen) {
   const int lane = threadIdx.x & 31;
   const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (row * p.num_q_heads + qh) * kHD);
@@ -199,7 +200,7 @@ __device__ __noinline__ void recompute_row(const PPParams &p, int seq, int qh, i
       if (blk >= 0 && blk < p.num_blocks)
         at = (static_cast<int64_t>(blk) * p.block_size + key % p.block_size) * p.num_kv_heads + qh / p.group;
     }
-    float s = -INFINITY;
+    float s = j < count ? 0.f : -INFINITY;
     if (at >= 0) {
       const uint4 *k = reinterpret_cast<const uint4 *>(p.k_cache + at * (kHD * 2));
       float2 acc = make_float2(0.f, 0.f);
