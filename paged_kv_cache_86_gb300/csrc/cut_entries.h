@@ -20,4 +20,11 @@ PKV_HOST_DEVICE bool merges_entry(int seq, int first, int last, int at, bool by_
   return seq >= 0 && seq < num_seqs && (!by_seq || seq == at) && first >= 0 && first < last && last < ranges;
 }
 
+// Tiles of a range: the line's `total`, below 2^31, over `ranges` of them rounded up, and at
+// least `least`. (total + ranges - 1 may be past 2^31.)
+PKV_HOST_DEVICE int range_length(int total, int ranges, int least) {
+  const int n = total / ranges + (total % ranges > 0 ? 1 : 0);
+  return n > least ? n : least;
+}
+
 }  // namespace pkv

@@ -498,7 +498,7 @@ __device__ __forceinline__ Plan plan_ranges(const WarpParams &p, int unit, int w
     if (w < warp) before += part[w];
     total += part[w];
   }
-  const int range_len = max((total + p.ranges - 1) / p.ranges, kMinTiles);
+  const int range_len = range_length(total, p.ranges, kMinTiles);
   int at = before;
   for (int i = lo; i < hi; ++i) {
     const int end = at + cost_of(seen_of(p, i, unit, false), unit);

@@ -1,5 +1,5 @@
 """The arithmetic of the decode by independent warps that compiles for the host as well
-(csrc/cut_entries.h): which entries its merge follows."""
+(csrc/cut_entries.h): which entries its merge follows, and the length of a range."""
 import ctypes
 import itertools
 import os
@@ -14,6 +14,7 @@ SHIM = """
 extern "C" int merges_entry(int seq, int first, int last, int at, int by_seq, int num_seqs, int ranges) {
   return pkv::merges_entry(seq, first, last, at, by_seq != 0, num_seqs, ranges);
 }
+extern "C" int range_length(int total, int ranges, int least) { return pkv::range_length(total, ranges, least); }
 """
 LARGE = (1 << 31) - 1
 
@@ -58,3 +59,13 @@ def test_the_merge_asks(lib):
     text = open(os.path.join(CSRC, "decode_warp.cu")).read()
     body = text[text.index("decode_warp_combine_kernel"):]
     assert "if (!merges_entry(seq, r0, r1, " in body[:body.index("p.ml[")]
+
+
+@pytest.mark.parametrize("ranges", [1, 2, 7, 152, 304, 1216, 65535])
+def test_ranges_hold_the_whole_line(lib, ranges):
+    """Up to the longest line that a call may have (16 sequences of 2^31 - 512 tokens are 2^31 - 480 tiles)."""
+    for total in [0, 1, 3, 4, 5, 100, ranges, 4 * ranges, 4 * ranges + 1, 10**6, LARGE - ranges, LARGE - ranges + 1,
+                  LARGE - 479, LARGE]:
+        n = lib.range_length(total, ranges, 4)
+        assert n * ranges >= total and n >= 4
+        assert n == 4 or (n - 1) * ranges < total
