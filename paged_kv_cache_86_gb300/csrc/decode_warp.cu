@@ -68,6 +68,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // by 2^kLift, between 2^-24 and 2^15.
 constexpr float kGrow = 8.f;
 constexpr float kLift = 7.f;
+constexpr float kDrop = 1.f / 128.f;       // 2^-kLift
 
 // n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, "Division by
 // Invariant Integers using Multiplication")
@@ -122,6 +123,14 @@ __device__ __forceinline__ uint32_t div_of(uint32_t n, const FastDiv &f) {
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// With results below 2^-126: the values' scales go down to 2^-120, and a kept maximum
+// may be off by 2^8.
+__device__ __forceinline__ float ex2_far(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -295,8 +304,10 @@ struct Heads {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float x = s[nt][e] * qmul[nt][e & 1];
-        if constexpr (kFp8) x *= e < 2 ? ks0 : ks1;
+        // (fp8: the factors first: a score of 2^130 that a scale of 2^-120 takes back must not
+        // be infinite in between. Rounded to zero, their product is finite: 0 times it is 0.)
+        float x = s[nt][e];
+        x *= kFp8 ? __fmul_rz(qmul[nt][e & 1], e < 2 ? ks0 : ks1) : qmul[nt][e & 1];
         x = (e < 2 ? real0 : real1) ? x : -INFINITY;
         s[nt][e] = x;
         grow |= x > m[nt][e & 1] + kGrow;
@@ -416,7 +427,10 @@ struct Heads {
         const int dim0 = kFp8 ? 16 * g : 8 * g, dim1 = kFp8 ? dim0 + 8 : dim0 + 64;
         if (whole) {
           float f = 1.f / sum, fw = 1.f;            // 0 / 0: every seen score is -inf
-          if constexpr (kFp8) fw = ex2(mw[nt][e] == -INFINITY ? 0.f : mw[nt][e] - m[nt][e] - kLift);
+          if constexpr (kFp8) {
+            f *= kDrop;
+            fw = ex2_far(mw[nt][e] == -INFINITY ? 0.f : mw[nt][e] - m[nt][e]);
+          }
           uint32_t w[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) w[i] = float2_to_bf16x2(v[2 * i] * f * fw, v[2 * i + 1] * f * fw);
@@ -930,8 +944,8 @@ decode_ring_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 // --------------------------------------------------------------- combine --
 
 // `share` warps per (entry of cuts, query head) merge the records of a cut sequence:
-// out = sum O_i 2^(M_i - M*) / sum l_i 2^(m_i - m*) * 2^(M* - m* - lift)
-__global__ void __launch_bounds__(kCombineWarps * 32) decode_warp_combine_kernel(const WarpParams p, int share, float lift) {
+// out = sum O_i 2^(M_i - M*) / sum l_i 2^(m_i - m*) * drop * 2^(M* - m*)
+__global__ void __launch_bounds__(kCombineWarps * 32) decode_warp_combine_kernel(const WarpParams p, int share, float drop) {
   __shared__ float4 s_acc[kCombineWarps][32];
   __shared__ float s_sum[kCombineWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1010,7 +1024,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) decode_warp_combine_kernel
     }
   }
   if (!row) return;
-  const float f = 1.f / sum, fw = ex2(refw - ref - lift);
+  const float f = 1.f / sum * drop, fw = ex2_far(refw - ref);
   reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(seq) * p.num_q_heads + qh) * kHD)[lane] =
       make_uint2(float2_to_bf16x2(acc.x * f * fw, acc.y * f * fw), float2_to_bf16x2(acc.z * f * fw, acc.w * f * fw));
 }
@@ -1218,7 +1232,7 @@ cudaError_t launch_decode_warp(const DecodeWarpArgs &a, cudaStream_t stream) {
   while (share < kCombineWarps && share * 8 * static_cast<int64_t>(a.num_seqs) < s.ranges) share *= 2;
   const int rows = kCombineWarps / share;
   return launch_dependent(stream, dim3(p.cuts_by_seq ? a.num_seqs : s.ranges, (a.num_q_heads + rows - 1) / rows), kCombineWarps * 32, 0,
-                          decode_warp_combine_kernel, p, share, fp8 ? kLift : 0.f);
+                          decode_warp_combine_kernel, p, share, fp8 ? kDrop : 1.f);
 }
 
 }  // namespace pkv
