@@ -528,6 +528,7 @@ def paged_prefill(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_tables,
 
 _BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 _MAX_I32 = 0x7fffffff   # windows and sinks beyond it see the same: no context is longer
+_MAX_TOKENS = _MAX_I32 - 512   # longest context of the windowed calls
 # the current stream's handle without building a Stream object (2 us of a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -941,6 +942,11 @@ def tree_decode(q, key, value, k_cache, v_cache, block_tables, context_lens, cu_
     return out
 
 
+def _clip(n: int) -> int:
+    """n as a C int that means the same: ctypes keeps the low 32 bits of a larger one."""
+    return n if 0 <= n <= _MAX_I32 else -1 if n < 0 else _MAX_I32
+
+
 # The calls below check everything in one expression; where it does not hold, their
 # _refuse says what is wrong. Where the tensors' GPU is current and no stream is named, they
 # launch without _enter: a call on a few sequences is bound by the host.
@@ -1155,8 +1161,9 @@ def paged_decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables
         status = lib.pkv_paged_decode_fp8_block(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), mb,
-            context_lens.data_ptr(), s, mb * bs if max_context_len is None else max_context_len,
-            window if window < _MAX_I32 else _MAX_I32, sinks if sinks < _MAX_I32 else _MAX_I32,
+            context_lens.data_ptr(), s,
+            min(mb * bs, _MAX_TOKENS) if max_context_len is None else _clip(max_context_len),
+            _clip(window), _clip(sinks),
             hq, hkv, d, bs, nb, scale, workspace.data_ptr(), workspace.nbytes, st)
         if status != 0:
             raise PkvError(status, "pkv_paged_decode_fp8_block")
@@ -1207,8 +1214,8 @@ def paged_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale: 
         status = lib.pkv_paged_decode_window(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_tables.data_ptr(), mb, context_lens.data_ptr(), s,
-            mb * bs if max_context_len is None else max_context_len,
-            window if window < _MAX_I32 else _MAX_I32, sinks if sinks < _MAX_I32 else _MAX_I32,
+            min(mb * bs, _MAX_TOKENS) if max_context_len is None else _clip(max_context_len),
+            _clip(window), _clip(sinks),
             hq, hkv, d, bs, nb, scale, workspace.data_ptr(), workspace.nbytes, PKV_BF16, st)
         if status != 0:
             raise PkvError(status, "pkv_paged_decode_window")
@@ -1260,9 +1267,9 @@ def paged_prefill_window(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_
             _need_workspace(workspace, q)
         status = lib.pkv_paged_prefill_window(
             out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), max_seqlen_q, max_seqlen_k,
-            block_tables.data_ptr(), mb, s, total, window if window < _MAX_I32 else _MAX_I32,
-            sinks if sinks < _MAX_I32 else _MAX_I32, hq, hkv, d, bs, nb, scale,
+            cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), _clip(max_seqlen_q),
+            _clip(max_seqlen_k), block_tables.data_ptr(), mb, s, total, _clip(window),
+            _clip(sinks), hq, hkv, d, bs, nb, scale,
             workspace.data_ptr(), workspace.nbytes, PKV_BF16, st)
         if status != 0:
             raise PkvError(status, "pkv_paged_prefill_window")
