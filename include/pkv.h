@@ -492,8 +492,9 @@ pkv_status pkv_load_kvcache_fp8_block(void *key_out, void *value_out,
  * window 1 is the token itself; sinks 0 a plain window). window >= 1, sinks >= 0,
  * both may pass the context. A seen token of a block with a bad id
  * (PKV_DEVERR_BLOCK_ID) counts as a zero key and value, in the three calls below.
- * Blocks whose tokens are not seen are not read,
- * except, in the prefill, the rest of a box of up to 32 rows at an edge.
+ * What is read is the seen tokens, and where 8 divides block_size the rest of the
+ * boxes that they lie in (decode: 8 or 16 tokens, prefill: up to 64), so blocks in which
+ * no box is seen may be given back or hold anything.
  *
  * pkv_paged_decode_window: pkv_paged_decode over the seen tokens of sequence i,
  * whose query is at position context_lens[i] - 1.
@@ -504,9 +505,10 @@ pkv_status pkv_load_kvcache_fp8_block(void *key_out, void *value_out,
  *   > 0; max_context_len and num_blocks * block_size at most 2^31 - 512; out
  *   and q must not overlap;
  *   workspace of pkv_decode_window_workspace_size bytes.
- *   A token that is not seen, and a row behind the last token, is never touched,
- *   whatever it holds. A seen key or value that is not finite counts as it does
- *   in the formula. A row whose seen scores are all -inf is NaN.
+ *   A token that is not seen, and a row behind the last token, never changes a
+ *   result, whatever it holds; beside a seen token, in its box, it may be read.
+ *   A seen key or value that is not finite counts as it does in the formula. A row
+ *   whose seen scores are all -inf is NaN.
  *   The weights are rounded to bf16 (bf16 cache; the softmax's sum is of the
  *   rounded ones) or f16 (fp8 cache) before they multiply V; all sums are fp32.
  *

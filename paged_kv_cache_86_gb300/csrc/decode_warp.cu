@@ -25,8 +25,8 @@
 // every warp loads its rows straight into the registers that the MMAs take them
 // from (decode_direct_kernel). Its pieces of 128 or 256 bytes, read at eight different
 // times, DRAM served at 0.45 of its rate; asked for in L2 together, a tile ahead, at
-// 0.6 to 0.7. 512 sequences (fp8, 0.59 M tokens): 201 us at block 16, 315 at block 6;
-// behind a window of 1024 (bf16) 242 and 345. At 0.91 and 0.99 of the copy rate, merge
+// 0.6 to 0.7. 512 sequences (fp8, 0.59 M tokens): 202 us at block 16, 311 at block 6;
+// behind a window of 1024 (bf16) 242-246 and 338. At 0.91 and 0.98 of the copy rate, merge
 // included, the rings are bound by HBM; 3 sequences take 13 us, two launches of
 // dependent loads, and 17 with direct loads.
 //
